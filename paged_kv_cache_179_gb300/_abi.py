@@ -1,4 +1,5 @@
-"""Thin ctypes binding of libpa (include/pa.h): argument marshalling only.
+"""Thin ctypes binding of libpa (include/pa.h, include/pa_serving.h): argument
+marshalling only.
 
 Every function takes torch tensors, checks that they are CUDA, contiguous and
 of the expected dtype and shape, passes their device pointers and the current
@@ -12,6 +13,7 @@ import ctypes
 import os
 import threading
 
+import numpy as np
 import torch
 
 from . import build as _build
@@ -23,6 +25,8 @@ PA_NOALLOC_SCRATCH_BYTES = 16 << 20
 PA_STATUS_BAD_BLOCK, PA_STATUS_BAD_LEN, PA_STATUS_BAD_SLOT, PA_STATUS_TIMEOUT = 1, 2, 4, 8
 PA_STATUS_NO_WORKSPACE = 16
 PA_STATUS_WS_DIRTY = 32
+PA_F32 = 3
+PA_STATUS_BAD_TOKEN = 64
 PA_DECODE_EARLY_PROLOGUE = 1
 PA_DECODE_EARLY_COPIES = 2
 
@@ -71,6 +75,26 @@ SIGNATURES = {
     "pa_test_merge_timeout": ([_vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _sz,
                                ctypes.c_uint64, _vp], _i32),
 }
+# the entry points of include/pa_serving.h
+SERVING_SIGNATURES = {
+    "pa_rope": ([_vp, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp], _i32),
+    "pa_rope_append": ([_vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i32, _i32,
+                        _i32, _i32, _i32, _i32, _i32, _vp], _i32),
+    "pa_rope_append_fp8": ([_vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                            _i32, _i32, _i32, _i32, _i32, _i32, _i32, _vp], _i32),
+    "pa_attention_weights_workspace_size": ([_i32, _i32, _i32, _i32, _i32], _sz),
+    "pa_attention_weights": ([_vp, _i64, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32,
+                              _i32, _i32, _f32, _f32, _i32, _i32, _i32, _vp, _sz, _vp], _i32),
+    "pa_attention_weights_fp8": ([_vp, _i64, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32,
+                                  _i32, _i32, _i32, _f32, _f32, _i32, _i32, _i32, _vp, _sz, _vp],
+                                 _i32),
+    "pa_evict": ([_vp, _vp, _vp, _i64, _vp, _i64, _vp, _i32, _vp, _i32, _vp, _i32, _vp, _vp, _vp,
+                  _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _vp], _i32),
+    "pa_evict_fp8": ([_vp, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _i32, _vp, _i32, _vp, _i32,
+                      _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _vp], _i32),
+    "pa_verify_drafts": ([_vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i32, _i32, _i32, _i32,
+                          _vp], _i32),
+}
 
 _lock = threading.Lock()
 _lib = None
@@ -97,7 +121,7 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
                                        "or python -m paged_kv_cache_179_gb300.build")
                 _build.build()
             L = ctypes.CDLL(_build.LIB)
-            for name, (args, res) in SIGNATURES.items():
+            for name, (args, res) in (*SIGNATURES.items(), *SERVING_SIGNATURES.items()):
                 fn = getattr(L, name)
                 fn.argtypes = args
                 fn.restype = res
@@ -572,3 +596,315 @@ def pa_get_status(device=None) -> tuple[int, int]:
     bits = ctypes.c_uint(0)
     rc = load().pa_get_status(_stream(device or torch.cuda.current_device()), ctypes.byref(bits))
     return rc, bits.value
+
+
+# ------------------------------------------- around the decode step (pa_serving.h)
+def _here(dev):
+    """The tensors of a call must be on the current device (its streams and kernels are)."""
+    if dev.type == "cuda" and dev.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {dev}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
+def _rows(t, name, dtype, device):
+    """Checks a [T][H][D] tensor whose tokens may lie apart (a view of a wider
+    projection) but whose heads are dense; returns the elements from one token
+    to the next."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have 3 dims, has {t.dim()}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    T, H, D = t.shape
+    if t.numel() and ((D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D)):
+        raise ValueError(f"{name}: each token's heads must be contiguous")
+    return t.stride(0) if T > 1 else H * D
+
+
+class _RopeStruct(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("freq_axis", ctypes.c_void_p),
+                ("num_axes", ctypes.c_int), ("rotary_dim", ctypes.c_int),
+                ("adjacent", ctypes.c_int), ("amplitude", ctypes.c_float)]
+
+
+class RopeSpec:
+    """A rotation (pa_rope_spec): ``inv_freq[i]`` radians per position of pair
+    i, ``freq_axis[i]`` the axis of the positions it turns with (None: one
+    axis), pairs (i, i + rotary_dim / 2) or, ``adjacent``, (2i, 2i + 1);
+    rotary_dim is twice the number of frequencies.  Made once and kept."""
+
+    def __init__(self, inv_freq, freq_axis=None, *, adjacent=False, amplitude=1.0, num_axes=None):
+        self.inv_freq = np.ascontiguousarray(inv_freq, dtype=np.float64).reshape(-1).copy()
+        self.freq_axis = None if freq_axis is None else \
+            np.ascontiguousarray(freq_axis, dtype=np.int32).reshape(-1).copy()
+        if self.freq_axis is not None and self.freq_axis.shape != self.inv_freq.shape:
+            raise ValueError("freq_axis and inv_freq must have one entry per pair")
+        if num_axes is None:
+            num_axes = 1 if freq_axis is None or not self.freq_axis.size \
+                else int(self.freq_axis.max()) + 1
+        self.num_axes, self.rotary_dim = int(num_axes), 2 * self.inv_freq.size
+        self.struct = _RopeStruct(self.inv_freq.ctypes.data,
+                                  None if self.freq_axis is None else self.freq_axis.ctypes.data,
+                                  self.num_axes, self.rotary_dim, int(bool(adjacent)),
+                                  float(amplitude))
+        self.pointer = ctypes.c_void_p(ctypes.addressof(self.struct))
+        self.pointer.owner = self      # a recorded call keeps the specification alive
+
+
+def _positions(positions, spec, T, dev):
+    if not isinstance(spec, RopeSpec):
+        raise TypeError("spec must be a RopeSpec")
+    _need(positions, "positions", torch.int32, None, dev)
+    if tuple(positions.shape) not in ((spec.num_axes, T),) + (((T,),) if spec.num_axes == 1 else ()):
+        raise ValueError(f"positions must be [{spec.num_axes}][{T}]")
+
+
+def pa_rope(q_out, q, k_out, k, positions, spec: RopeSpec) -> None:
+    """Rotate q [T][Hq][D] into q_out and k [T][Hkv][D] into k_out (either pair
+    may be None) by positions int32 [axes][T]; q and k may be views of one
+    projection, or the outputs themselves (in place)."""
+    ref = q if q is not None else k
+    if ref is None:
+        raise ValueError("q or k must be given")
+    dev = ref.device
+    act = (torch.float16, torch.bfloat16)
+    strides, heads = [0, 0], [0, 0]
+    for i, (o, t, n) in enumerate(((q_out, q, "q"), (k_out, k, "k"))):
+        if (o is None) != (t is None):
+            raise ValueError(f"{n} and {n}_out go together")
+        if t is None:
+            continue
+        strides[i] = _rows(t, n, act if t is ref else ref.dtype, dev)
+        _need(o, n + "_out", ref.dtype, 3, dev)
+        if o.shape != t.shape or t.shape[0] != ref.shape[0] or t.shape[2] != ref.shape[2]:
+            raise ValueError("shape mismatch")
+        heads[i] = t.shape[1]
+    T, _, D = ref.shape
+    _positions(positions, spec, T, dev)
+    _here(dev)
+    _call(load().pa_rope, "pa_rope", _ptr(q_out), _ptr(q), strides[0], _ptr(k_out), _ptr(k),
+          strides[1], _ptr(positions), spec.pointer, T, heads[0], heads[1], D,
+          _act_code(ref.dtype), _stream(dev))
+
+
+def _rope_append_args(q_out, q, k_new, v_new, k_cache, v_cache, slot_mapping, positions, spec,
+                      pool_dtype):
+    dev = k_cache.device
+    sq = _rows(q, "q", (torch.float16, torch.bfloat16), dev)
+    sk, sv = _rows(k_new, "k_new", q.dtype, dev), _rows(v_new, "v_new", q.dtype, dev)
+    _need(q_out, "q_out", q.dtype, 3, dev)
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _need(t, n, pool_dtype or q.dtype, 4, dev)
+    _need(slot_mapping, "slot_mapping", torch.int64, 1, dev)
+    T, Hq, D = q.shape
+    NB, Hkv, bs, D2 = k_cache.shape
+    if q_out.shape != q.shape or k_new.shape != (T, Hkv, D) or v_new.shape != k_new.shape \
+            or v_cache.shape != k_cache.shape or D2 != D or slot_mapping.shape[0] != T:
+        raise ValueError("shape mismatch")
+    _positions(positions, spec, T, dev)
+    _here(dev)
+    return (_ptr(q_out), _ptr(q), sq, _ptr(k_new), sk, _ptr(v_new), sv, _ptr(k_cache),
+            _ptr(v_cache)), (_ptr(slot_mapping), _ptr(positions), spec.pointer, T, Hq, Hkv, D, bs,
+                             NB, _act_code(q.dtype), _stream(dev))
+
+
+def pa_rope_append(q_out, q, k_new, v_new, k_cache, v_cache, slot_mapping, positions,
+                   spec: RopeSpec) -> None:
+    """pa_rope then pa_cache_append in one launch: q rotated into q_out, k
+    rotated into k_cache and v copied into v_cache at slot_mapping."""
+    a, b = _rope_append_args(q_out, q, k_new, v_new, k_cache, v_cache, slot_mapping, positions,
+                             spec, None)
+    _call(load().pa_rope_append, "pa_rope_append", *a, *b)
+
+
+def pa_rope_append_fp8(q_out, q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, slot_mapping,
+                       positions, spec: RopeSpec) -> None:
+    """pa_rope then pa_cache_append_fp8 in one launch."""
+    a, b = _rope_append_args(q_out, q, k_new, v_new, k_cache, v_cache, slot_mapping, positions,
+                             spec, torch.uint8)
+    for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        _need(t, n, torch.float32, 2, k_cache.device)
+        if t.shape != k_cache.shape[:2]:
+            raise ValueError("shape mismatch")
+    _call(load().pa_rope_append_fp8, "pa_rope_append_fp8", *a, _ptr(k_scale), _ptr(v_scale), *b)
+
+
+def pa_attention_weights_workspace_size(num_seqs, num_q_heads, num_kv_heads, max_context_len,
+                                        queries_per_seq=1) -> int:
+    return int(load().pa_attention_weights_workspace_size(
+        int(num_seqs), int(num_q_heads), int(num_kv_heads), int(max_context_len),
+        int(queries_per_seq)))
+
+
+def alloc_weights_workspace(num_seqs, num_q_heads, num_kv_heads, max_context_len,
+                            queries_per_seq, device):
+    """Workspace for pa_attention_weights (need not be cleared)."""
+    n = pa_attention_weights_workspace_size(num_seqs, num_q_heads, num_kv_heads, max_context_len,
+                                            queries_per_seq)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def _weights_args(weights, q, k_cache, block_tables, context_lens, pool_dtype, dev):
+    _need(q, "q", (torch.float16, torch.bfloat16), None, dev)
+    _need(weights, "weights", torch.float32, 3, dev)
+    _need(k_cache, "k_cache", pool_dtype or q.dtype, 4, dev)
+    B, nq, Hq, D = _decode_common(q, q, block_tables, context_lens, dev)
+    NB, Hkv, bs, D2 = k_cache.shape
+    if weights.shape[:2] != (B, Hkv) or D2 != D:
+        raise ValueError("shape mismatch")
+    _here(dev)
+    return B, nq, Hq, Hkv, D, bs, NB
+
+
+def pa_attention_weights(weights, q, k_cache, block_tables, context_lens, max_context_len: int,
+                         scale: float, workspace, *, decay: float = 1.0,
+                         fresh_tokens: int = 0) -> None:
+    """weights[b][h][t] = decay * weights + the softmax weights that q's rows
+    give token t (0 in the old one's place for the last fresh_tokens tokens).
+    weights fp32 [B][Hkv][n >= max_context_len]; q [B][Hq][D] or [B][n_q][Hq][D]."""
+    dev = q.device
+    B, nq, Hq, Hkv, D, bs, NB = _weights_args(weights, q, k_cache, block_tables, context_lens,
+                                              None, dev)
+    _call(load().pa_attention_weights, "pa_attention_weights", _ptr(weights), weights.shape[2],
+          _ptr(q), _ptr(k_cache), _ptr(block_tables), block_tables.shape[1], _ptr(context_lens),
+          int(max_context_len), B, Hq, Hkv, D, bs, NB, float(scale), float(decay),
+          int(fresh_tokens), nq, _act_code(q.dtype), _ptr(workspace), _ws_bytes(workspace, dev),
+          _stream(dev))
+
+
+def pa_attention_weights_fp8(weights, q, k_cache, k_scale, block_tables, context_lens,
+                             max_context_len: int, scale: float, workspace, *,
+                             decay: float = 1.0, fresh_tokens: int = 0) -> None:
+    """As pa_attention_weights over an E4M3 pool with [NB][Hkv] scales."""
+    dev = q.device
+    B, nq, Hq, Hkv, D, bs, NB = _weights_args(weights, q, k_cache, block_tables, context_lens,
+                                              torch.uint8, dev)
+    _need(k_scale, "k_scale", torch.float32, 2, dev)
+    if k_scale.shape != (NB, Hkv):
+        raise ValueError("shape mismatch")
+    _call(load().pa_attention_weights_fp8, "pa_attention_weights_fp8", _ptr(weights),
+          weights.shape[2], _ptr(q), _ptr(k_cache), _ptr(k_scale), _ptr(block_tables),
+          block_tables.shape[1], _ptr(context_lens), int(max_context_len), B, Hq, Hkv, D, bs, NB,
+          float(scale), float(decay), int(fresh_tokens), nq, _act_code(q.dtype), _ptr(workspace),
+          _ws_bytes(workspace, dev), _stream(dev))
+
+
+def _evict_args(k_cache, v_cache, weights, weights_out, block_tables, context_lens,
+                max_context_len, spare_tables, tables_out, new_lens, kept, dtype):
+    dev = k_cache.device
+    _need(k_cache, "k_cache", dtype, 4, dev)
+    _need(v_cache, "v_cache", k_cache.dtype, 4, dev)
+    _need(weights, "weights", torch.float32, 3, dev)
+    _need(block_tables, "block_tables", torch.int32, 2, dev)
+    _need(context_lens, "context_lens", torch.int32, 1, dev)
+    _need(spare_tables, "spare_tables", torch.int32, 2, dev)
+    _need(new_lens, "new_lens", torch.int32, 1, dev)
+    _need(kept, "kept", torch.int32, 3, dev)
+    B, (NB, Hkv, bs, D) = block_tables.shape[0], k_cache.shape
+    if v_cache.shape != k_cache.shape or weights.shape[:2] != (B, Hkv) or \
+            kept.shape[:2] != (B, Hkv) or context_lens.shape[0] != B or \
+            spare_tables.shape[0] != B or new_lens.shape[0] != B:
+        raise ValueError("shape mismatch")
+    if weights_out is not None:
+        _need(weights_out, "weights_out", torch.float32, 3, dev)
+        if weights_out.shape[:2] != (B, Hkv):
+            raise ValueError("shape mismatch")
+    if tables_out is not None:
+        _need(tables_out, "tables_out", torch.int32, 2, dev)
+        if tables_out.shape != spare_tables.shape:
+            raise ValueError("shape mismatch")
+    _here(dev)
+    keep = kept.shape[2]
+    return (_ptr(weights), weights.shape[2], _ptr(weights_out),
+            0 if weights_out is None else weights_out.shape[2], _ptr(block_tables),
+            block_tables.shape[1], _ptr(context_lens), int(max_context_len), _ptr(spare_tables),
+            spare_tables.shape[1], _ptr(tables_out), _ptr(new_lens), _ptr(kept), B, Hkv, D, bs,
+            NB, keep)
+
+
+def pa_evict(k_cache, v_cache, weights, weights_out, block_tables, context_lens,
+             max_context_len: int, spare_tables, tables_out, new_lens, kept, *,
+             first_tokens: int = 0, recent_tokens: int = 0) -> None:
+    """Cut each sequence with more than keep = kept.shape[2] tokens to the first
+    first_tokens, the last recent_tokens and the heaviest of the rest, moved
+    into the blocks of spare_tables; weights_out and tables_out may be None."""
+    a = _evict_args(k_cache, v_cache, weights, weights_out, block_tables, context_lens,
+                    max_context_len, spare_tables, tables_out, new_lens, kept,
+                    (torch.float16, torch.bfloat16))
+    _call(load().pa_evict, "pa_evict", _ptr(k_cache), _ptr(v_cache), *a, int(first_tokens),
+          int(recent_tokens), _act_code(k_cache.dtype), _stream(k_cache.device))
+
+
+def pa_evict_fp8(k_cache, v_cache, k_scale, v_scale, weights, weights_out, block_tables,
+                 context_lens, max_context_len: int, spare_tables, tables_out, new_lens, kept, *,
+                 first_tokens: int = 0, recent_tokens: int = 0) -> None:
+    """As pa_evict over E4M3 pools: a page that is written gets the scale of the
+    rows it now holds."""
+    a = _evict_args(k_cache, v_cache, weights, weights_out, block_tables, context_lens,
+                    max_context_len, spare_tables, tables_out, new_lens, kept, torch.uint8)
+    for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        _need(t, n, torch.float32, 2, k_cache.device)
+        if t.shape != k_cache.shape[:2]:
+            raise ValueError("shape mismatch")
+    _call(load().pa_evict_fp8, "pa_evict_fp8", _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+          _ptr(v_scale), *a, int(first_tokens), int(recent_tokens), _stream(k_cache.device))
+
+
+def _prob_rows(t, name, dtype, dev, rows):
+    """Checks [B][rows][V] probabilities whose rows may be padded; the row stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.dim() != 3 or t.shape[1] != rows:
+        raise ValueError(f"{name} must be [num_seqs][{rows}][vocab_size]")
+    B, n, V = t.shape
+    row = t.stride(1) if n > 1 else t.stride(0) if B > 1 else V
+    if t.numel() and ((V > 1 and t.stride(2) != 1) or (B > 1 and t.stride(0) != n * row)):
+        raise ValueError(f"{name}: rows must be contiguous and evenly spaced")
+    return row
+
+
+def pa_verify_drafts(out_tokens, num_accepted, target_probs, draft_probs, draft_tokens, uniforms,
+                     *, num_drafts=None) -> None:
+    """Accept the drafts draft_tokens int32 [B][n] in order while uniforms[b][i]
+    * q_i(x_i) < p_i(x_i), then draw one more token; p = target_probs
+    [B][n + 1][V], q = draft_probs [B][n][V] or None (drafts without
+    probabilities), fp32, fp16 or bf16; uniforms fp32 [B][n + 1].  out_tokens
+    int32 [B][n + 1] (-1 behind the drawn token), num_accepted int32 [B];
+    num_drafts int32 [B]: how many drafts each sequence has (None: all n)."""
+    dev = target_probs.device
+    codes = {torch.float32: PA_F32, torch.float16: PA_F16, torch.bfloat16: PA_BF16}
+    if target_probs.dtype not in codes:
+        raise TypeError(f"unsupported probability dtype {target_probs.dtype}")
+    _need(out_tokens, "out_tokens", torch.int32, 2, dev)
+    _need(num_accepted, "num_accepted", torch.int32, 1, dev)
+    _need(draft_tokens, "draft_tokens", torch.int32, 2, dev)
+    _need(uniforms, "uniforms", torch.float32, 2, dev)
+    B, n = draft_tokens.shape
+    ps = _prob_rows(target_probs, "target_probs", target_probs.dtype, dev, n + 1)
+    V, qs = target_probs.shape[2], 0
+    if draft_probs is not None:
+        qs = _prob_rows(draft_probs, "draft_probs", target_probs.dtype, dev, n)
+        if draft_probs.shape != (B, n, V):
+            raise ValueError("shape mismatch")
+    if num_drafts is not None:
+        _need(num_drafts, "num_drafts", torch.int32, 1, dev)
+        if num_drafts.shape[0] != B:
+            raise ValueError("shape mismatch")
+    if target_probs.shape[0] != B or out_tokens.shape != (B, n + 1) or \
+            uniforms.shape != (B, n + 1) or num_accepted.shape[0] != B:
+        raise ValueError("shape mismatch")
+    _here(dev)
+    _call(load().pa_verify_drafts, "pa_verify_drafts", _ptr(out_tokens), _ptr(num_accepted),
+          _ptr(target_probs), ps, _ptr(draft_probs), qs, _ptr(draft_tokens), _ptr(num_drafts),
+          _ptr(uniforms), B, n, V, codes[target_probs.dtype], _stream(dev))
