@@ -446,6 +446,8 @@ VERIFY = [  # B, n, V, dtype, draft, pad
     (9, 2, 4099, F16, True, 1),
     (3, 8, 32000, torch.float32, False, 0),
     (40, 3, 129, BF16, True, 0),
+    (1, 1, 300001, torch.float32, True, 0),       # a warp's part is narrowed down twice
+    (700, 1, 40, torch.float32, True, 0),         # more sequences than CTAs fit at once
 ]
 
 
