@@ -24,6 +24,7 @@
 // fragments are loaded with the same permutation.
 #include <climits>
 
+#include "pa_e4m3.cuh"
 #include "pa_launch.h"
 #include "pa_ptx.cuh"
 #include "serving_launch.h"
@@ -31,18 +32,25 @@
 namespace pa {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
 constexpr int kPrefix = kWeightsMaxBatch + 1;
+constexpr int kMaxWarps = 12;
+// Warps of a score CTA and CTAs an SM: up to 16 query rows keep 16 warps an SM;
+// the fragments of 32 take 64 registers, which leaves room for 12.
+template <int NT>
+struct Score {
+  static constexpr int kWarps = NT == 4 ? 12 : 8;
+  static constexpr int kCtas = NT == 4 ? 1 : 2;
+};
+constexpr int kFinishWarps = 8;
+constexpr int kFinishThreads = kFinishWarps * 32;
 
 // ------------------------------------------------------------ the line of pages
 struct Line {
   int64_t n;        // pages of all units
   int workers;      // warps that have pages: each has at least one
 };
-__device__ __forceinline__ Line make_line(const WeightsArgs& a, const int* cum) {
+__device__ __forceinline__ Line make_line(const WeightsArgs& a, const int* cum, int warps) {
   const int64_t n = static_cast<int64_t>(cum[a.B]) * a.Hkv;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarps;
   return Line{n, static_cast<int>(n < warps ? n : warps)};
 }
 // The pages worker w takes: [start(w), start(w + 1)).
@@ -64,10 +72,11 @@ __device__ __forceinline__ int checked_len(const WeightsArgs& a, int b, bool rep
 }
 
 // cum[b] = pages of the sequences before b, cum[B] = all; by the whole CTA.
+template <int WARPS>
 __device__ __forceinline__ void prefix_pages(const WeightsArgs& a, int* cum, int* warp_sums) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int carry = 0;
-  for (int base = 0; base < a.B; base += kThreads) {
+  for (int base = 0; base < a.B; base += WARPS * 32) {
     const int b = base + tid;
     const int v = b < a.B ? (checked_len(a, b, blockIdx.x == 0) + 15) / 16 : 0;
     int s = v;
@@ -79,7 +88,7 @@ __device__ __forceinline__ void prefix_pages(const WeightsArgs& a, int* cum, int
     if (lane == 31) warp_sums[warp] = s;
     __syncthreads();
     int before = carry;
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < WARPS; ++w) {
       if (w < warp) before += warp_sums[w];
       carry += warp_sums[w];
     }
@@ -122,38 +131,34 @@ struct Work {
 __device__ __host__ __forceinline__ size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 // ----------------------------------------------------------------- K fragments
-// KV: 0 fp16, 1 bf16, 2 E4M3 with fp16 q, 3 E4M3 with bf16 q
+// KV: 0 fp16, 1 bf16, 2 E4M3 with fp16 q, 3 E4M3 with bf16 q.  E4M3 codes become
+// fp16, exactly; a bf16 row of q then enters the fp16 product scaled by the power
+// of two that brings its largest element into [2^14, 2^15).  Its 8 bits fit
+// fp16's 11, and what falls below fp16's smallest step is 2^-39 of the largest.
 template <int KV>
 struct Kind {
   static constexpr bool kE4m3 = KV >= 2;
-  static constexpr bool kBf16 = KV == 1 || KV == 3;
+  static constexpr bool kBf16 = KV == 1;        // of the product
+  static constexpr bool kScaledQ = KV == 3;
 };
-
-// Two E4M3 codes as two values of the activations' type; exact.
-template <bool BF16>
-__device__ __forceinline__ uint32_t codes2(uint32_t two) {
-  const uint32_t h = e4m3x2_to_f16x2(two);
-  if constexpr (BF16) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-    return pack2<true>(f.x, f.y);
-  } else {
-    return h;
-  }
-}
 
 // The lane's part of one page: NLD 16-byte chunks of row r, then of row r + 8.
 template <int D, int KV>
 struct Page {
   static constexpr int NLD = D / (Kind<KV>::kE4m3 ? 64 : 32);
   uint4 lo[NLD], hi[NLD];
-  __device__ __forceinline__ void load(const void* page, int lane) {
+  float scale;     // of an E4M3 page
+  __device__ __forceinline__ void load(const WeightsArgs& a, int id, int h, int lane) {
     constexpr int row_chunks = NLD * 4;
-    const uint4* p = static_cast<const uint4*>(page) + (lane >> 2) * row_chunks + (lane & 3);
+    const int64_t tile = static_cast<int64_t>(id) * a.Hkv + h;
+    const uint4* p = static_cast<const uint4*>(a.k_cache) + tile * (16 * row_chunks) +
+                     (lane >> 2) * row_chunks + (lane & 3);
 #pragma unroll
     for (int j = 0; j < NLD; ++j) {
       lo[j] = __ldcs(p + 4 * j);
       hi[j] = __ldcs(p + 8 * row_chunks + 4 * j);
     }
+    if constexpr (Kind<KV>::kE4m3) scale = __ldg(a.k_scale + tile);
   }
 };
 
@@ -161,7 +166,8 @@ struct Page {
 template <int D, int KV>
 struct Query {
   uint32_t w[D / 16][2];   // b0, b1 of each of the D / 16 MMA steps
-  __device__ __forceinline__ void load(const uint16_t* row, bool live, int lane) {
+  // returns what the scores have to be multiplied by (1 unless q was scaled)
+  __device__ __forceinline__ float load(const uint16_t* row, bool live, int lane) {
     constexpr int per = Kind<KV>::kE4m3 ? 16 : 8;    // elements of a K chunk
     constexpr int NLD = D / (4 * per);
 #pragma unroll
@@ -178,6 +184,29 @@ struct Query {
         w[s + 1][1] = v.w;
       }
     }
+    if constexpr (Kind<KV>::kScaledQ) {
+      float amax = 0.f;
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float2 v = bits2_to_float2<true>(w[s][i]);
+          amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
+        }
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      const int e = max(static_cast<int>(__float_as_uint(amax) >> 23), 15);   // biased exponent
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + 127 + 14 - e) << 23);
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float2 v = bits2_to_float2<true>(w[s][i]);
+          w[s][i] = pack2<false>(v.x * up, v.y * up);
+        }
+      return __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+    }
+    return 1.f;
   }
 };
 
@@ -196,8 +225,8 @@ __device__ __forceinline__ void page_scores(float (&acc)[NT][4], const Page<D, K
     if constexpr (Kind<KV>::kE4m3) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t a0 = codes2<BF16>(lo[i] & 0xffffu), a2 = codes2<BF16>(lo[i] >> 16);
-        const uint32_t a1 = codes2<BF16>(hi[i] & 0xffffu), a3 = codes2<BF16>(hi[i] >> 16);
+        const uint32_t a0 = e4m3x2_to_f16x2(lo[i] & 0xffffu), a2 = e4m3x2_to_f16x2(lo[i] >> 16);
+        const uint32_t a1 = e4m3x2_to_f16x2(hi[i] & 0xffffu), a3 = e4m3x2_to_f16x2(hi[i] >> 16);
 #pragma unroll
         for (int t = 0; t < NT; ++t)
           mma16816<BF16>(acc[t], a0, a1, a2, a3, q[t].w[4 * j + i][0], q[t].w[4 * j + i][1]);
@@ -213,37 +242,87 @@ __device__ __forceinline__ void page_scores(float (&acc)[NT][4], const Page<D, K
   }
 }
 
-// Running (max, sum) of a row in log2 units; an empty row is (-inf, 0).
+// (reference, sum) of a row in log2 units: sum = sum over its tokens of
+// 2^(s - reference).  An empty row is (kNoScore, 0); 2^(-inf - kNoScore) is 0.
+constexpr float kNoScore = -3.402823466e38f;
 __device__ __forceinline__ void stat_join(float& m, float& l, float m2, float l2) {
   const float top = fmaxf(m, m2);
-  const float base = top == -INFINITY ? 0.f : top;
-  l = l * fast_exp2(m - base) + l2 * fast_exp2(m2 - base);
+  l = l * fast_exp2(m - top) + l2 * fast_exp2(m2 - top);
   m = top;
 }
 
 // ------------------------------------------------------------------- launch 1
+// What a warp keeps of one partition.
+template <int NT>
+struct Partition {
+  float m[NT][2], l[NT][2];   // of the lane's two columns of each tile, over its own tokens
+
+  // The scores of one page: into the workspace and the statistics.  The
+  // reference moves only when a score exceeds it by 2^8, so that few pages pay
+  // for a rescale; a sum of up to 2^8 a token is as exact as one of 1.
+  __device__ __forceinline__ void take(const float (&s)[NT][4], float4* out) {
+    bool grow = false;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      out[t * 32] = make_float4(s[t][0], s[t][1], s[t][2], s[t][3]);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) grow |= fmaxf(s[t][c], s[t][c + 2]) > m[t][c] + 8.f;
+    }
+    if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float top = fmaxf(m[t][c], fmaxf(s[t][c], s[t][c + 2]));
+          l[t][c] *= fast_exp2(m[t][c] - top);
+          m[t][c] = top;
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        l[t][c] += fast_exp2(s[t][c] - m[t][c]) + fast_exp2(s[t][c + 2] - m[t][c]);
+  }
+};
+
 template <int D, int KV, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 4 ? 1 : 2)
+__global__ void __launch_bounds__(Score<NT>::kWarps * 32, Score<NT>::kCtas)
 weights_score_kernel(const __grid_constant__ WeightsArgs a, Work ws) {
+  constexpr int WARPS = Score<NT>::kWarps;
   __shared__ int cum[kPrefix];
-  __shared__ int warp_sums[kWarps];
+  __shared__ int warp_sums[WARPS];
   constexpr int R = 8 * NT;
+  griddep_launch_dependents();   // the finish launch may do its prologue
   const int lane = threadIdx.x & 31;
-  const int w = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  prefix_pages(a, cum, warp_sums);
-  const Line line = make_line(a, cum);
+  const int w = blockIdx.x * WARPS + (threadIdx.x >> 5);
+  prefix_pages<WARPS>(a, cum, warp_sums);
+  const Line line = make_line(a, cum, static_cast<int>(gridDim.x) * WARPS);
   if (w >= line.workers) return;
   int64_t x = part_start(line, w);
   const int64_t end = part_start(line, w + 1);
   const int rows = a.n_q * a.group;
-  const int64_t page_bytes = 16 * D * (Kind<KV>::kE4m3 ? 1 : 2);
   while (x < end) {
     const Place at = find(cum, a.B, a.Hkv, x);
     const int L = __ldg(a.context_lens + at.b);
-    const int stop = static_cast<int>(min(static_cast<int64_t>(at.pages), at.page + (end - x)));
-    // q, and for the lane's two columns of each tile the first position not attended
+    const int n = static_cast<int>(min(static_cast<int64_t>(at.pages - at.page), end - x));
+    const int32_t* table = a.block_tables + static_cast<int64_t>(at.b) * a.mbs + at.page;
+    // block ids, 32 pages at a time, one a lane; -1 outside the pool
+    auto ids_from = [&](int i) {
+      int id = i + lane < n ? __ldg(table + i + lane) : -1;
+      if (i + lane < n && (id < 0 || id >= a.num_blocks)) {
+        atomicOr(a.status, kStatusBadBlock);
+        id = -1;
+      }
+      return id;
+    };
+    int ids = ids_from(0);
+    auto id_of = [&](int i) { return __shfl_sync(0xffffffffu, ids, i & 31); };
+    Page<D, KV> buf[2];
+    int id0 = id_of(0), id1 = -1;
+    buf[0].load(a, max(id0, 0), at.h, lane);
     Query<D, KV> q[NT];
-    int bound[NT][2];
+    float f[NT][2];   // score -> log2 units, for the lane's columns
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int r = 8 * t + (lane >> 2);
@@ -251,161 +330,235 @@ weights_score_kernel(const __grid_constant__ WeightsArgs a, Work ws) {
       const uint16_t* row = static_cast<const uint16_t*>(a.q) +
           ((static_cast<int64_t>(at.b) * a.q_tokens + a.q_first + i) * a.Hq +
            at.h * a.group + g) * D;
-      q[t].load(row, r < rows, lane);
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int col = 8 * t + 2 * (lane & 3) + c;
-        bound[t][c] = col < rows ? L - a.q_tokens + a.q_first + col / a.group + 1 : 0;
-      }
+      const float back = q[t].load(row, r < rows, lane) * a.scale_log2;
+      f[t][0] = __shfl_sync(0xffffffffu, back, (lane & 3) * 8);
+      f[t][1] = __shfl_sync(0xffffffffu, back, (lane & 3) * 8 + 4);
     }
-    float m[NT][2], l[NT][2];
+    // tokens from here on are not attended by some row; padding rows (q = 0)
+    // are left out by the finish launch
+    const int all_see = L - a.q_tokens + a.q_first + 1;
+    Partition<NT> part;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) m[t][c] = -INFINITY, l[t][c] = 0.f;
-    const int32_t* table = a.block_tables + static_cast<int64_t>(at.b) * a.mbs;
-    float4* out = ws.logits + (at.unit_start * NT) * 32 + lane;
-    for (int page = at.page; page < stop; ++page) {
-      const int id = __ldg(table + page);
-      const bool good = id >= 0 && id < a.num_blocks;
-      if (!good && lane == 0) atomicOr(a.status, kStatusBadBlock);
-      const int64_t tile = static_cast<int64_t>(good ? id : 0) * a.Hkv + at.h;
-      Page<D, KV> k;
-      k.load(static_cast<const uint8_t*>(a.k_cache) + tile * page_bytes, lane);
-      float f = a.scale_log2;
-      if constexpr (Kind<KV>::kE4m3) f *= __ldg(a.k_scale + tile);
+      for (int c = 0; c < 2; ++c) part.m[t][c] = kNoScore, part.l[t][c] = 0.f;
+    float4* out = ws.logits + (at.unit_start + at.page) * (NT * 32) + lane;
+    auto step = [&](const Page<D, KV>& k, int id, int i) {
       float s[NT][4];
       page_scores<D, KV, NT>(s, k, q);
-      const int tok = page * 16 + (lane >> 2);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const bool seen = good && tok + (i & 2 ? 8 : 0) < bound[t][i & 1];
-          s[t][i] = seen ? s[t][i] * f : -INFINITY;
-        }
-        out[(static_cast<int64_t>(page) * NT + t) * 32] =
-            make_float4(s[t][0], s[t][1], s[t][2], s[t][3]);
+        for (int j = 0; j < 4; ++j)
+          s[t][j] *= Kind<KV>::kE4m3 ? f[t][j & 1] * k.scale : f[t][j & 1];
+      const int first = (at.page + i) * 16;
+      if (first + 16 > all_see || id < 0) {
+        const int tok = first + (lane >> 2);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float top = fmaxf(m[t][c], fmaxf(s[t][c], s[t][c + 2]));
-          const float base = top == -INFINITY ? 0.f : top;
-          l[t][c] = l[t][c] * fast_exp2(m[t][c] - base) + fast_exp2(s[t][c] - base) +
-                    fast_exp2(s[t][c + 2] - base);
-          m[t][c] = top;
-        }
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int col = 8 * t + 2 * (lane & 3) + (j & 1);
+            if (id < 0 || tok + (j & 2 ? 8 : 0) >= all_see + col / a.group) s[t][j] = -INFINITY;
+          }
       }
+      part.take(s, out + static_cast<int64_t>(i) * (NT * 32));
+    };
+    for (int i = 0; i < n; i += 2) {
+      if (i + 1 < n) {
+        id1 = id_of(i + 1);
+        buf[1].load(a, max(id1, 0), at.h, lane);
+      }
+      step(buf[0], id0, i);
+      if (i + 1 >= n) break;
+      if (i + 2 < n) {
+        if (((i + 2) & 31) == 0) ids = ids_from(i + 2);
+        id0 = id_of(i + 2);
+        buf[0].load(a, max(id0, 0), at.h, lane);
+      }
+      step(buf[1], id1, i + 1);
     }
     // the partition's statistics: over the 8 lanes that hold the same columns
-    const int64_t part = static_cast<int64_t>(at.b) * a.Hkv + at.h + w;
+    const int64_t index = static_cast<int64_t>(at.b) * a.Hkv + at.h + w;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
       for (int c = 0; c < 2; ++c)
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1)
-          stat_join(m[t][c], l[t][c], __shfl_xor_sync(0xffffffffu, m[t][c], o),
-                    __shfl_xor_sync(0xffffffffu, l[t][c], o));
-      if (lane < 4) {
-        float2* st = ws.stats + part * R + 8 * t + 2 * lane;
-        st[0] = make_float2(m[t][0], l[t][0]);
-        st[1] = make_float2(m[t][1], l[t][1]);
-      }
+          stat_join(part.m[t][c], part.l[t][c], __shfl_xor_sync(0xffffffffu, part.m[t][c], o),
+                    __shfl_xor_sync(0xffffffffu, part.l[t][c], o));
+      if (lane < 4)
+        *reinterpret_cast<float4*>(ws.stats + index * R + 8 * t + 2 * lane) =
+            make_float4(part.m[t][0], part.l[t][0], part.m[t][1], part.l[t][1]);
     }
-    x += stop - at.page;
+    x += n;
   }
 }
 
 // ------------------------------------------------------------------- launch 2
-template <int NT>
-__global__ void __launch_bounds__(kThreads, 2)
-weights_finish_kernel(const __grid_constant__ WeightsArgs a, Work ws) {
-  __shared__ int cum[kPrefix];
-  __shared__ int warp_sums[kWarps];
-  constexpr int R = 8 * NT;
-  const int lane = threadIdx.x & 31;
-  const int w = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  prefix_pages(a, cum, warp_sums);
-  const Line line = make_line(a, cum);
-  if (w >= line.workers) return;
-  int64_t x = part_start(line, w);
-  const int64_t end = part_start(line, w + 1);
-  while (x < end) {
-    const Place at = find(cum, a.B, a.Hkv, x);
-    const int L = __ldg(a.context_lens + at.b);
-    const int stop = static_cast<int>(min(static_cast<int64_t>(at.pages), at.page + (end - x)));
-    const int64_t unit = static_cast<int64_t>(at.b) * a.Hkv + at.h;
-    // the unit's statistics: lane holds row lane % R of every 32 / R-th partition
-    const int w0 = part_of(line, at.unit_start), w1 = part_of(line, at.unit_start + at.pages - 1);
-    const float2* st = ws.stats + (unit + w0) * R;
-    float m = -INFINITY, l = 0.f;
-    for (int i = lane; i < (w1 - w0 + 1) * R; i += 32) {
-      const float2 v = st[i];
-      stat_join(m, l, v.x, v.y);
-    }
+// Joins the partitions [0, n) of a unit at st (R rows each): by one warp, lane
+// i taking row i % R of every 32 / R-th partition.
+template <int R>
+__device__ __forceinline__ float2 join_by_warp(const float2* st, int n, int lane) {
+  float m = kNoScore, l = 0.f;
+  for (int i = lane; i < n * R; i += 32) {
+    const float2 v = st[i];
+    stat_join(m, l, v.x, v.y);
+  }
 #pragma unroll
-    for (int o = R; o < 32; o <<= 1)
-      stat_join(m, l, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, l, o));
-    // an empty row gives every token 0: its logits are -inf
-    const float base = m == -INFINITY ? 0.f : m;
-    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+  for (int o = R; o < 32; o <<= 1)
+    stat_join(m, l, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, l, o));
+  return make_float2(m, l);   // of row lane % R
+}
+
+// A unit of more partitions than this is joined by a whole CTA, once for its
+// warps: at most two such units (its first and its last) reach into a CTA's pages.
+constexpr int kWarpJoin = 16;
+
+template <int NT>
+__global__ void __launch_bounds__(kFinishThreads, 2)
+weights_finish_kernel(const __grid_constant__ WeightsArgs a, Work ws, int score_workers) {
+  constexpr int R = 8 * NT;
+  __shared__ int cum[kPrefix];
+  __shared__ int warp_sums[kFinishWarps];
+  __shared__ float2 joined[2][R];
+  __shared__ float2 scratch[kFinishThreads];
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int w = blockIdx.x * kFinishWarps + (tid >> 5);
+  prefix_pages<kFinishWarps>(a, cum, warp_sums);
+  const Line scored = make_line(a, cum, score_workers);
+  const Line line = make_line(a, cum, static_cast<int>(gridDim.x) * kFinishWarps);
+  const int w_first = blockIdx.x * kFinishWarps;
+  griddep_wait();                        // the scores are written
+  if (w_first >= line.workers) return;   // the whole CTA
+  int long_unit[2] = {-1, -1};
+  {
+    const int w_last = min(w_first + kFinishWarps, line.workers);
+    const int64_t ends[2] = {part_start(line, w_first), part_start(line, w_last) - 1};
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const Place at = find(cum, a.B, a.Hkv, ends[e]);
+      const int unit = at.b * a.Hkv + at.h;
+      if (e == 1 && unit == long_unit[0]) break;
+      const int w0 = part_of(scored, at.unit_start);
+      const int n = part_of(scored, at.unit_start + at.pages - 1) - w0 + 1;
+      if (n <= kWarpJoin) continue;
+      long_unit[e] = unit;
+      const float2* st = ws.stats + (static_cast<int64_t>(unit) + w0) * R;
+      float m = kNoScore, l = 0.f;
+      for (int i = tid; i < n * R; i += kFinishThreads) {
+        const float2 v = st[i];
+        stat_join(m, l, v.x, v.y);
+      }
+      scratch[tid] = make_float2(m, l);
+      __syncthreads();
+      if (tid < R) {
+        for (int i = tid + R; i < kFinishThreads; i += R) stat_join(m, l, scratch[i].x, scratch[i].y);
+        joined[e][tid] = make_float2(m, l);
+      }
+      __syncthreads();
+    }
+  }
+  if (w >= line.workers) return;
+  const int64_t start = part_start(line, w);
+  int64_t x = part_start(line, w + 1);
+  const int rows = a.n_q * a.group;
+  while (x > start) {   // from the end: the scores written last are the likeliest in L2
+    const Place at = find(cum, a.B, a.Hkv, x - 1);
+    const int L = __ldg(a.context_lens + at.b);
+    const int n = static_cast<int>(min(static_cast<int64_t>(at.page) + 1, x - start));
+    const int unit = at.b * a.Hkv + at.h;
+    float2 st;
+    if (unit == long_unit[0]) {
+      st = joined[0][lane % R];
+    } else if (unit == long_unit[1]) {
+      st = joined[1][lane % R];
+    } else {
+      const int w0 = part_of(scored, at.unit_start);
+      st = join_by_warp<R>(ws.stats + (static_cast<int64_t>(unit) + w0) * R,
+                           part_of(scored, at.unit_start + at.pages - 1) - w0 + 1, lane);
+    }
+    // an empty row's and a padding row's tokens get 0
+    const float inv = lane % R < rows && (st.y > 0.f || st.y != st.y) ? 1.f / st.y : 0.f;
     float top[NT][2], f[NT][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int r = 8 * t + 2 * (lane & 3) + c;
-        top[t][c] = __shfl_sync(0xffffffffu, base, r);
+        top[t][c] = __shfl_sync(0xffffffffu, st.x, r);
         f[t][c] = __shfl_sync(0xffffffffu, inv, r);
       }
-    float* weights = a.weights + unit * a.stride;
-    const float4* in = ws.logits + (at.unit_start * NT) * 32 + lane;
-    for (int page = at.page; page < stop; ++page) {
+    float* weights = a.weights + static_cast<int64_t>(unit) * a.stride;
+    const float4* in = ws.logits + (at.unit_start + at.page) * (NT * 32) + lane;
+    float4 next[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) next[t] = in[t * 32];
+    for (int i = 0; i < n; ++i) {
+      float4 s[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) s[t] = next[t];
+      in -= NT * 32;
+      if (i + 1 < n) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) next[t] = in[t * 32];
+      }
+      const int tok = (at.page - i) * 16 + (lane >> 2) + (lane & 1) * 8;
+      const bool mine = (lane & 2) == 0 && tok < L;
+      float old = 0.f;
+      if (mine && a.decay != 0.f && tok < L - a.fresh) old = a.decay * weights[tok];
       float lo = 0.f, hi = 0.f;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const float4 s = in[(static_cast<int64_t>(page) * NT + t) * 32];
-        lo += fast_exp2(s.x - top[t][0]) * f[t][0] + fast_exp2(s.y - top[t][1]) * f[t][1];
-        hi += fast_exp2(s.z - top[t][0]) * f[t][0] + fast_exp2(s.w - top[t][1]) * f[t][1];
+        lo += fast_exp2(s[t].x - top[t][0]) * f[t][0] + fast_exp2(s[t].y - top[t][1]) * f[t][1];
+        hi += fast_exp2(s[t].z - top[t][0]) * f[t][0] + fast_exp2(s[t].w - top[t][1]) * f[t][1];
       }
 #pragma unroll
       for (int o = 1; o < 4; o <<= 1) {
         lo += __shfl_xor_sync(0xffffffffu, lo, o);
         hi += __shfl_xor_sync(0xffffffffu, hi, o);
       }
-      const int tok = page * 16 + (lane >> 2) + (lane & 1) * 8;
-      if ((lane & 2) == 0 && tok < L) {
-        const float old = a.decay != 0.f && tok < L - a.fresh ? a.decay * weights[tok] : 0.f;
-        weights[tok] = old + (lane & 1 ? hi : lo);
-      }
+      if (mine) weights[tok] = old + (lane & 1 ? hi : lo);
     }
-    x += stop - at.page;
+    x -= n;
   }
 }
 
 int tiles_of(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
 
-template <int D, int KV>
-cudaError_t launch_pass(const WeightsArgs& a, int nt, int grid, const Work& ws, cudaStream_t s) {
-  if (nt == 1) {
-    weights_score_kernel<D, KV, 1><<<grid, kThreads, 0, s>>>(a, ws);
-    weights_finish_kernel<1><<<grid, kThreads, 0, s>>>(a, ws);
-  } else if (nt == 2) {
-    weights_score_kernel<D, KV, 2><<<grid, kThreads, 0, s>>>(a, ws);
-    weights_finish_kernel<2><<<grid, kThreads, 0, s>>>(a, ws);
-  } else {
-    weights_score_kernel<D, KV, 4><<<grid, kThreads, 0, s>>>(a, ws);
-    weights_finish_kernel<4><<<grid, kThreads, 0, s>>>(a, ws);
-  }
-  return cudaGetLastError();
+// CTAs of a launch of `warps` warps each, `ctas` of them an SM; fewer when there
+// cannot be as many pages as warps.
+int weights_grid(const WeightsArgs& a, int warps, int ctas) {
+  const int64_t pages = static_cast<int64_t>(a.B) * a.Hkv *
+                        ((static_cast<int64_t>(a.max_context_len) + 15) / 16);
+  const int64_t want = (pages + warps - 1) / warps;
+  const int most = ctas * device_sm_count();
+  return static_cast<int>(want < 1 ? 1 : want < most ? want : most);
 }
 
-// CTAs of a launch: two a SM, fewer when there are fewer pages than warps.
-int weights_grid(int B, int Hkv, int max_context_len) {
-  const int64_t pages = static_cast<int64_t>(B) * Hkv * ((static_cast<int64_t>(max_context_len) + 15) / 16);
-  const int64_t want = (pages + kWarps - 1) / kWarps;
-  const int most = 2 * device_sm_count();
-  return static_cast<int>(want < 1 ? 1 : want < most ? want : most);
+template <int D, int KV, int NT>
+cudaError_t launch_tiles(const WeightsArgs& a, const Work& ws, cudaStream_t s) {
+  constexpr int warps = Score<NT>::kWarps;
+  const int grid = weights_grid(a, warps, Score<NT>::kCtas);
+  weights_score_kernel<D, KV, NT><<<grid, warps * 32, 0, s>>>(a, ws);
+  if (cudaError_t e = cudaGetLastError()) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(weights_grid(a, kFinishWarps, 2));
+  cfg.blockDim = dim3(kFinishThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, weights_finish_kernel<NT>, a, ws, grid * warps);
+}
+
+template <int D, int KV>
+cudaError_t launch_pass(const WeightsArgs& a, int nt, const Work& ws, cudaStream_t s) {
+  return nt == 1 ? launch_tiles<D, KV, 1>(a, ws, s) : nt == 2 ? launch_tiles<D, KV, 2>(a, ws, s)
+                                                              : launch_tiles<D, KV, 4>(a, ws, s);
 }
 
 }  // namespace
@@ -415,7 +568,7 @@ size_t weights_workspace_bytes(int B, int Hkv, int max_context_len, int rows) {
   if (B > kWeightsMaxBatch) B = kWeightsMaxBatch;
   const size_t units = static_cast<size_t>(B) * Hkv;
   const size_t pages = units * ((static_cast<size_t>(max_context_len) + 15) / 16);
-  const size_t parts = units + static_cast<size_t>(weights_grid(B, Hkv, max_context_len)) * kWarps;
+  const size_t parts = units + static_cast<size_t>(2 * device_sm_count()) * kMaxWarps;
   return align256(pages * nt * 32 * sizeof(float4)) + align256(parts * nt * 8 * sizeof(float2));
 }
 
@@ -437,7 +590,6 @@ cudaError_t launch_weights(const WeightsArgs& a0, bool fp8, bool bf16, cudaStrea
         a.fresh = 0;
       }
       const int nt = tiles_of(a.n_q * a.group);
-      const int grid = weights_grid(a.B, a.Hkv, a.max_context_len);
       const size_t pages = static_cast<size_t>(a.B) * a.Hkv * ((static_cast<size_t>(a.max_context_len) + 15) / 16);
       Work ws;
       ws.logits = static_cast<float4*>(a.workspace);
@@ -446,11 +598,11 @@ cudaError_t launch_weights(const WeightsArgs& a0, bool fp8, bool bf16, cudaStrea
       const int kv = (fp8 ? 2 : 0) + (bf16 ? 1 : 0);
       cudaError_t e;
       if (a.D == 128)
-        e = kv == 0 ? launch_pass<128, 0>(a, nt, grid, ws, s) : kv == 1 ? launch_pass<128, 1>(a, nt, grid, ws, s)
-          : kv == 2 ? launch_pass<128, 2>(a, nt, grid, ws, s) : launch_pass<128, 3>(a, nt, grid, ws, s);
+        e = kv == 0 ? launch_pass<128, 0>(a, nt, ws, s) : kv == 1 ? launch_pass<128, 1>(a, nt, ws, s)
+          : kv == 2 ? launch_pass<128, 2>(a, nt, ws, s) : launch_pass<128, 3>(a, nt, ws, s);
       else
-        e = kv == 0 ? launch_pass<64, 0>(a, nt, grid, ws, s) : kv == 1 ? launch_pass<64, 1>(a, nt, grid, ws, s)
-          : kv == 2 ? launch_pass<64, 2>(a, nt, grid, ws, s) : launch_pass<64, 3>(a, nt, grid, ws, s);
+        e = kv == 0 ? launch_pass<64, 0>(a, nt, ws, s) : kv == 1 ? launch_pass<64, 1>(a, nt, ws, s)
+          : kv == 2 ? launch_pass<64, 2>(a, nt, ws, s) : launch_pass<64, 3>(a, nt, ws, s);
       if (e) return e;
     }
   }
