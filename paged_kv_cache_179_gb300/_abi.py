@@ -743,10 +743,11 @@ def pa_attention_weights_workspace_size(num_seqs, num_q_heads, num_kv_heads, max
 
 def alloc_weights_workspace(num_seqs, num_q_heads, num_kv_heads, max_context_len,
                             queries_per_seq, device):
-    """Workspace for pa_attention_weights (need not be cleared)."""
+    """Caller-owned workspace for pa_attention_weights, zero-filled as it needs
+    to be before its first use."""
     n = pa_attention_weights_workspace_size(num_seqs, num_q_heads, num_kv_heads, max_context_len,
                                             queries_per_seq)
-    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+    return torch.zeros(max(n, 256), dtype=torch.uint8, device=device)
 
 
 def _weights_args(weights, q, k_cache, block_tables, context_lens, pool_dtype, dev):

@@ -3,26 +3,27 @@
 //   W[b][h][t] = old(t) + sum_r softmax_t(scale q_r . K_t)
 // over the query rows r of (sequence b, kv head h): n_q tokens times the query
 // group.  The weight of a token needs the softmax statistics of the whole
-// context, so there are two launches:
+// context, so one cooperative launch works in two phases with a grid barrier
+// between them:
 //   score:  every page's logits by mma.sync (a page's 16 tokens are the 16 rows
-//           of the MMA's A, the query rows its 8 columns), written to the
-//           workspace, and per partition and row the running (max, sum);
+//           of the MMA's A, the query rows its 8 columns) and, per partition and
+//           row, the running (reference, sum);
 //   finish: per row the statistics of the whole context, joined from those of
 //           its partitions, then each token's weights summed over the rows.
-// K is read once: 2 D bytes a token and kv head (D for E4M3) are the floor; the
-// logits (4 bytes a query row and token, written and read) stay in L2 when they
-// fit there.
+// K is read once: 2 D bytes a token and kv head (D for E4M3) are the floor.  A
+// warp keeps the logits of its first pages in shared memory (200 KB an SM) and
+// those behind them in the workspace, where they mostly stay in L2.
 //
 // Work split: the pages of all (sequence, kv head) units form one line, divided
-// evenly among the warps of both launches.  A warp's part of a unit is a
-// partition.  Units and warps both grow along the line, so unit + warp numbers
-// every partition uniquely, and a unit's partitions are consecutive.
+// evenly among the warps.  A warp's part of a unit is a partition.  Units and
+// warps both grow along the line, so unit + warp numbers every partition
+// uniquely, and a unit's partitions are consecutive.
 //
 // K goes from global memory straight into the MMA's registers.  A dot product
 // does not care in which order the dimensions are summed, so lane (r, c) of a
 // quad takes the 16-byte chunks c, c + 4, ... of rows r and r + 8, and q's
 // fragments are loaded with the same permutation.
-#include <climits>
+#include <mutex>
 
 #include "pa_e4m3.cuh"
 #include "pa_launch.h"
@@ -34,15 +35,17 @@ namespace {
 
 constexpr int kPrefix = kWeightsMaxBatch + 1;
 constexpr int kMaxWarps = 12;
-// Warps of a score CTA and CTAs an SM: up to 16 query rows keep 16 warps an SM;
-// the fragments of 32 take 64 registers, which leaves room for 12.
+// Warps of a CTA, CTAs an SM, and the pages whose logits a warp keeps in shared
+// memory: up to 16 query rows keep 16 warps an SM; the fragments of 32 take 64
+// registers, which leaves room for 12.
 template <int NT>
-struct Score {
+struct Shape {
   static constexpr int kWarps = NT == 4 ? 12 : 8;
   static constexpr int kCtas = NT == 4 ? 1 : 2;
+  static constexpr int kKept = NT == 1 ? 25 : NT == 2 ? 12 : 9;
+  static constexpr int kPage = NT * 32;   // float4s of a page's logits
+  static constexpr int kSmem = kWarps * kKept * kPage * 16;
 };
-constexpr int kFinishWarps = 8;
-constexpr int kFinishThreads = kFinishWarps * 32;
 
 // ------------------------------------------------------------ the line of pages
 struct Line {
@@ -124,11 +127,14 @@ __device__ __forceinline__ Place find(const int* cum, int B, int Hkv, int64_t x)
 // ------------------------------------------------------------------ workspace
 // logits: per page of the line and tile of 8 query rows, one float4 a lane (the
 // MMA's result fragment); statistics: per partition and row (max, sum), log2 units.
+// barrier: the grid barrier's count and generation; the count is 0 between calls.
 struct Work {
+  uint32_t* barrier;
   float4* logits;
   float2* stats;
 };
-__device__ __host__ __forceinline__ size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+constexpr size_t kBarrierBytes = 256;
+inline size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 // ----------------------------------------------------------------- K fragments
 // KV: 0 fp16, 1 bf16, 2 E4M3 with fp16 q, 3 E4M3 with bf16 q.  E4M3 codes become
@@ -251,7 +257,37 @@ __device__ __forceinline__ void stat_join(float& m, float& l, float m2, float l2
   m = top;
 }
 
-// ------------------------------------------------------------------- launch 1
+// ------------------------------------------------------------------ the kernel
+// Grid barrier among the `n` CTAs that have work, by one thread of each.  What a
+// CTA wrote before it (and a __syncthreads) is seen after it by the others.
+// False: the wait reached its limit.  A count above what a finished call can leave
+// is reported, and nobody is kept waiting for it.
+__device__ __forceinline__ bool grid_barrier(uint32_t* words, uint32_t n, unsigned* status,
+                                             uint64_t limit_ns) {
+  __threadfence();
+  const uint32_t gen = ld_acquire_b32(words + 1);
+  const uint32_t old = atomicAdd(words, 1u);
+  if (old > n - 1) {
+    atomicOr(status, kStatusWsDirty);
+    return true;
+  }
+  if (old == n - 1) {
+    atomicExch(words, 0u);
+    __threadfence();
+    st_release_gpu_b32(words + 1, gen + 1);
+    return true;
+  }
+  if (ld_acquire_b32(words + 1) != gen) return true;
+  const uint64_t t0 = global_ns();
+  while (ld_acquire_b32(words + 1) == gen) {
+    if (global_ns() - t0 >= limit_ns) {
+      atomicOr(status, kStatusTimeout);
+      return false;
+    }
+  }
+  return true;
+}
+
 // What a warp keeps of one partition.
 template <int NT>
 struct Partition {
@@ -286,22 +322,12 @@ struct Partition {
   }
 };
 
-template <int D, int KV, int NT>
-__global__ void __launch_bounds__(Score<NT>::kWarps * 32, Score<NT>::kCtas)
-weights_score_kernel(const __grid_constant__ WeightsArgs a, Work ws) {
-  constexpr int WARPS = Score<NT>::kWarps;
-  __shared__ int cum[kPrefix];
-  __shared__ int warp_sums[WARPS];
+// The scores of pages [x, end) of the line, by one warp.
+template <int D, int KV, int NT, typename LogitsAt>
+__device__ __forceinline__ void score_pages(const WeightsArgs& a, const Work& ws, const int* cum,
+                                            int64_t x, int64_t end, int w, int lane, int rows,
+                                            const LogitsAt& logits_at) {
   constexpr int R = 8 * NT;
-  griddep_launch_dependents();   // the finish launch may do its prologue
-  const int lane = threadIdx.x & 31;
-  const int w = blockIdx.x * WARPS + (threadIdx.x >> 5);
-  prefix_pages<WARPS>(a, cum, warp_sums);
-  const Line line = make_line(a, cum, static_cast<int>(gridDim.x) * WARPS);
-  if (w >= line.workers) return;
-  int64_t x = part_start(line, w);
-  const int64_t end = part_start(line, w + 1);
-  const int rows = a.n_q * a.group;
   while (x < end) {
     const Place at = find(cum, a.B, a.Hkv, x);
     const int L = __ldg(a.context_lens + at.b);
@@ -342,7 +368,6 @@ weights_score_kernel(const __grid_constant__ WeightsArgs a, Work ws) {
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int c = 0; c < 2; ++c) part.m[t][c] = kNoScore, part.l[t][c] = 0.f;
-    float4* out = ws.logits + (at.unit_start + at.page) * (NT * 32) + lane;
     auto step = [&](const Page<D, KV>& k, int id, int i) {
       float s[NT][4];
       page_scores<D, KV, NT>(s, k, q);
@@ -362,7 +387,7 @@ weights_score_kernel(const __grid_constant__ WeightsArgs a, Work ws) {
             if (id < 0 || tok + (j & 2 ? 8 : 0) >= all_see + col / a.group) s[t][j] = -INFINITY;
           }
       }
-      part.take(s, out + static_cast<int64_t>(i) * (NT * 32));
+      part.take(s, logits_at(x + i));
     };
     for (int i = 0; i < n; i += 2) {
       if (i + 1 < n) {
@@ -396,14 +421,13 @@ weights_score_kernel(const __grid_constant__ WeightsArgs a, Work ws) {
   }
 }
 
-// ------------------------------------------------------------------- launch 2
 // Joins the partitions [0, n) of a unit at st (R rows each): by one warp, lane
 // i taking row i % R of every 32 / R-th partition.
 template <int R>
 __device__ __forceinline__ float2 join_by_warp(const float2* st, int n, int lane) {
   float m = kNoScore, l = 0.f;
   for (int i = lane; i < n * R; i += 32) {
-    const float2 v = st[i];
+    const float2 v = __ldcg(st + i);
     stat_join(m, l, v.x, v.y);
   }
 #pragma unroll
@@ -416,55 +440,72 @@ __device__ __forceinline__ float2 join_by_warp(const float2* st, int n, int lane
 // warps: at most two such units (its first and its last) reach into a CTA's pages.
 constexpr int kWarpJoin = 16;
 
-template <int NT>
-__global__ void __launch_bounds__(kFinishThreads, 2)
-weights_finish_kernel(const __grid_constant__ WeightsArgs a, Work ws, int score_workers) {
+template <int D, int KV, int NT>
+__global__ void __launch_bounds__(Shape<NT>::kWarps * 32, Shape<NT>::kCtas)
+weights_kernel(const __grid_constant__ WeightsArgs a, Work ws) {
+  using S = Shape<NT>;
   constexpr int R = 8 * NT;
+  constexpr int kThreads = S::kWarps * 32;
+  extern __shared__ float4 kept_logits[];
   __shared__ int cum[kPrefix];
-  __shared__ int warp_sums[kFinishWarps];
+  __shared__ int warp_sums[S::kWarps];
   __shared__ float2 joined[2][R];
-  __shared__ float2 scratch[kFinishThreads];
+  __shared__ float2 scratch[kThreads];
+  __shared__ bool passed;
   const int tid = threadIdx.x, lane = tid & 31;
-  const int w = blockIdx.x * kFinishWarps + (tid >> 5);
-  prefix_pages<kFinishWarps>(a, cum, warp_sums);
-  const Line scored = make_line(a, cum, score_workers);
-  const Line line = make_line(a, cum, static_cast<int>(gridDim.x) * kFinishWarps);
-  const int w_first = blockIdx.x * kFinishWarps;
-  griddep_wait();                        // the scores are written
+  const int w_first = blockIdx.x * S::kWarps, w = w_first + (tid >> 5);
+  prefix_pages<S::kWarps>(a, cum, warp_sums);
+  const Line line = make_line(a, cum, static_cast<int>(gridDim.x) * S::kWarps);
   if (w_first >= line.workers) return;   // the whole CTA
+  const int rows = a.n_q * a.group;
+  const int64_t start = part_start(line, min(w, line.workers));
+  const int64_t end = part_start(line, min(w + 1, line.workers));
+  // the logits of page x: of the warp's first kKept in shared memory
+  float4* kept = kept_logits + (tid >> 5) * (S::kKept * S::kPage) + lane;
+  auto logits_at = [&](int64_t x) {
+    return x - start < S::kKept ? kept + (x - start) * S::kPage : ws.logits + x * S::kPage + lane;
+  };
+  score_pages<D, KV, NT>(a, ws, cum, start, end, w, lane, rows, logits_at);
+
+  // ---- all statistics are written
+  __syncthreads();
+  const uint32_t ctas = static_cast<uint32_t>((line.workers + S::kWarps - 1) / S::kWarps);
+  if (ctas > 1) {
+    if (tid == 0) passed = grid_barrier(ws.barrier, ctas, a.status, a.wait_limit_ns);
+    __syncthreads();
+    if (!passed) return;
+  }
+  // units of many partitions are joined by the whole CTA
   int long_unit[2] = {-1, -1};
   {
-    const int w_last = min(w_first + kFinishWarps, line.workers);
+    const int w_last = min(w_first + S::kWarps, line.workers);
     const int64_t ends[2] = {part_start(line, w_first), part_start(line, w_last) - 1};
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const Place at = find(cum, a.B, a.Hkv, ends[e]);
       const int unit = at.b * a.Hkv + at.h;
       if (e == 1 && unit == long_unit[0]) break;
-      const int w0 = part_of(scored, at.unit_start);
-      const int n = part_of(scored, at.unit_start + at.pages - 1) - w0 + 1;
+      const int w0 = part_of(line, at.unit_start);
+      const int n = part_of(line, at.unit_start + at.pages - 1) - w0 + 1;
       if (n <= kWarpJoin) continue;
       long_unit[e] = unit;
       const float2* st = ws.stats + (static_cast<int64_t>(unit) + w0) * R;
       float m = kNoScore, l = 0.f;
-      for (int i = tid; i < n * R; i += kFinishThreads) {
-        const float2 v = st[i];
+      for (int i = tid; i < n * R; i += kThreads) {
+        const float2 v = __ldcg(st + i);
         stat_join(m, l, v.x, v.y);
       }
       scratch[tid] = make_float2(m, l);
       __syncthreads();
       if (tid < R) {
-        for (int i = tid + R; i < kFinishThreads; i += R) stat_join(m, l, scratch[i].x, scratch[i].y);
+        for (int i = tid + R; i < kThreads; i += R) stat_join(m, l, scratch[i].x, scratch[i].y);
         joined[e][tid] = make_float2(m, l);
       }
       __syncthreads();
     }
   }
-  if (w >= line.workers) return;
-  const int64_t start = part_start(line, w);
-  int64_t x = part_start(line, w + 1);
-  const int rows = a.n_q * a.group;
-  while (x > start) {   // from the end: the scores written last are the likeliest in L2
+  int64_t x = end;
+  while (x > start) {   // from the end: the logits written last are the likeliest in L2
     const Place at = find(cum, a.B, a.Hkv, x - 1);
     const int L = __ldg(a.context_lens + at.b);
     const int n = static_cast<int>(min(static_cast<int64_t>(at.page) + 1, x - start));
@@ -475,9 +516,9 @@ weights_finish_kernel(const __grid_constant__ WeightsArgs a, Work ws, int score_
     } else if (unit == long_unit[1]) {
       st = joined[1][lane % R];
     } else {
-      const int w0 = part_of(scored, at.unit_start);
+      const int w0 = part_of(line, at.unit_start);
       st = join_by_warp<R>(ws.stats + (static_cast<int64_t>(unit) + w0) * R,
-                           part_of(scored, at.unit_start + at.pages - 1) - w0 + 1, lane);
+                           part_of(line, at.unit_start + at.pages - 1) - w0 + 1, lane);
     }
     // an empty row's and a padding row's tokens get 0
     const float inv = lane % R < rows && (st.y > 0.f || st.y != st.y) ? 1.f / st.y : 0.f;
@@ -491,35 +532,38 @@ weights_finish_kernel(const __grid_constant__ WeightsArgs a, Work ws, int score_
         f[t][c] = __shfl_sync(0xffffffffu, inv, r);
       }
     float* weights = a.weights + static_cast<int64_t>(unit) * a.stride;
-    const float4* in = ws.logits + (at.unit_start + at.page) * (NT * 32) + lane;
-    float4 next[NT];
+    // a few pages at a time: their old weights and logits are asked for together
+    constexpr int kGroup = NT == 4 ? 2 : 4;
+    for (int i = 0; i < n; i += kGroup) {
+      float4 s[kGroup][NT];
+      float old[kGroup];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) next[t] = in[t * 32];
-    for (int i = 0; i < n; ++i) {
-      float4 s[NT];
+      for (int j = 0; j < kGroup; ++j) {
+        old[j] = 0.f;
+        if (i + j >= n) continue;
+        const int tok = (at.page - i - j) * 16 + (lane >> 2) + (lane & 1) * 8;
+        if ((lane & 2) == 0 && a.decay != 0.f && tok < L - a.fresh) old[j] = weights[tok];
+        const float4* in = logits_at(x - 1 - i - j);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) s[t] = next[t];
-      in -= NT * 32;
-      if (i + 1 < n) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t) next[t] = in[t * 32];
-      }
-      const int tok = (at.page - i) * 16 + (lane >> 2) + (lane & 1) * 8;
-      const bool mine = (lane & 2) == 0 && tok < L;
-      float old = 0.f;
-      if (mine && a.decay != 0.f && tok < L - a.fresh) old = a.decay * weights[tok];
-      float lo = 0.f, hi = 0.f;
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        lo += fast_exp2(s[t].x - top[t][0]) * f[t][0] + fast_exp2(s[t].y - top[t][1]) * f[t][1];
-        hi += fast_exp2(s[t].z - top[t][0]) * f[t][0] + fast_exp2(s[t].w - top[t][1]) * f[t][1];
+        for (int t = 0; t < NT; ++t) s[j][t] = in[t * 32];
       }
 #pragma unroll
-      for (int o = 1; o < 4; o <<= 1) {
-        lo += __shfl_xor_sync(0xffffffffu, lo, o);
-        hi += __shfl_xor_sync(0xffffffffu, hi, o);
+      for (int j = 0; j < kGroup; ++j) {
+        if (i + j >= n) break;
+        const int tok = (at.page - i - j) * 16 + (lane >> 2) + (lane & 1) * 8;
+        float lo = 0.f, hi = 0.f;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          lo += fast_exp2(s[j][t].x - top[t][0]) * f[t][0] + fast_exp2(s[j][t].y - top[t][1]) * f[t][1];
+          hi += fast_exp2(s[j][t].z - top[t][0]) * f[t][0] + fast_exp2(s[j][t].w - top[t][1]) * f[t][1];
+        }
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+          lo += __shfl_xor_sync(0xffffffffu, lo, o);
+          hi += __shfl_xor_sync(0xffffffffu, hi, o);
+        }
+        if ((lane & 2) == 0 && tok < L) weights[tok] = a.decay * old[j] + (lane & 1 ? hi : lo);
       }
-      if (mine) weights[tok] = old + (lane & 1 ? hi : lo);
     }
     x -= n;
   }
@@ -539,20 +583,34 @@ int weights_grid(const WeightsArgs& a, int warps, int ctas) {
 
 template <int D, int KV, int NT>
 cudaError_t launch_tiles(const WeightsArgs& a, const Work& ws, cudaStream_t s) {
-  constexpr int warps = Score<NT>::kWarps;
-  const int grid = weights_grid(a, warps, Score<NT>::kCtas);
-  weights_score_kernel<D, KV, NT><<<grid, warps * 32, 0, s>>>(a, ws);
-  if (cudaError_t e = cudaGetLastError()) return e;
+  using S = Shape<NT>;
+  auto* kernel = weights_kernel<D, KV, NT>;
+  {
+    // more than 48 KB of shared memory has to be asked for, once per device
+    static std::mutex mu;
+    static bool raised[kMaxDevices] = {};
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev)) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!raised[dev]) {
+      if (cudaError_t e = cudaFuncSetAttribute(
+              kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem))
+        return e;
+      raised[dev] = true;
+    }
+  }
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(weights_grid(a, kFinishWarps, 2));
-  cfg.blockDim = dim3(kFinishThreads);
+  cfg.gridDim = dim3(weights_grid(a, S::kWarps, S::kCtas));
+  cfg.blockDim = dim3(S::kWarps * 32);
+  cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
+  attr.id = cudaLaunchAttributeCooperative;   // the CTAs wait for one another
+  attr.val.cooperative = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, weights_finish_kernel<NT>, a, ws, grid * warps);
+  return cudaLaunchKernelEx(&cfg, kernel, a, ws);
 }
 
 template <int D, int KV>
@@ -569,7 +627,8 @@ size_t weights_workspace_bytes(int B, int Hkv, int max_context_len, int rows) {
   const size_t units = static_cast<size_t>(B) * Hkv;
   const size_t pages = units * ((static_cast<size_t>(max_context_len) + 15) / 16);
   const size_t parts = units + static_cast<size_t>(2 * device_sm_count()) * kMaxWarps;
-  return align256(pages * nt * 32 * sizeof(float4)) + align256(parts * nt * 8 * sizeof(float2));
+  return kBarrierBytes + align256(pages * nt * 32 * sizeof(float4)) +
+         align256(parts * nt * 8 * sizeof(float2));
 }
 
 cudaError_t launch_weights(const WeightsArgs& a0, bool fp8, bool bf16, cudaStream_t s) {
@@ -592,9 +651,11 @@ cudaError_t launch_weights(const WeightsArgs& a0, bool fp8, bool bf16, cudaStrea
       const int nt = tiles_of(a.n_q * a.group);
       const size_t pages = static_cast<size_t>(a.B) * a.Hkv * ((static_cast<size_t>(a.max_context_len) + 15) / 16);
       Work ws;
-      ws.logits = static_cast<float4*>(a.workspace);
-      ws.stats = reinterpret_cast<float2*>(static_cast<uint8_t*>(a.workspace) +
-                                           align256(pages * nt * 32 * sizeof(float4)));
+      uint8_t* base = static_cast<uint8_t*>(a.workspace);
+      ws.barrier = reinterpret_cast<uint32_t*>(base);
+      base += kBarrierBytes;
+      ws.logits = reinterpret_cast<float4*>(base);
+      ws.stats = reinterpret_cast<float2*>(base + align256(pages * nt * 32 * sizeof(float4)));
       const int kv = (fp8 ? 2 : 0) + (bf16 ? 1 : 0);
       cudaError_t e;
       if (a.D == 128)

@@ -212,6 +212,7 @@ def run_weights(q, kc, ks, bt, lens, w, scale, decay, fresh, max_len=None, ws=No
     n = _abi.pa_attention_weights_workspace_size(B, Hq, Hkv, mx, n_q)
     if ws is None:
         ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")   # NaN everywhere
+        ws[:256] = 0                                                   # but for the barrier
     wd = w.cuda()
     args = (bt.cuda(), lens.cuda(), mx, scale, ws)
     if ks is None:
@@ -307,6 +308,20 @@ def test_attention_weights_bad_indexes_are_skipped_and_reported():
     got = run_weights(q, kc, ks, bt, L2, w, .125, 0., 0).cpu()
     assert _abi.pa_get_status()[1] == _abi.PA_STATUS_BAD_LEN
     assert torch.equal(got[1], w[1])
+
+
+def test_attention_weights_reports_a_workspace_that_was_not_cleared():
+    q, kc, ks, bt, L, w = weights_case([640, 3], 4, 2, 64, 1, "16", F16, 14)
+    n = _abi.pa_attention_weights_workspace_size(2, 4, 2, bt.shape[1] * 16, 1)
+    ws = torch.full((n,), 0x7f, dtype=torch.uint8, device="cuda")
+    run_weights(q, kc, ks, bt, L, w, .125, 0., 0, ws=ws)
+    assert _abi.pa_get_status() == (_abi.PA_ERR_WORKSPACE, _abi.PA_STATUS_WS_DIRTY)
+    ws.zero_()
+    got = run_weights(q, kc, ks, bt, L, w, .125, 0., 0, ws=ws)
+    ok()
+    again = run_weights(q, kc, ks, bt, L, w, .125, 0., 0, ws=ws)   # left as it was needed
+    ok()
+    assert torch.equal(got, again) and not ws[:4].any()
 
 
 def test_attention_weights_workspace_too_small():
