@@ -117,12 +117,11 @@ int pa_rope_append_fp8(void *q_out, const void *q, int64_t q_stride, const void 
  *   q: [num_seqs][n_q][num_q_heads][head_dim]; queries_per_seq n_q 1..1024: up
  *   to 32 query rows (n_q x group) take one pass over K, more take several.
  *   workspace: pa_attention_weights_workspace_size bytes, 256-byte aligned,
- *   zero-filled by the caller once before its first use (its first 256 bytes
- *   are enough): its barrier's count, which every call leaves at zero.  It then
- *   serves call after call, whatever their sizes.  After a status with
- *   PA_STATUS_TIMEOUT or PA_STATUS_WS_DIRTY (a count that no call leaves)
+ *   zero-filled by the caller once before its first use; it then serves call
+ *   after call, whatever their sizes.  After a status with PA_STATUS_TIMEOUT or
+ *   PA_STATUS_WS_DIRTY (it held what no call leaves; results may be wrong)
  *   zero-fill it again.  Calls that share one must not overlap on the device.
- * One cooperative launch per pass: its CTAs wait, bounded by 2 s, for one
+ * One cooperative launch per pass: its warps wait, bounded by 2 s, for one
  * another's softmax statistics.
  * Results do not depend on the order of execution.
  */

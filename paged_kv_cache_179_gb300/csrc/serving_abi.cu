@@ -108,6 +108,7 @@ int attention_weights(WeightsArgs a, int block_size, float scale, int dtype, siz
                                                             a.q_tokens))
     return PA_ERR_WORKSPACE;
   a.scale_log2 = scale * 1.4426950408889634f;
+  a.wide = aligned(a.k_cache, 32);
   a.wait_limit_ns = kWaitLimitNs;
   return cuda_status(launch_weights(a, fp8, dtype == PA_BF16, static_cast<cudaStream_t>(stream)));
 }

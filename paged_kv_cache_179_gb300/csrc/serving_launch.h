@@ -64,7 +64,8 @@ struct WeightsArgs {
   int q_first, n_q;            // those this pass serves
   float scale_log2, decay;
   int fresh;                   // tokens whose old weight is 0
-  uint64_t wait_limit_ns;      // time limit of the grid barrier's wait
+  bool wide;                   // k_cache is 32-byte aligned
+  uint64_t wait_limit_ns;      // time limit of a warp's wait for others
 };
 constexpr int kWeightsMaxBatch = 512;    // sequences per launch pair
 constexpr int kWeightsMaxRows = 32;      // query rows per pass

@@ -3,16 +3,18 @@
 //   W[b][h][t] = old(t) + sum_r softmax_t(scale q_r . K_t)
 // over the query rows r of (sequence b, kv head h): n_q tokens times the query
 // group.  The weight of a token needs the softmax statistics of the whole
-// context, so one cooperative launch works in two phases with a grid barrier
-// between them:
+// context, so one cooperative launch works in two phases:
 //   score:  every page's logits by mma.sync (a page's 16 tokens are the 16 rows
 //           of the MMA's A, the query rows its 8 columns) and, per partition and
 //           row, the running (reference, sum);
 //   finish: per row the statistics of the whole context, joined from those of
 //           its partitions, then each token's weights summed over the rows.
+// A warp waits between them only for the warps that share its first and its last
+// (sequence, kv head), so that slow SMs do not hold up the others.
 // K is read once: 2 D bytes a token and kv head (D for E4M3) are the floor.  A
-// warp keeps the logits of its first pages in shared memory (200 KB an SM) and
-// those behind them in the workspace, where they mostly stay in L2.
+// warp keeps the logits of its first pages in shared memory and those behind
+// them in the workspace, where they mostly stay in L2; the old weights come into
+// shared memory while K is read.
 //
 // Work split: the pages of all (sequence, kv head) units form one line, divided
 // evenly among the warps.  A warp's part of a unit is a partition.  Units and
@@ -21,7 +23,7 @@
 //
 // K goes from global memory straight into the MMA's registers.  A dot product
 // does not care in which order the dimensions are summed, so lane (r, c) of a
-// quad takes the 16-byte chunks c, c + 4, ... of rows r and r + 8, and q's
+// quad takes the 32-byte chunks c, c + 4, ... of rows r and r + 8, and q's
 // fragments are loaded with the same permutation.
 #include <mutex>
 
@@ -35,33 +37,42 @@ namespace {
 
 constexpr int kPrefix = kWeightsMaxBatch + 1;
 constexpr int kMaxWarps = 12;
-// Warps of a CTA, CTAs an SM, and the pages whose logits a warp keeps in shared
-// memory: up to 16 query rows keep 16 warps an SM; the fragments of 32 take 64
-// registers, which leaves room for 12.
+// Warps of a CTA, CTAs an SM, and what a warp's share of shared memory holds: the
+// logits of kKept pages and the old weights of kOld.  Up to 16 query rows keep 16
+// warps an SM; the q fragments of 32 take 64 registers, which leaves room for 12.
 template <int NT>
 struct Shape {
   static constexpr int kWarps = NT == 4 ? 12 : 8;
   static constexpr int kCtas = NT == 4 ? 1 : 2;
-  static constexpr int kKept = NT == 1 ? 25 : NT == 2 ? 12 : 9;
-  static constexpr int kPage = NT * 32;   // float4s of a page's logits
-  static constexpr int kSmem = kWarps * kKept * kPage * 16;
+  static constexpr int kKept = NT == 1 ? 22 : NT == 2 ? 11 : 8;
+  static constexpr int kPage = NT * 32;        // float4s of a page's logits
+  static constexpr int kOld = 32;
+  static constexpr int kWarpBytes = kKept * kPage * 16 + kOld * 64;
+  static constexpr int kSmem = kWarps * kWarpBytes;
 };
 
 // ------------------------------------------------------------ the line of pages
 struct Line {
   int64_t n;        // pages of all units
   int workers;      // warps that have pages: each has at least one
+  bool small;       // (n + 1) * workers fits 32 bits: the short division will do
 };
 __device__ __forceinline__ Line make_line(const WeightsArgs& a, const int* cum, int warps) {
   const int64_t n = static_cast<int64_t>(cum[a.B]) * a.Hkv;
-  return Line{n, static_cast<int>(n < warps ? n : warps)};
+  const int workers = static_cast<int>(n < warps ? n : warps);
+  return Line{n, workers, (n + 1) * workers < (INT64_C(1) << 32)};
 }
 // The pages worker w takes: [start(w), start(w + 1)).
 __device__ __forceinline__ int64_t part_start(const Line& l, int w) {
+  if (l.small)
+    return static_cast<uint32_t>(l.n) * static_cast<uint32_t>(w) / static_cast<uint32_t>(l.workers);
   return l.n * w / l.workers;
 }
 // The worker that takes page x of the line.
 __device__ __forceinline__ int part_of(const Line& l, int64_t x) {
+  if (l.small)
+    return static_cast<int>((static_cast<uint32_t>(x + 1) * static_cast<uint32_t>(l.workers) - 1u) /
+                            static_cast<uint32_t>(l.n));
   return static_cast<int>(((x + 1) * l.workers - 1) / l.n);
 }
 
@@ -118,23 +129,34 @@ __device__ __forceinline__ Place find(const int* cum, int B, int Hkv, int64_t x)
   p.b = lo;
   p.pages = cum[lo + 1] - cum[lo];
   const int64_t in_seq = x - static_cast<int64_t>(cum[lo]) * Hkv;
-  p.h = static_cast<int>(in_seq / p.pages);
+  // fewer than 2^31 pages a sequence; all its heads' may be more
+  p.h = in_seq < (INT64_C(1) << 32)
+            ? static_cast<int>(static_cast<uint32_t>(in_seq) / static_cast<uint32_t>(p.pages))
+            : static_cast<int>(in_seq / p.pages);
   p.page = static_cast<int>(in_seq - static_cast<int64_t>(p.h) * p.pages);
   p.unit_start = x - p.page;
   return p;
 }
 
 // ------------------------------------------------------------------ workspace
-// logits: per page of the line and tile of 8 query rows, one float4 a lane (the
-// MMA's result fragment); statistics: per partition and row (max, sum), log2 units.
-// barrier: the grid barrier's count and generation; the count is 0 between calls.
+// sync[0]: CTAs done, 0 between calls; sync[1]: the number of the last call;
+// sync[2 + w]: the call in which warp w has last written its statistics.
+// logits: per page of the line and tile of 8 query rows, [token][row] (a token's
+// two halves swapped by bit 2 of the token: no bank conflicts in shared memory);
+// of 32 rows, most of which go to the workspace, as the MMA's result fragment, one
+// float4 a lane.
+// statistics: per partition and row (reference, sum), log2 units.
 struct Work {
-  uint32_t* barrier;
-  float4* logits;
+  uint32_t* sync;
+  float* logits;
   float2* stats;
 };
-constexpr size_t kBarrierBytes = 256;
 inline size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+
+// 4-byte asynchronous copy global -> shared.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
 
 // ----------------------------------------------------------------- K fragments
 // KV: 0 fp16, 1 bf16, 2 E4M3 with fp16 q, 3 E4M3 with bf16 q.  E4M3 codes become
@@ -148,21 +170,47 @@ struct Kind {
   static constexpr bool kScaledQ = KV == 3;
 };
 
-// The lane's part of one page: NLD 16-byte chunks of row r, then of row r + 8.
+// 32 bytes of global memory that are read once.
+struct Bytes32 {
+  uint32_t w[8];
+};
+__device__ __forceinline__ Bytes32 load32(const void* p, bool aligned) {
+  Bytes32 v;
+  if (!aligned) {   // a pool that starts at 16 bytes
+    const uint4 x = __ldcs(static_cast<const uint4*>(p));
+    const uint4 y = __ldcs(static_cast<const uint4*>(p) + 1);
+    return Bytes32{{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w}};
+  }
+  asm volatile("ld.global.L1::no_allocate.L2::evict_first.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]), "=r"(v.w[4]),
+                 "=r"(v.w[5]), "=r"(v.w[6]), "=r"(v.w[7])
+               : "l"(p));
+  return v;
+}
+
+// The lane's part of one page: 32-byte chunks c, c + 4, ... of row r, then of row
+// r + 8, so that the quad of a row reads whole 128-byte lines.
 template <int D, int KV>
 struct Page {
-  static constexpr int NLD = D / (Kind<KV>::kE4m3 ? 64 : 32);
-  uint4 lo[NLD], hi[NLD];
+  static constexpr int kRow = D * (Kind<KV>::kE4m3 ? 1 : 2);   // bytes
+  static constexpr int NLD = kRow < 128 ? 1 : kRow / 128;
+  Bytes32 lo[NLD], hi[NLD];
   float scale;     // of an E4M3 page
   __device__ __forceinline__ void load(const WeightsArgs& a, int id, int h, int lane) {
-    constexpr int row_chunks = NLD * 4;
     const int64_t tile = static_cast<int64_t>(id) * a.Hkv + h;
-    const uint4* p = static_cast<const uint4*>(a.k_cache) + tile * (16 * row_chunks) +
-                     (lane >> 2) * row_chunks + (lane & 3);
+    const uint8_t* p = static_cast<const uint8_t*>(a.k_cache) + tile * (16 * kRow) +
+                       (lane >> 2) * kRow;
+    if constexpr (kRow < 128) {   // 64-byte rows: 16 bytes a lane
+      const uint4 x = __ldcs(reinterpret_cast<const uint4*>(p + (lane & 3) * 16));
+      const uint4 y = __ldcs(reinterpret_cast<const uint4*>(p + 8 * kRow + (lane & 3) * 16));
+      lo[0] = Bytes32{{x.x, x.y, x.z, x.w, 0, 0, 0, 0}};
+      hi[0] = Bytes32{{y.x, y.y, y.z, y.w, 0, 0, 0, 0}};
+    } else {
 #pragma unroll
-    for (int j = 0; j < NLD; ++j) {
-      lo[j] = __ldcs(p + 4 * j);
-      hi[j] = __ldcs(p + 8 * row_chunks + 4 * j);
+      for (int j = 0; j < NLD; ++j) {
+        lo[j] = load32(p + ((lane & 3) + 4 * j) * 32, a.wide);
+        hi[j] = load32(p + 8 * kRow + ((lane & 3) + 4 * j) * 32, a.wide);
+      }
     }
     if constexpr (Kind<KV>::kE4m3) scale = __ldg(a.k_scale + tile);
   }
@@ -174,10 +222,11 @@ struct Query {
   uint32_t w[D / 16][2];   // b0, b1 of each of the D / 16 MMA steps
   // returns what the scores have to be multiplied by (1 unless q was scaled)
   __device__ __forceinline__ float load(const uint16_t* row, bool live, int lane) {
-    constexpr int per = Kind<KV>::kE4m3 ? 16 : 8;    // elements of a K chunk
-    constexpr int NLD = D / (4 * per);
+    // elements of a K chunk: its bytes over an element's
+    constexpr int kRow = Page<D, KV>::kRow;
+    constexpr int per = (kRow < 128 ? 16 : 32) / (Kind<KV>::kE4m3 ? 1 : 2);
 #pragma unroll
-    for (int j = 0; j < NLD; ++j) {
+    for (int j = 0; j < D / (4 * per); ++j) {
 #pragma unroll
       for (int x = 0; x < per / 8; ++x) {
         uint4 v = make_uint4(0, 0, 0, 0);
@@ -224,28 +273,65 @@ __device__ __forceinline__ void page_scores(float (&acc)[NT][4], const Page<D, K
   for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[t][i] = 0.f;
+  // a step takes 4 elements a lane: two words of 16-bit values, one of codes
+  constexpr int kWords = Page<D, KV>::kRow < 128 ? 4 : 8;
 #pragma unroll
   for (int j = 0; j < Page<D, KV>::NLD; ++j) {
-    const uint32_t lo[4] = {k.lo[j].x, k.lo[j].y, k.lo[j].z, k.lo[j].w};
-    const uint32_t hi[4] = {k.hi[j].x, k.hi[j].y, k.hi[j].z, k.hi[j].w};
+    const uint32_t* lo = k.lo[j].w;
+    const uint32_t* hi = k.hi[j].w;
     if constexpr (Kind<KV>::kE4m3) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < kWords; ++i) {
         const uint32_t a0 = e4m3x2_to_f16x2(lo[i] & 0xffffu), a2 = e4m3x2_to_f16x2(lo[i] >> 16);
         const uint32_t a1 = e4m3x2_to_f16x2(hi[i] & 0xffffu), a3 = e4m3x2_to_f16x2(hi[i] >> 16);
 #pragma unroll
         for (int t = 0; t < NT; ++t)
-          mma16816<BF16>(acc[t], a0, a1, a2, a3, q[t].w[4 * j + i][0], q[t].w[4 * j + i][1]);
+          mma16816<BF16>(acc[t], a0, a1, a2, a3, q[t].w[kWords * j + i][0],
+                         q[t].w[kWords * j + i][1]);
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < kWords / 2; ++i)
 #pragma unroll
         for (int t = 0; t < NT; ++t)
           mma16816<BF16>(acc[t], lo[2 * i], hi[2 * i], lo[2 * i + 1], hi[2 * i + 1],
-                         q[t].w[2 * j + i][0], q[t].w[2 * j + i][1]);
+                         q[t].w[kWords / 2 * j + i][0], q[t].w[kWords / 2 * j + i][1]);
     }
   }
+}
+
+// Two fp32 values an instruction.
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 pack(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpack(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 exp2_2(F2 a) {
+  const float2 x = unpack(a);
+  return pack(fast_exp2(x.x), fast_exp2(x.y));
 }
 
 // (reference, sum) of a row in log2 units: sum = sum over its tokens of
@@ -258,151 +344,180 @@ __device__ __forceinline__ void stat_join(float& m, float& l, float m2, float l2
 }
 
 // ------------------------------------------------------------------ the kernel
-// Grid barrier among the `n` CTAs that have work, by one thread of each.  What a
-// CTA wrote before it (and a __syncthreads) is seen after it by the others.
-// False: the wait reached its limit.  A count above what a finished call can leave
-// is reported, and nobody is kept waiting for it.
-__device__ __forceinline__ bool grid_barrier(uint32_t* words, uint32_t n, unsigned* status,
-                                             uint64_t limit_ns) {
-  __threadfence();
-  const uint32_t gen = ld_acquire_b32(words + 1);
-  const uint32_t old = atomicAdd(words, 1u);
-  if (old > n - 1) {
-    atomicOr(status, kStatusWsDirty);
-    return true;
-  }
-  if (old == n - 1) {
-    atomicExch(words, 0u);
-    __threadfence();
-    st_release_gpu_b32(words + 1, gen + 1);
-    return true;
-  }
-  if (ld_acquire_b32(words + 1) != gen) return true;
-  const uint64_t t0 = global_ns();
-  while (ld_acquire_b32(words + 1) == gen) {
-    if (global_ns() - t0 >= limit_ns) {
-      atomicOr(status, kStatusTimeout);
-      return false;
+// Waits until warps [w0, w0 + n) have written their statistics in call `call`;
+// by the threads `first`, first + step, ... of a warp or CTA, each for its share.
+// False: the wait reached its limit.
+__device__ __forceinline__ bool await_warps(const Work& ws, int w0, int n, uint32_t call, int first,
+                                            int step, unsigned* status, uint64_t limit_ns) {
+  for (int i = first; i < n; i += step) {
+    const uint32_t* flag = ws.sync + 2 + w0 + i;
+    if (ld_acquire_b32(flag) == call) continue;
+    const uint64_t t0 = global_ns();
+    while (ld_acquire_b32(flag) != call) {
+      if (global_ns() - t0 >= limit_ns) {
+        atomicOr(status, kStatusTimeout);
+        return false;
+      }
     }
   }
   return true;
 }
 
-// What a warp keeps of one partition.
-template <int NT>
-struct Partition {
-  float m[NT][2], l[NT][2];   // of the lane's two columns of each tile, over its own tokens
+// Where the score of (token of the page, row 2 c of tile t) stands among a page's.
+__device__ __forceinline__ int logit_at(int t, int tok, int c) {
+  return t * 128 + tok * 8 + (((c >> 1) ^ ((tok >> 2) & 1)) << 2) + (c & 1) * 2;
+}
 
-  // The scores of one page: into the workspace and the statistics.  The
-  // reference moves only when a score exceeds it by 2^8, so that few pages pay
-  // for a rescale; a sum of up to 2^8 a token is as exact as one of 1.
-  __device__ __forceinline__ void take(const float (&s)[NT][4], float4* out) {
-    bool grow = false;
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      out[t * 32] = make_float4(s[t][0], s[t][1], s[t][2], s[t][3]);
-#pragma unroll
-      for (int c = 0; c < 2; ++c) grow |= fmaxf(s[t][c], s[t][c + 2]) > m[t][c] + 8.f;
+// One warp's pages of one unit: n pages from page at.page on.  Calls take(scores,
+// scale of the page, i, skip) for each (i counts from at.page; skip: its block is
+// outside the pool).
+template <int D, int KV, int NT, typename Take>
+__device__ __forceinline__ void for_pages(const WeightsArgs& a, const Place& at, int n, int lane,
+                                          const Query<D, KV> (&q)[NT], const Take& take) {
+  using P = Page<D, KV>;
+  // pages in registers, the one at work among them: up to 64 registers
+  constexpr int kAhead = P::kRow >= 256 || NT == 4 ? 2 : NT == 1 ? 4 : 3;
+  const int32_t* table = a.block_tables + static_cast<int64_t>(at.b) * a.mbs + at.page;
+  // block ids, 32 pages at a time, one a lane; -1 outside the pool
+  auto ids_from = [&](int j) {
+    int id = j + lane < n ? __ldg(table + j + lane) : -1;
+    if (j + lane < n && (id < 0 || id >= a.num_blocks)) {
+      atomicOr(a.status, kStatusBadBlock);
+      id = -1;
     }
-    if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float top = fmaxf(m[t][c], fmaxf(s[t][c], s[t][c + 2]));
-          l[t][c] *= fast_exp2(m[t][c] - top);
-          m[t][c] = top;
-        }
+    return id;
+  };
+  int ids = ids_from(0);
+  P buf[kAhead];
+  uint32_t bad = 0;   // of the last 32 pages asked for: outside the pool
+  auto ask = [&](int j, P& into) {
+    if (j < n) {
+      if ((j & 31) == 0 && j > 0) ids = ids_from(j);
+      const int id = __shfl_sync(0xffffffffu, ids, j & 31);
+      bad = id < 0 ? bad | 1u << (j & 31) : bad & ~(1u << (j & 31));
+      into.load(a, max(id, 0), at.h, lane);
     }
+  };
+  auto step = [&](const P& k, int j) {
+    float s[NT][4];
+    page_scores<D, KV, NT>(s, k, q);
+    take(s, Kind<KV>::kE4m3 ? k.scale : 1.f, j, (bad >> (j & 31) & 1) != 0);
+  };
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+  for (int j = 0; j < kAhead - 1; ++j) ask(j, buf[j]);
+  for (int i = 0; i < n; i += kAhead) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-        l[t][c] += fast_exp2(s[t][c] - m[t][c]) + fast_exp2(s[t][c + 2] - m[t][c]);
+    for (int j = 0; j < kAhead; ++j) {
+      if (i + j >= n) break;
+      ask(i + j + kAhead - 1, buf[(j + kAhead - 1) % kAhead]);
+      step(buf[j], i + j);
+    }
   }
-};
+}
 
-// The scores of pages [x, end) of the line, by one warp.
+// The query rows of a unit and what turns their scores into log2 units, for the
+// lane's two columns of each tile.
+template <int D, int KV, int NT>
+__device__ __forceinline__ void load_rows(const WeightsArgs& a, const Place& at, int rows, int lane,
+                                          Query<D, KV> (&q)[NT], float (&f)[NT][2]) {
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int r = 8 * t + (lane >> 2);
+    const int i = r / a.group, g = r - i * a.group;
+    const uint16_t* row = static_cast<const uint16_t*>(a.q) +
+        ((static_cast<int64_t>(at.b) * a.q_tokens + a.q_first + i) * a.Hq +
+         at.h * a.group + g) * D;
+    const float back = q[t].load(row, r < rows, lane) * a.scale_log2;
+    f[t][0] = __shfl_sync(0xffffffffu, back, (lane & 3) * 8);
+    f[t][1] = __shfl_sync(0xffffffffu, back, (lane & 3) * 8 + 4);
+  }
+}
+
+// Scores of tokens that a row does not attend become -inf: those from all_see +
+// (its query's number) on, and all of a skipped page.  Padding rows (q = 0) get
+// weight 0 in the second phase instead.
+template <int NT>
+__device__ __forceinline__ void mask(float (&s)[NT][4], int first, int all_see, bool skip, int group,
+                                     int lane) {
+  if (first + 16 <= all_see && !skip) return;
+  const int tok = first + (lane >> 2);
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int col = 8 * t + 2 * (lane & 3) + (j & 1);
+      if (skip || tok + (j & 2 ? 8 : 0) >= all_see + col / group) s[t][j] = -INFINITY;
+    }
+}
+
+// The logits of one warp's pages [start, end) of the line, and their statistics.
 template <int D, int KV, int NT, typename LogitsAt>
 __device__ __forceinline__ void score_pages(const WeightsArgs& a, const Work& ws, const int* cum,
-                                            int64_t x, int64_t end, int w, int lane, int rows,
-                                            const LogitsAt& logits_at) {
+                                            int64_t start, int64_t end, int w, int lane, int rows,
+                                            float* old_weights, const LogitsAt& logits_at) {
   constexpr int R = 8 * NT;
+  int64_t x = start;
   while (x < end) {
     const Place at = find(cum, a.B, a.Hkv, x);
     const int L = __ldg(a.context_lens + at.b);
     const int n = static_cast<int>(min(static_cast<int64_t>(at.pages - at.page), end - x));
-    const int32_t* table = a.block_tables + static_cast<int64_t>(at.b) * a.mbs + at.page;
-    // block ids, 32 pages at a time, one a lane; -1 outside the pool
-    auto ids_from = [&](int i) {
-      int id = i + lane < n ? __ldg(table + i + lane) : -1;
-      if (i + lane < n && (id < 0 || id >= a.num_blocks)) {
-        atomicOr(a.status, kStatusBadBlock);
-        id = -1;
-      }
-      return id;
-    };
-    int ids = ids_from(0);
-    auto id_of = [&](int i) { return __shfl_sync(0xffffffffu, ids, i & 31); };
-    Page<D, KV> buf[2];
-    int id0 = id_of(0), id1 = -1;
-    buf[0].load(a, max(id0, 0), at.h, lane);
     Query<D, KV> q[NT];
-    float f[NT][2];   // score -> log2 units, for the lane's columns
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int r = 8 * t + (lane >> 2);
-      const int i = r / a.group, g = r - i * a.group;
-      const uint16_t* row = static_cast<const uint16_t*>(a.q) +
-          ((static_cast<int64_t>(at.b) * a.q_tokens + a.q_first + i) * a.Hq +
-           at.h * a.group + g) * D;
-      const float back = q[t].load(row, r < rows, lane) * a.scale_log2;
-      f[t][0] = __shfl_sync(0xffffffffu, back, (lane & 3) * 8);
-      f[t][1] = __shfl_sync(0xffffffffu, back, (lane & 3) * 8 + 4);
-    }
-    // tokens from here on are not attended by some row; padding rows (q = 0)
-    // are left out by the finish launch
+    float f[NT][2];
+    load_rows<D, KV, NT>(a, at, rows, lane, q, f);
     const int all_see = L - a.q_tokens + a.q_first + 1;
-    Partition<NT> part;
+    const float* weights = a.weights + (static_cast<int64_t>(at.b) * a.Hkv + at.h) * a.stride;
+    const int old_end = a.decay != 0.f ? L - a.fresh : 0;   // tokens with an old weight
+    // the reference and the sum of the lane's columns over its own tokens
+    float m[NT][2], l[NT][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) part.m[t][c] = kNoScore, part.l[t][c] = 0.f;
-    auto step = [&](const Page<D, KV>& k, int id, int i) {
-      float s[NT][4];
-      page_scores<D, KV, NT>(s, k, q);
+      for (int c = 0; c < 2; ++c) m[t][c] = kNoScore, l[t][c] = 0.f;
+    auto take = [&](float (&s)[NT][4], float page_scale, int i, bool skip) {
+      const int first = (at.page + i) * 16;
+      if (x - start + i < Shape<NT>::kOld && lane < 16 && first + lane < old_end)
+        cp_async4(smem_u32(old_weights + (x - start + i) * 16 + lane), weights + first + lane);
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          s[t][j] *= Kind<KV>::kE4m3 ? f[t][j & 1] * k.scale : f[t][j & 1];
-      const int first = (at.page + i) * 16;
-      if (first + 16 > all_see || id < 0) {
-        const int tok = first + (lane >> 2);
+          s[t][j] *= Kind<KV>::kE4m3 ? f[t][j & 1] * page_scale : f[t][j & 1];
+      mask<NT>(s, first, all_see, skip, a.group, lane);
+      float* out = logits_at(x + i);
+      // The reference moves only when a score exceeds it by 2^8, so that few pages
+      // pay for a rescale; a sum of up to 2^8 a token is as exact as one of 1.
+      bool grow = false;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        if constexpr (NT == 4) {
+          *reinterpret_cast<float4*>(out + (t * 32 + lane) * 4) =
+              make_float4(s[t][0], s[t][1], s[t][2], s[t][3]);
+        } else {
+          *reinterpret_cast<float2*>(out + logit_at(t, lane >> 2, lane & 3)) =
+              make_float2(s[t][0], s[t][1]);
+          *reinterpret_cast<float2*>(out + logit_at(t, (lane >> 2) + 8, lane & 3)) =
+              make_float2(s[t][2], s[t][3]);
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) grow |= fmaxf(s[t][c], s[t][c + 2]) > m[t][c] + 8.f;
+      }
+      if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int col = 8 * t + 2 * (lane & 3) + (j & 1);
-            if (id < 0 || tok + (j & 2 ? 8 : 0) >= all_see + col / a.group) s[t][j] = -INFINITY;
+          for (int c = 0; c < 2; ++c) {
+            const float top = fmaxf(m[t][c], fmaxf(s[t][c], s[t][c + 2]));
+            l[t][c] *= fast_exp2(m[t][c] - top);
+            m[t][c] = top;
           }
       }
-      part.take(s, logits_at(x + i));
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          l[t][c] += fast_exp2(s[t][c] - m[t][c]) + fast_exp2(s[t][c + 2] - m[t][c]);
     };
-    for (int i = 0; i < n; i += 2) {
-      if (i + 1 < n) {
-        id1 = id_of(i + 1);
-        buf[1].load(a, max(id1, 0), at.h, lane);
-      }
-      step(buf[0], id0, i);
-      if (i + 1 >= n) break;
-      if (i + 2 < n) {
-        if (((i + 2) & 31) == 0) ids = ids_from(i + 2);
-        id0 = id_of(i + 2);
-        buf[0].load(a, max(id0, 0), at.h, lane);
-      }
-      step(buf[1], id1, i + 1);
-    }
+    for_pages<D, KV, NT>(a, at, n, lane, q, take);
     // the partition's statistics: over the 8 lanes that hold the same columns
     const int64_t index = static_cast<int64_t>(at.b) * a.Hkv + at.h + w;
 #pragma unroll
@@ -411,13 +526,117 @@ __device__ __forceinline__ void score_pages(const WeightsArgs& a, const Work& ws
       for (int c = 0; c < 2; ++c)
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1)
-          stat_join(part.m[t][c], part.l[t][c], __shfl_xor_sync(0xffffffffu, part.m[t][c], o),
-                    __shfl_xor_sync(0xffffffffu, part.l[t][c], o));
+          stat_join(m[t][c], l[t][c], __shfl_xor_sync(0xffffffffu, m[t][c], o),
+                    __shfl_xor_sync(0xffffffffu, l[t][c], o));
       if (lane < 4)
         *reinterpret_cast<float4*>(ws.stats + index * R + 8 * t + 2 * lane) =
-            make_float4(part.m[t][0], part.l[t][0], part.m[t][1], part.l[t][1]);
+            make_float4(m[t][0], l[t][0], m[t][1], l[t][1]);
     }
     x += n;
+  }
+}
+
+// The weights of one segment from its logits: pages [x0, x0 + n) of the line, from
+// page `first` on of the unit.  st: reference and 1 / sum of row lane % R.  From
+// the end (the logits written last are the likeliest in L2), a few pages at a
+// time, whose logits are asked for together.
+template <int NT, typename LogitsAt>
+__device__ __forceinline__ void finish_pages(const WeightsArgs& a, float* weights, int L, int first,
+                                             int n, int64_t x0, int64_t start, float2 st, int lane,
+                                             const float* old_weights, const LogitsAt& logits_at) {
+  const int old_end = a.decay != 0.f ? L - a.fresh : 0;
+  auto old_of = [&](int page, int in_page) {
+    return x0 + page - start < Shape<NT>::kOld ? old_weights[(x0 + page - start) * 16 + in_page]
+                                               : weights[(first + page) * 16 + in_page];
+  };
+  // a token a lane, two pages a step
+  constexpr int R = 8 * NT;
+  constexpr int kGroup = NT == 1 ? 4 : 2;
+  F2 minus_top[R / 2], f[R / 2];
+#pragma unroll
+  for (int i = 0; i < R / 2; ++i) {
+    minus_top[i] = pack(-__shfl_sync(0xffffffffu, st.x, 2 * i), -__shfl_sync(0xffffffffu, st.x, 2 * i + 1));
+    f[i] = pack(__shfl_sync(0xffffffffu, st.y, 2 * i), __shfl_sync(0xffffffffu, st.y, 2 * i + 1));
+  }
+  for (int i = (n - 1) / 2; i >= 0; i -= kGroup) {
+    float4 s[kGroup][2 * NT];
+    float old[kGroup];
+#pragma unroll
+    for (int j = 0; j < kGroup; ++j) {
+      const int page = 2 * (i - j) + (lane >> 4);
+      old[j] = 0.f;
+      if (i - j >= 0 && page < n) {
+        const float* in = logits_at(x0 + page);
+#pragma unroll
+        for (int h = 0; h < 2 * NT; ++h)
+          s[j][h] = *reinterpret_cast<const float4*>(in + logit_at(h / 2, lane & 15, h % 2 * 2));
+        if ((first + page) * 16 + (lane & 15) < old_end) old[j] = old_of(page, lane & 15);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kGroup; ++j) {
+      const int page = 2 * (i - j) + (lane >> 4);
+      const int tok = (first + page) * 16 + (lane & 15);
+      if (i - j < 0 || page >= n || tok >= L) continue;
+      F2 sum = pack(0.f, 0.f);
+#pragma unroll
+      for (int h = 0; h < 2 * NT; ++h) {
+        sum = fma2(exp2_2(pack(s[j][h].x, s[j][h].y) + minus_top[2 * h]), f[2 * h], sum);
+        sum = fma2(exp2_2(pack(s[j][h].z, s[j][h].w) + minus_top[2 * h + 1]), f[2 * h + 1], sum);
+      }
+      weights[tok] = a.decay * old[j] + (unpack(sum).x + unpack(sum).y);
+    }
+  }
+}
+
+// 32 rows: from the fragments, a lane's two columns of each tile and a quad's sum.
+template <typename LogitsAt>
+__device__ __forceinline__ void finish_pages4(const WeightsArgs& a, float* weights, int L, int first,
+                                              int n, int64_t x0, int64_t start, float2 st, int lane,
+                                              const float* old_weights, const LogitsAt& logits_at) {
+  const int old_end = a.decay != 0.f ? L - a.fresh : 0;
+  constexpr int kGroup = 3;
+  F2 minus_top[4], f[4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const int r = 8 * t + 2 * (lane & 3);
+    minus_top[t] = pack(-__shfl_sync(0xffffffffu, st.x, r), -__shfl_sync(0xffffffffu, st.x, r + 1));
+    f[t] = pack(__shfl_sync(0xffffffffu, st.y, r), __shfl_sync(0xffffffffu, st.y, r + 1));
+  }
+  const int in_page = (lane >> 2) + (lane & 1) * 8;   // the token whose sum the lane will hold
+  for (int i = n - 1; i >= 0; i -= kGroup) {
+    float4 s[kGroup][4];
+    float old[kGroup];
+#pragma unroll
+    for (int j = 0; j < kGroup; ++j) {
+      old[j] = 0.f;
+      if (i - j < 0) continue;
+      const float4* in = reinterpret_cast<const float4*>(logits_at(x0 + i - j)) + lane;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) s[j][t] = in[t * 32];
+      if ((lane & 2) == 0 && (first + i - j) * 16 + in_page < old_end)
+        old[j] = x0 + i - j - start < Shape<4>::kOld
+                     ? old_weights[(x0 + i - j - start) * 16 + in_page]
+                     : weights[(first + i - j) * 16 + in_page];
+    }
+#pragma unroll
+    for (int j = 0; j < kGroup; ++j) {
+      if (i - j < 0) break;
+      F2 lo = pack(0.f, 0.f), hi = lo;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        lo = fma2(exp2_2(pack(s[j][t].x, s[j][t].y) + minus_top[t]), f[t], lo);
+        hi = fma2(exp2_2(pack(s[j][t].z, s[j][t].w) + minus_top[t]), f[t], hi);
+      }
+      float x = unpack(lo).x + unpack(lo).y, y = unpack(hi).x + unpack(hi).y;
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) {
+        x += __shfl_xor_sync(0xffffffffu, x, o);
+        y += __shfl_xor_sync(0xffffffffu, y, o);
+      }
+      const int tok = (first + i - j) * 16 + in_page;
+      if ((lane & 2) == 0 && tok < L) weights[tok] = a.decay * old[j] + (lane & 1 ? y : x);
+    }
   }
 }
 
@@ -446,39 +665,39 @@ weights_kernel(const __grid_constant__ WeightsArgs a, Work ws) {
   using S = Shape<NT>;
   constexpr int R = 8 * NT;
   constexpr int kThreads = S::kWarps * 32;
-  extern __shared__ float4 kept_logits[];
+  extern __shared__ __align__(16) uint8_t warp_smem[];
   __shared__ int cum[kPrefix];
   __shared__ int warp_sums[S::kWarps];
   __shared__ float2 joined[2][R];
   __shared__ float2 scratch[kThreads];
-  __shared__ bool passed;
   const int tid = threadIdx.x, lane = tid & 31;
   const int w_first = blockIdx.x * S::kWarps, w = w_first + (tid >> 5);
+  const uint32_t call = ld_relaxed_b32(ws.sync + 1) + 1;   // changed only when all CTAs are done
   prefix_pages<S::kWarps>(a, cum, warp_sums);
   const Line line = make_line(a, cum, static_cast<int>(gridDim.x) * S::kWarps);
   if (w_first >= line.workers) return;   // the whole CTA
+  const int w_last = min(w_first + S::kWarps, line.workers);
   const int rows = a.n_q * a.group;
   const int64_t start = part_start(line, min(w, line.workers));
   const int64_t end = part_start(line, min(w + 1, line.workers));
+  uint8_t* mine = warp_smem + (tid >> 5) * S::kWarpBytes;
+  float* kept = reinterpret_cast<float*>(mine);
+  float* old_weights = reinterpret_cast<float*>(mine + S::kKept * S::kPage * 16);
   // the logits of page x: of the warp's first kKept in shared memory
-  float4* kept = kept_logits + (tid >> 5) * (S::kKept * S::kPage) + lane;
   auto logits_at = [&](int64_t x) {
-    return x - start < S::kKept ? kept + (x - start) * S::kPage : ws.logits + x * S::kPage + lane;
+    return x - start < S::kKept ? kept + (x - start) * (S::kPage * 4) : ws.logits + x * (S::kPage * 4);
   };
-  score_pages<D, KV, NT>(a, ws, cum, start, end, w, lane, rows, logits_at);
+  score_pages<D, KV, NT>(a, ws, cum, start, end, w, lane, rows, old_weights, logits_at);
+  __threadfence();
+  __syncwarp();
+  if (lane == 0 && w < line.workers) st_release_gpu_b32(ws.sync + 2 + w, call);
+  cp_async_wait_all();   // the old weights, each lane's own copies
+  __syncwarp();
 
-  // ---- all statistics are written
-  __syncthreads();
-  const uint32_t ctas = static_cast<uint32_t>((line.workers + S::kWarps - 1) / S::kWarps);
-  if (ctas > 1) {
-    if (tid == 0) passed = grid_barrier(ws.barrier, ctas, a.status, a.wait_limit_ns);
-    __syncthreads();
-    if (!passed) return;
-  }
   // units of many partitions are joined by the whole CTA
   int long_unit[2] = {-1, -1};
+  bool ok = true;
   {
-    const int w_last = min(w_first + S::kWarps, line.workers);
     const int64_t ends[2] = {part_start(line, w_first), part_start(line, w_last) - 1};
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -489,6 +708,9 @@ weights_kernel(const __grid_constant__ WeightsArgs a, Work ws) {
       const int n = part_of(line, at.unit_start + at.pages - 1) - w0 + 1;
       if (n <= kWarpJoin) continue;
       long_unit[e] = unit;
+      ok = await_warps(ws, w0, n, call, tid, kThreads, a.status, a.wait_limit_ns);
+      ok = __syncthreads_and(ok);
+      if (!ok) break;
       const float2* st = ws.stats + (static_cast<int64_t>(unit) + w0) * R;
       float m = kNoScore, l = 0.f;
       for (int i = tid; i < n * R; i += kThreads) {
@@ -504,7 +726,7 @@ weights_kernel(const __grid_constant__ WeightsArgs a, Work ws) {
       __syncthreads();
     }
   }
-  int64_t x = end;
+  int64_t x = ok ? end : start;
   while (x > start) {   // from the end: the logits written last are the likeliest in L2
     const Place at = find(cum, a.B, a.Hkv, x - 1);
     const int L = __ldg(a.context_lens + at.b);
@@ -517,55 +739,33 @@ weights_kernel(const __grid_constant__ WeightsArgs a, Work ws) {
       st = joined[1][lane % R];
     } else {
       const int w0 = part_of(line, at.unit_start);
-      st = join_by_warp<R>(ws.stats + (static_cast<int64_t>(unit) + w0) * R,
-                           part_of(line, at.unit_start + at.pages - 1) - w0 + 1, lane);
+      const int parts = part_of(line, at.unit_start + at.pages - 1) - w0 + 1;
+      const bool there = await_warps(ws, w0, parts, call, lane, 32, a.status, a.wait_limit_ns);
+      if (!__all_sync(0xffffffffu, there)) break;
+      st = join_by_warp<R>(ws.stats + (static_cast<int64_t>(unit) + w0) * R, parts, lane);
     }
     // an empty row's and a padding row's tokens get 0
-    const float inv = lane % R < rows && (st.y > 0.f || st.y != st.y) ? 1.f / st.y : 0.f;
-    float top[NT][2], f[NT][2];
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int r = 8 * t + 2 * (lane & 3) + c;
-        top[t][c] = __shfl_sync(0xffffffffu, st.x, r);
-        f[t][c] = __shfl_sync(0xffffffffu, inv, r);
-      }
+    st.y = lane % R < rows && (st.y > 0.f || st.y != st.y) ? 1.f / st.y : 0.f;
     float* weights = a.weights + static_cast<int64_t>(unit) * a.stride;
-    // a few pages at a time: their old weights and logits are asked for together
-    constexpr int kGroup = NT == 4 ? 2 : 4;
-    for (int i = 0; i < n; i += kGroup) {
-      float4 s[kGroup][NT];
-      float old[kGroup];
-#pragma unroll
-      for (int j = 0; j < kGroup; ++j) {
-        old[j] = 0.f;
-        if (i + j >= n) continue;
-        const int tok = (at.page - i - j) * 16 + (lane >> 2) + (lane & 1) * 8;
-        if ((lane & 2) == 0 && a.decay != 0.f && tok < L - a.fresh) old[j] = weights[tok];
-        const float4* in = logits_at(x - 1 - i - j);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) s[j][t] = in[t * 32];
-      }
-#pragma unroll
-      for (int j = 0; j < kGroup; ++j) {
-        if (i + j >= n) break;
-        const int tok = (at.page - i - j) * 16 + (lane >> 2) + (lane & 1) * 8;
-        float lo = 0.f, hi = 0.f;
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          lo += fast_exp2(s[j][t].x - top[t][0]) * f[t][0] + fast_exp2(s[j][t].y - top[t][1]) * f[t][1];
-          hi += fast_exp2(s[j][t].z - top[t][0]) * f[t][0] + fast_exp2(s[j][t].w - top[t][1]) * f[t][1];
-        }
-#pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-          lo += __shfl_xor_sync(0xffffffffu, lo, o);
-          hi += __shfl_xor_sync(0xffffffffu, hi, o);
-        }
-        if ((lane & 2) == 0 && tok < L) weights[tok] = a.decay * old[j] + (lane & 1 ? hi : lo);
-      }
-    }
+    if constexpr (NT == 4)
+      finish_pages4(a, weights, L, at.page - n + 1, n, x - n, start, st, lane, old_weights, logits_at);
+    else
+      finish_pages<NT>(a, weights, L, at.page - n + 1, n, x - n, start, st, lane, old_weights,
+                       logits_at);
     x -= n;
+  }
+  // the last CTA closes the call
+  __syncthreads();
+  if (tid == 0) {
+    const uint32_t ctas = static_cast<uint32_t>((line.workers + S::kWarps - 1) / S::kWarps);
+    __threadfence();
+    const uint32_t done = atomicAdd(ws.sync, 1u);
+    if (done == ctas - 1) {
+      atomicExch(ws.sync, 0u);
+      atomicExch(ws.sync + 1, call);
+    } else if (done >= ctas) {
+      atomicOr(a.status, kStatusWsDirty);   // a count that no call leaves
+    }
   }
 }
 
@@ -619,6 +819,9 @@ cudaError_t launch_pass(const WeightsArgs& a, int nt, const Work& ws, cudaStream
                                                               : launch_tiles<D, KV, 4>(a, ws, s);
 }
 
+// The words at the start of a workspace: the same ones for every call.
+size_t sync_bytes() { return align256((2 + 2 * device_sm_count() * kMaxWarps) * sizeof(uint32_t)); }
+
 }  // namespace
 
 size_t weights_workspace_bytes(int B, int Hkv, int max_context_len, int rows) {
@@ -627,7 +830,7 @@ size_t weights_workspace_bytes(int B, int Hkv, int max_context_len, int rows) {
   const size_t units = static_cast<size_t>(B) * Hkv;
   const size_t pages = units * ((static_cast<size_t>(max_context_len) + 15) / 16);
   const size_t parts = units + static_cast<size_t>(2 * device_sm_count()) * kMaxWarps;
-  return kBarrierBytes + align256(pages * nt * 32 * sizeof(float4)) +
+  return sync_bytes() + align256(pages * nt * 32 * sizeof(float4)) +
          align256(parts * nt * 8 * sizeof(float2));
 }
 
@@ -652,9 +855,9 @@ cudaError_t launch_weights(const WeightsArgs& a0, bool fp8, bool bf16, cudaStrea
       const size_t pages = static_cast<size_t>(a.B) * a.Hkv * ((static_cast<size_t>(a.max_context_len) + 15) / 16);
       Work ws;
       uint8_t* base = static_cast<uint8_t*>(a.workspace);
-      ws.barrier = reinterpret_cast<uint32_t*>(base);
-      base += kBarrierBytes;
-      ws.logits = reinterpret_cast<float4*>(base);
+      ws.sync = reinterpret_cast<uint32_t*>(base);
+      base += sync_bytes();
+      ws.logits = reinterpret_cast<float*>(base);
       ws.stats = reinterpret_cast<float2*>(base + align256(pages * nt * 32 * sizeof(float4)));
       const int kv = (fp8 ? 2 : 0) + (bf16 ? 1 : 0);
       cudaError_t e;

@@ -211,8 +211,9 @@ def run_weights(q, kc, ks, bt, lens, w, scale, decay, fresh, max_len=None, ws=No
     mx = bt.shape[1] * 16 if max_len is None else max_len
     n = _abi.pa_attention_weights_workspace_size(B, Hq, Hkv, mx, n_q)
     if ws is None:
-        ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")   # NaN everywhere
-        ws[:256] = 0                                                   # but for the barrier
+        ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+        ws[n // 2:] = 255          # what another call may leave in the scores and statistics
+        ws[:1 << 16] = 0
     wd = w.cuda()
     args = (bt.cuda(), lens.cuda(), mx, scale, ws)
     if ks is None:
@@ -313,7 +314,8 @@ def test_attention_weights_bad_indexes_are_skipped_and_reported():
 def test_attention_weights_reports_a_workspace_that_was_not_cleared():
     q, kc, ks, bt, L, w = weights_case([640, 3], 4, 2, 64, 1, "16", F16, 14)
     n = _abi.pa_attention_weights_workspace_size(2, 4, 2, bt.shape[1] * 16, 1)
-    ws = torch.full((n,), 0x7f, dtype=torch.uint8, device="cuda")
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    ws[:4] = 0x7f
     run_weights(q, kc, ks, bt, L, w, .125, 0., 0, ws=ws)
     assert _abi.pa_get_status() == (_abi.PA_ERR_WORKSPACE, _abi.PA_STATUS_WS_DIRTY)
     ws.zero_()
