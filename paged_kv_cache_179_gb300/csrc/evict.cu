@@ -19,6 +19,32 @@
 namespace pa {
 namespace {
 
+// ------------------------------------------------------------------- clusters
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// All threads of the cluster; shared memory written before it is seen after it.
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n"
+               "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The word that p (in this CTA's shared memory) is in CTA `rank`'s.
+__device__ __forceinline__ int ld_cluster(const int* p, uint32_t rank) {
+  uint32_t at;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+
 // Larger weight, larger key; NaN the lowest; -0 as 0.
 __device__ __forceinline__ uint32_t weight_key(float w) {
   if (w != w) return 0u;
@@ -37,28 +63,27 @@ __device__ __forceinline__ int checked_len(const EvictArgs& a, int b, bool repor
 }
 
 // ------------------------------------------------------------------- select
-// One CTA per (kv head, sequence).  A warp owns a contiguous part of the
-// candidates, so that positions come out in order with one scan over the warps'
-// counts and ballots inside each.  The keys of the first kKeys candidates stay in
-// shared memory (those behind them are read again, from L2).
+// One cluster of CTAs per (kv head, sequence): each takes a contiguous part of the
+// candidates, each warp of it a contiguous part of that, so that positions come
+// out in order with scans over the parts' counts and ballots inside a warp.  A
+// part of up to kKeys candidates stays in the threads' registers (ONE); longer
+// ones are read again, from L2, in every step.
 //
 // Radix selection in digits of 11, 11 and 10 bits.  The first digit's histogram
 // sees every key, and the weights' few exponents would make the lanes of a warp
-// add to the same few bins: kCopies copies, one for every kCopies-th lane.  What
-// falls into the chosen bin is then gathered into a list, on which the other
-// digits work (on all keys again, if the list does not hold them).
-template <int THREADS>
-struct Select {
-  static constexpr int kWarps = THREADS / 32;
-  static constexpr int kKeys = THREADS * 32;
-  static constexpr int kCopies = THREADS == 1024 ? 8 : 4;
-  static constexpr int kBins = 2048;
-  static constexpr int kList = (kCopies - 1) * kBins;   // in the other copies' place
-  static constexpr int kSmem = (kKeys + kCopies * kBins) * 4;
-};
+// add to the same few bins: four copies, one for every fourth lane.  The CTAs'
+// histograms are joined through distributed shared memory; every CTA does the
+// whole search for itself.
+constexpr int kSelectThreads = 512;
+constexpr int kSelectWarps = kSelectThreads / 32;
+constexpr int kPer = 16;                                 // keys a thread
+constexpr int kKeys = kSelectThreads * kPer;             // a CTA
+constexpr int kMaxSelectCluster = 8;
+constexpr int kBins = 2048;
+constexpr int kCopies = 4;
+constexpr int kSelectSmem = (kCopies + 3) * kBins * 4;   // the copies, and each digit's histogram
 
 // Exclusive sum of v over the CTA's threads.
-template <int WARPS>
 __device__ __forceinline__ int block_scan(int v, int* warp_sums) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int s = v;
@@ -69,33 +94,33 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums) {
   }
   if (lane == 31) warp_sums[warp] = s;
   __syncthreads();
-  int before = 0;
-#pragma unroll
-  for (int w = 0; w < WARPS; ++w) before += w < warp ? warp_sums[w] : 0;
+  int before = lane < warp ? warp_sums[lane & (kSelectWarps - 1)] : 0;
+  before = __reduce_add_sync(0xffffffffu, before);
   __syncthreads();
   return before + s - v;
 }
 
-template <int THREADS>
-__global__ void __launch_bounds__(THREADS) evict_select_kernel(const __grid_constant__ EvictArgs a) {
-  using S = Select<THREADS>;
-  extern __shared__ uint32_t smem[];
-  uint32_t* keys = smem;
-  int* hist = reinterpret_cast<int*>(smem + S::kKeys);
-  uint32_t* list = smem + S::kKeys + S::kBins;
-  __shared__ int warp_sums[S::kWarps];
-  __shared__ int warp_gt[S::kWarps], warp_eq[S::kWarps];
-  __shared__ int s_bin, s_left, s_count, s_listed;
+template <bool ONE>
+__global__ void __launch_bounds__(kSelectThreads, 2)
+evict_select_kernel(const __grid_constant__ EvictArgs a) {
+  extern __shared__ int smem[];
+  int* copies = smem;                    // [bin][copy]
+  int* hist = smem + kCopies * kBins;    // [digit][bin], of this CTA
+  __shared__ int warp_sums[kSelectWarps];
+  __shared__ int warp_gt[kSelectWarps], warp_eq[kSelectWarps];
+  __shared__ int cta_gt, cta_eq, s_bin, s_left;
   griddep_launch_dependents();   // the move may do its prologue
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int h = blockIdx.x, b = blockIdx.y;
-  const int L = checked_len(a, b, h == 0 && tid == 0);
+  const int rank = static_cast<int>(cluster_rank()), size = static_cast<int>(cluster_size());
+  const int h = blockIdx.x / size, b = blockIdx.y;
+  const int L = checked_len(a, b, h == 0 && rank == 0 && tid == 0);
   const int64_t unit = static_cast<int64_t>(b) * a.Hkv + h;
   const bool cut = L > a.keep;
+  const int tid_all = rank * kSelectThreads + tid, threads_all = size * kSelectThreads;
   if (h == 0) {
-    if (tid == 0) a.new_lens[b] = cut ? a.keep : L;
+    if (tid_all == 0) a.new_lens[b] = cut ? a.keep : L;
     if (a.tables_out != nullptr)
-      for (int i = tid; i < a.spare_blocks; i += THREADS)
+      for (int i = tid_all; i < a.spare_blocks; i += threads_all)
         a.tables_out[static_cast<int64_t>(b) * a.spare_blocks + i] =
             cut ? a.spare[static_cast<int64_t>(b) * a.spare_blocks + i]
                 : i < a.mbs ? a.block_tables[static_cast<int64_t>(b) * a.mbs + i] : -1;
@@ -105,127 +130,121 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const __grid_cons
   int32_t* kept = a.kept + unit * a.keep;
   // the protected ends, or, uncut, everything
   const int head = cut ? a.first : L, tail = cut ? a.recent : 0;
-  for (int i = tid; i < head + tail; i += THREADS) {
+  for (int i = tid_all; i < head + tail; i += threads_all) {
     const int t = i < head ? i : L - tail + (i - head);
     const int pos = i < head ? i : a.keep - tail + (i - head);
     kept[pos] = t;
     if (w_out != nullptr) w_out[pos] = w[t];
   }
   const int k = a.keep - a.first - a.recent;   // how many of the m candidates stay; k < m
-  if (!cut || k == 0) return;
+  if (!cut || k == 0) return;                  // the whole cluster
   const int m = L - a.first - a.recent;
   const float* cand = w + a.first;
-  const int part = ((m + S::kWarps - 1) / S::kWarps + 31) / 32 * 32;
-  const int lo = min(warp * part, m), hi = min(lo + part, m);
-  for (int i = tid; i < S::kCopies * S::kBins; i += THREADS) hist[i] = 0;
-  if (tid == 0) s_listed = 0;
-  __syncthreads();
-  // ---- the first digit, and the keys into shared memory
-  for (int i0 = lo; i0 < hi; i0 += 8 * 32) {
-    float v[8];
+  const int share = ((m + size - 1) / size + 31) / 32 * 32;
+  const int cta_lo = static_cast<int>(min(static_cast<int64_t>(rank) * share, static_cast<int64_t>(m)));
+  const int cta_hi = min(cta_lo + share, m);
+  const int part = ((cta_hi - cta_lo + kSelectWarps - 1) / kSelectWarps + 31) / 32 * 32;
+  const int lo = min(cta_lo + warp * part, cta_hi), hi = min(lo + part, cta_hi);
+
+  uint32_t key[kPer];
+  auto load = [&](int i0) {   // the keys of candidates i0 + 32 j + lane
+    float v[kPer];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = i0 + j * 32 + lane < hi ? __ldg(cand + i0 + j * 32 + lane) : 0.f;
+    for (int j = 0; j < kPer; ++j) v[j] = i0 + 32 * j + lane < hi ? __ldg(cand + i0 + 32 * j + lane) : 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int i = i0 + j * 32 + lane;
-      if (i < hi) {
-        const uint32_t key = weight_key(v[j]);
-        if (i < S::kKeys) keys[i] = key;
-        atomicAdd(&hist[(key >> 21) * S::kCopies + (lane & (S::kCopies - 1))], 1);
+    for (int j = 0; j < kPer; ++j) key[j] = weight_key(v[j]);
+  };
+  // f(key, candidate, whether it is one), warp by warp in order
+  auto for_keys = [&](auto f) {
+    if constexpr (ONE) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) f(key[j], lo + 32 * j + lane, lo + 32 * j + lane < hi);
+    } else {
+      for (int i0 = lo; i0 < hi; i0 += 32 * kPer) {
+        load(i0);
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) f(key[j], i0 + 32 * j + lane, i0 + 32 * j + lane < hi);
       }
     }
-  }
+  };
+  if constexpr (ONE) load(lo);
+  for (int i = tid; i < (kCopies + 3) * kBins; i += kSelectThreads) smem[i] = 0;
   __syncthreads();
-  auto key_at = [&](int i) { return i < S::kKeys ? keys[i] : weight_key(__ldg(cand + i)); };
-  // Finds the bin, from the largest down, in which the left-th key lies.
-  int left = k;
-  auto find_bin = [&](int bins, int copies) {
-    const int each = bins / THREADS > 0 ? bins / THREADS : 1;
-    int c[S::kBins / THREADS > 0 ? S::kBins / THREADS : 1];
-    int sum = 0;
+  uint32_t prefix = 0;   // the k-th largest key's digits so far
+  int left = k;          // how many of the keys with that prefix stay
 #pragma unroll
-    for (int j = 0; j < S::kBins / THREADS; ++j) {
+  for (int digit = 0; digit < 3; ++digit) {
+    const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0;
+    const int bins = digit == 2 ? 1024 : 2048;
+    int* mine = hist + digit * kBins;
+    if (digit == 0) {
+      for_keys([&](uint32_t x, int, bool in) {
+        if (in) atomicAdd(&copies[(x >> 21) * kCopies + (lane & (kCopies - 1))], 1);
+      });
+      __syncthreads();
+      for (int i = tid; i < kBins; i += kSelectThreads) {
+        const int4 c = reinterpret_cast<const int4*>(copies)[i];
+        mine[i] = c.x + c.y + c.z + c.w;
+      }
+    } else {
+      const uint32_t mask = digit == 1 ? 0xffe00000u : 0xfffffc00u;
+      for_keys([&](uint32_t x, int, bool in) {
+        if (in && (x & mask) == prefix) atomicAdd(&mine[(x >> shift) & (bins - 1)], 1);
+      });
+    }
+    if (size > 1) cluster_sync();
+    else __syncthreads();
+    // the bin, from the largest down, in which the left-th key lies
+    constexpr int kEach = kBins / kSelectThreads;
+    int c[kEach], sum = 0;
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      const int bin = bins - 1 - (tid * kEach + j);
       c[j] = 0;
-      const int bin = bins - 1 - (tid * each + j);
-      if (j < each && bin >= 0)
-        for (int x = 0; x < copies; ++x) c[j] += hist[bin * copies + x];
+      if (bin >= 0)
+        for (int r = 0; r < size; ++r) c[j] += ld_cluster(mine + bin, r);
       sum += c[j];
     }
-    int above = block_scan<S::kWarps>(sum, warp_sums);
-    if (above < left && above + sum >= left) {
+    int over = block_scan(sum, warp_sums);
+    if (over < left && over + sum >= left) {
 #pragma unroll
-      for (int j = 0; j < S::kBins / THREADS; ++j) {
-        if (above < left && above + c[j] >= left) {
-          s_bin = bins - 1 - (tid * each + j);
-          s_left = left - above;
-          s_count = c[j];
+      for (int j = 0; j < kEach; ++j) {
+        if (over < left && over + c[j] >= left) {
+          s_bin = bins - 1 - (tid * kEach + j);
+          s_left = left - over;
         }
-        above += c[j];
+        over += c[j];
       }
     }
     __syncthreads();
-    left = s_left;
-  };
-  find_bin(S::kBins, S::kCopies);
-  uint32_t prefix = static_cast<uint32_t>(s_bin) << 21;
-  const int count = s_count;
-  const bool listed = count <= S::kList;
-  __syncthreads();
-  // ---- the other digits, on the keys of that bin
-  if (listed) {
-    for (int i = lo + lane; i - lane < hi; i += 32) {
-      const uint32_t key = i < hi ? key_at(i) : 0u;
-      const bool in = i < hi && (key >> 21) == (prefix >> 21);
-      const unsigned mask = __ballot_sync(0xffffffffu, in);
-      if (mask == 0) continue;
-      int at = 0;
-      if (lane == 0) at = atomicAdd(&s_listed, __popc(mask));
-      at = __shfl_sync(0xffffffffu, at, 0) + __popc(mask & ((1u << lane) - 1));
-      if (in) list[at] = key;
-    }
-  }
-#pragma unroll
-  for (int digit = 0; digit < 2; ++digit) {
-    const int shift = digit == 0 ? 10 : 0, bins = digit == 0 ? 2048 : 1024;
-    for (int i = tid; i < S::kBins; i += THREADS) hist[i] = 0;
-    __syncthreads();
-    const uint32_t mask = digit == 0 ? 0xffe00000u : 0xfffffc00u;
-    if (listed) {
-      for (int i = tid; i < count; i += THREADS)
-        if ((list[i] & mask) == prefix) atomicAdd(&hist[(list[i] >> shift) & (bins - 1)], 1);
-    } else {
-      for (int i = lo + lane; i < hi; i += 32) {
-        const uint32_t key = key_at(i);
-        if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & (bins - 1)], 1);
-      }
-    }
-    __syncthreads();
-    find_bin(bins, 1);
     prefix |= static_cast<uint32_t>(s_bin) << shift;
+    left = s_left;
     __syncthreads();
   }
-  // ---- every warp's larger keys and ties, then the positions in order
+  // every part's larger keys and ties, then the positions in order
   int gt = 0, eq = 0;
-  for (int i = lo + lane; i < hi; i += 32) {
-    const uint32_t key = key_at(i);
-    gt += key > prefix;
-    eq += key == prefix;
-  }
+  for_keys([&](uint32_t x, int, bool in) {
+    gt += in && x > prefix;
+    eq += in && x == prefix;
+  });
   gt = __reduce_add_sync(0xffffffffu, gt);
   eq = __reduce_add_sync(0xffffffffu, eq);
   if (lane == 0) warp_gt[warp] = gt, warp_eq[warp] = eq;
   __syncthreads();
-  int gt_before = lane < warp && lane < S::kWarps ? warp_gt[lane] : 0;
-  int ties = lane < warp && lane < S::kWarps ? warp_eq[lane] : 0;
-  gt_before = __reduce_add_sync(0xffffffffu, gt_before);
+  int pos = lane < warp ? warp_gt[lane & (kSelectWarps - 1)] : 0;
+  int ties = lane < warp ? warp_eq[lane & (kSelectWarps - 1)] : 0;
+  pos = __reduce_add_sync(0xffffffffu, pos);
   ties = __reduce_add_sync(0xffffffffu, ties);
-  int pos = a.first + gt_before + min(ties, left);
+  if (size > 1) {
+    if (tid == kSelectThreads - 1) cta_gt = pos + gt, cta_eq = ties + eq;
+    cluster_sync();
+    for (int r = 0; r < rank; ++r) pos += ld_cluster(&cta_gt, r), ties += ld_cluster(&cta_eq, r);
+  }
+  pos += a.first + min(ties, left);
   const unsigned below = (1u << lane) - 1;
-  for (int i = lo + lane; i - lane < hi; i += 32) {
-    const uint32_t key = i < hi ? key_at(i) : 0u;
-    const unsigned tied = __ballot_sync(0xffffffffu, i < hi && key == prefix);
-    const bool stay = i < hi && (key > prefix ||
-                                 (key == prefix && ties + __popc(tied & below) < left));
+  for_keys([&](uint32_t x, int i, bool in) {
+    const unsigned tied = __ballot_sync(0xffffffffu, in && x == prefix);
+    const bool stay = in && (x > prefix || (x == prefix && ties + __popc(tied & below) < left));
     const unsigned staying = __ballot_sync(0xffffffffu, stay);
     if (stay) {
       const int at = pos + __popc(staying & below);
@@ -234,7 +253,8 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const __grid_cons
     }
     pos += __popc(staying);
     ties += __popc(tied);
-  }
+  });
+  if (size > 1) cluster_sync();   // nobody's shared memory is read any more
 }
 
 // --------------------------------------------------------------------- move
@@ -296,30 +316,32 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
   }
 }
 
-// E4M3 codes of x / scale, the quotient rounded to fp32 as the division rounds it,
-// without dividing: x * (1 / scale) is within two steps of it, and where that is
-// not near a border between two codes (the 20 bits of the significand that a code
-// drops stand at their half), the code is the same.  Near one, and below the
-// smallest normal code, it does divide.
-struct Encoder {
-  float scale, inv;
-  bool divide;   // the reciprocal itself would leave fp32's normal range
-  static __device__ __forceinline__ Encoder of(float s) {
-    return Encoder{s, __fdiv_rn(1.f, s), !(s > 0x1p-100f && s < 0x1p100f)};
-  }
-  __device__ __forceinline__ uint32_t operator()(float x, float y) const {
-    const float p = __fmul_rn(x, inv), q = __fmul_rn(y, inv);
-    if (divide || doubtful(p) || doubtful(q))
-      return f32x2_to_e4m3x2(__fdiv_rn(x, scale), __fdiv_rn(y, scale));
-    return f32x2_to_e4m3x2(p, q);
-  }
-  static __device__ __forceinline__ bool doubtful(float q) {
-    const uint32_t b = __float_as_uint(q);
-    const bool border = (b + 4u - 0x80000u) * 4096u <= 8u * 4096u;
-    const bool small = (b & 0x7fffffffu) - 1u < 0x3c800000u - 1u;   // 0 < |q| < 2^-6
-    return border || small;
-  }
-};
+// Four E4M3 codes c of a row with page scale s become codes under page scale S:
+// E4M3(fl(fl(c s) / S)), both roundings to fp32, without dividing.  That quotient
+// is within 2^-23 of c s / S, and c r with r = fl(s fl(1 / S)) (1 -+ 2^-21) is below
+// and above it for certain (four roundings of 2^-24 are half of 2^-21); rounding to
+// a code is monotone, so where both give the same code it is the right one.  About
+// 3 pages in 100 have a code where they differ and are divided out.
+__device__ __forceinline__ uint32_t recode4(uint32_t codes, float r_lo, float r_hi, uint32_t& differ) {
+  const uint32_t h0 = e4m3x2_to_f16x2(codes & 0xffffu), h1 = e4m3x2_to_f16x2(codes >> 16);
+  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h0));
+  const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&h1));
+  const uint32_t lo = f32x2_to_e4m3x2(x.x * r_lo, x.y * r_lo) |
+                      f32x2_to_e4m3x2(y.x * r_lo, y.y * r_lo) << 16;
+  const uint32_t hi = f32x2_to_e4m3x2(x.x * r_hi, x.y * r_hi) |
+                      f32x2_to_e4m3x2(y.x * r_hi, y.y * r_hi) << 16;
+  differ |= lo ^ hi;
+  return lo;
+}
+
+// The largest magnitude among four codes.
+__device__ __forceinline__ float amax4(uint32_t codes) {
+  const uint32_t h0 = e4m3x2_to_f16x2(codes & 0xffffu), h1 = e4m3x2_to_f16x2(codes >> 16);
+  const __half2 m = __hmax2(__habs2(*reinterpret_cast<const __half2*>(&h0)),
+                            __habs2(*reinterpret_cast<const __half2*>(&h1)));
+  const float2 f = __half22float2(m);
+  return fmaxf(f.x, f.y);
+}
 
 // E4M3: one warp per (destination page, kv head, sequence, K|V).  A page's scale
 // is that of the rows it now holds, so all of them are read before any is written.
@@ -358,51 +380,53 @@ evict_move_e4m3_kernel(const __grid_constant__ EvictArgs a) {
       src_scale = scales[tile];
     }
   }
-  constexpr int P = RowF16<D>::PER_LANE;
   uint32_t codes[16];
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
     const int64_t r = __shfl_sync(0xffffffffu, src_row, j);
     codes[j] = r >= 0 ? load_row_codes<D>(pool + r * D, lane) : 0u;
   }
-  auto value2 = [&](uint32_t two, float scale) {
-    const uint32_t f = e4m3x2_to_f16x2(two);
-    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&f));
-    return make_float2(__fmul_rn(v.x, scale), __fmul_rn(v.y, scale));
-  };
+  // fl(c s) grows with c, so a row's largest value is its largest code's
   float amax = 0.f;
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const float s = __shfl_sync(0xffffffffu, src_scale, j);
-    const float2 v = value2(codes[j] & 0xffffu, s);
-    amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
-    if constexpr (P == 4) {
-      const float2 u = value2(codes[j] >> 16, s);
-      amax = fmaxf(amax, fmaxf(fabsf(u.x), fabsf(u.y)));
-    }
-  }
+  for (int j = 0; j < 16; ++j)
+    amax = fmaxf(amax, __fmul_rn(amax4(codes[j]), __shfl_sync(0xffffffffu, src_scale, j)));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  const Encoder encode = Encoder::of(e4m3_page_scale(amax));
+  const float scale = e4m3_page_scale(amax);
   const int64_t tile = static_cast<int64_t>(dst) * a.Hkv + h;
-  if (lane == 0) scales[tile] = encode.scale;
+  if (lane == 0) scales[tile] = scale;
+  const unsigned live_rows = __ballot_sync(0xffffffffu, src_row >= 0);
+  uint8_t* to = pool + tile * 16 * D;
+  // lane j: row j's factor; out of range (or not a number): divided out
+  const float factor = src_scale * __fdiv_rn(1.f, scale);
+  uint32_t differ = src_row >= 0 && !(factor < 0x1p20f) ? 1u : 0u;
+  if (!(scale > 0x1p-100f && scale < 0x1p100f)) differ = 1u;
+  uint32_t out[16];
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
-    const float s = __shfl_sync(0xffffffffu, src_scale, j);
-    if (__shfl_sync(0xffffffffu, src_row, j) < 0) continue;   // behind the last row, or skipped
-    const float2 v = value2(codes[j] & 0xffffu, s);
-    uint32_t c = encode(v.x, v.y);
-    if constexpr (P == 4) {
-      const float2 u = value2(codes[j] >> 16, s);
-      c |= encode(u.x, u.y) << 16;
-    }
-    store_row_codes<D>(pool + (tile * 16 + j) * D, lane, c);
+    const float r = __shfl_sync(0xffffffffu, factor, j);
+    out[j] = recode4(codes[j], r * (1.f - 0x1p-21f), r * (1.f + 0x1p-21f), differ);
   }
+  if (__any_sync(0xffffffffu, differ != 0)) {
+#pragma unroll 1
+    for (int j = 0; j < rows; ++j) {
+      const float s = __shfl_sync(0xffffffffu, src_scale, j);
+      uint32_t c = 0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) c = i == j ? codes[i] : c;
+      c = e4m3x2_rescale(c & 0xffffu, s, scale) | e4m3x2_rescale(c >> 16, s, scale) << 16;
+      if (live_rows >> j & 1) store_row_codes<D>(to + j * D, lane, c);
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    if (live_rows >> j & 1) store_row_codes<D>(to + j * D, lane, out[j]);
 }
 
-template <int THREADS>
-cudaError_t launch_select(const EvictArgs& a, cudaStream_t s) {
-  using S = Select<THREADS>;
+template <bool ONE>
+cudaError_t launch_select(const EvictArgs& a, int cluster, cudaStream_t s) {
   {
     // more than 48 KB of shared memory has to be asked for, once per device
     static std::mutex mu;
@@ -412,14 +436,24 @@ cudaError_t launch_select(const EvictArgs& a, cudaStream_t s) {
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
     std::lock_guard<std::mutex> lock(mu);
     if (!raised[dev]) {
-      if (cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<THREADS>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem))
+      if (cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<ONE>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kSelectSmem))
         return e;
       raised[dev] = true;
     }
   }
-  evict_select_kernel<THREADS><<<dim3(a.Hkv, a.B), THREADS, S::kSmem, s>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.Hkv) * cluster, a.B);
+  cfg.blockDim = dim3(kSelectThreads);
+  cfg.dynamicSmemBytes = kSelectSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = cluster;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, evict_select_kernel<ONE>, a);
 }
 
 template <typename Kernel>
@@ -439,9 +473,11 @@ cudaError_t launch_move(Kernel* kernel, const EvictArgs& a, int pages, int threa
 }  // namespace
 
 cudaError_t launch_evict(const EvictArgs& a, bool fp8, cudaStream_t s) {
-  // 8 warps select among up to 8192 candidates (three CTAs an SM), 32 among more
-  if (cudaError_t e = a.max_context_len <= Select<256>::kKeys ? launch_select<256>(a, s)
-                                                              : launch_select<1024>(a, s))
+  // as many CTAs a unit as hold its candidates in registers, up to a portable cluster
+  int cluster = 1;
+  while (cluster < kMaxSelectCluster && a.max_context_len > cluster * kKeys) cluster *= 2;
+  if (cudaError_t e = a.max_context_len <= cluster * kKeys ? launch_select<true>(a, cluster, s)
+                                                           : launch_select<false>(a, cluster, s))
     return e;
   if (fp8)
     return launch_move(a.D == 128 ? evict_move_e4m3_kernel<128> : evict_move_e4m3_kernel<64>, a,

@@ -391,9 +391,11 @@ EVICT = [  # lens, Hkv, D, keep, first, recent, pool, dtype, kind
     ([500, 77], 1, 64, 33, 3, 5, "16", F16, "equal"),           # all alike: the lowest indexes
     ([600, 80, 49], 2, 128, 48, 2, 6, "16", F16, "odd"),
     ([5000, 1030, 1024], 2, 64, 1023, 4, 100, "16", F16, "random"),
-    ([40000, 33000], 1, 64, 700, 5, 20, "16", F16, "random"),   # more keys than stay in shared memory
-    ([40000], 1, 64, 20001, 0, 0, "16", F16, "equal"),          # one bin holds more than the list does
-    ([9000], 1, 64, 4000, 0, 7, "16", F16, "ties"),
+    ([9000, 8193], 1, 64, 4000, 0, 7, "16", F16, "ties"),       # two CTAs a unit, and so on
+    ([20000, 30000], 1, 64, 700, 5, 20, "16", F16, "odd"),
+    ([40000, 33000, 100], 1, 64, 700, 5, 20, "16", F16, "random"),
+    ([40000], 1, 64, 20001, 0, 0, "16", F16, "equal"),
+    ([70000, 66000, 9], 1, 64, 333, 1, 2, "16", F16, "ties"),   # more than the registers hold
     ([65, 64, 200], 2, 64, 64, 4, 16, "fp8", F16, "random"),
     ([300, 129, 20], 3, 128, 99, 1, 31, "fp8", F16, "ties"),
 ]
