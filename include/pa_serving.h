@@ -69,7 +69,7 @@ typedef struct pa_rope_spec {
  * num_q_heads or num_kv_heads 0 leaves that side out (its pointers unused).
  *   positions: int32 [num_axes][num_tokens], any value (negative ones turn the
  *   other way); head_dim a multiple of 8, at most 256; strides multiples of 8;
- *   dtype PA_F16 or PA_BF16.
+ *   num_q_heads + 2 num_kv_heads at most 65535; dtype PA_F16 or PA_BF16.
  */
 int pa_rope(void *q_out, const void *q, int64_t q_stride, void *k_out, const void *k,
             int64_t k_stride, const int32_t *positions, const pa_rope_spec *spec, int num_tokens,

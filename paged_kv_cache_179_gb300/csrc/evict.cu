@@ -36,12 +36,22 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n"
                "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// The word that p (in this CTA's shared memory) is in CTA `rank`'s.
-__device__ __forceinline__ int ld_cluster(const int* p, uint32_t rank) {
+// What p (in this CTA's shared memory) is in CTA `rank`'s.
+__device__ __forceinline__ uint32_t in_cluster(const void* p, uint32_t rank) {
   uint32_t at;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  return at;
+}
+__device__ __forceinline__ int ld_cluster(const int* p, uint32_t rank) {
   int v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(in_cluster(p, rank)));
+  return v;
+}
+__device__ __forceinline__ int4 ld_cluster4(const int* p, uint32_t rank) {
+  int4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(in_cluster(p, rank)));
   return v;
 }
 
@@ -71,9 +81,11 @@ __device__ __forceinline__ int checked_len(const EvictArgs& a, int b, bool repor
 //
 // Radix selection in digits of 11, 11 and 10 bits.  The first digit's histogram
 // sees every key, and the weights' few exponents would make the lanes of a warp
-// add to the same few bins: four copies, one for every fourth lane.  The CTAs'
-// histograms are joined through distributed shared memory; every CTA does the
-// whole search for itself.
+// add to the same few bins: four copies, one for every fourth lane.  Once the bin
+// that is found holds no more keys than a CTA has threads, they are listed and each
+// thread counts the larger ones of one, instead of more digits.  The CTAs'
+// histograms and lists are joined through distributed shared memory; every CTA
+// does the whole search for itself.
 constexpr int kSelectThreads = 512;
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kPer = 16;                                 // keys a thread
@@ -108,7 +120,7 @@ evict_select_kernel(const __grid_constant__ EvictArgs a) {
   int* hist = smem + kCopies * kBins;    // [digit][bin], of this CTA
   __shared__ int warp_sums[kSelectWarps];
   __shared__ int warp_gt[kSelectWarps], warp_eq[kSelectWarps];
-  __shared__ int cta_gt, cta_eq, s_bin, s_left;
+  __shared__ int cta_gt, cta_eq, s_bin, s_left, s_count, s_listed;
   griddep_launch_dependents();   // the move may do its prologue
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = static_cast<int>(cluster_rank()), size = static_cast<int>(cluster_size());
@@ -168,7 +180,9 @@ evict_select_kernel(const __grid_constant__ EvictArgs a) {
     }
   };
   if constexpr (ONE) load(lo);
-  for (int i = tid; i < (kCopies + 3) * kBins; i += kSelectThreads) smem[i] = 0;
+  for (int i = tid; i < (kCopies + 3) * kBins / 4; i += kSelectThreads)
+    reinterpret_cast<int4*>(smem)[i] = make_int4(0, 0, 0, 0);
+  if (tid == 0) s_listed = 0;
   __syncthreads();
   uint32_t prefix = 0;   // the k-th largest key's digits so far
   int left = k;          // how many of the keys with that prefix stay
@@ -195,15 +209,20 @@ evict_select_kernel(const __grid_constant__ EvictArgs a) {
     if (size > 1) cluster_sync();
     else __syncthreads();
     // the bin, from the largest down, in which the left-th key lies
-    constexpr int kEach = kBins / kSelectThreads;
-    int c[kEach], sum = 0;
+    // (four bins a thread, every CTA's asked for before any is used)
+    constexpr int kEach = 4;
+    static_assert(kEach * kSelectThreads == kBins, "");
+    int c[kEach] = {}, sum = 0;
+    const int low = bins - kEach * (tid + 1);   // the thread's lowest bin
+    if (low >= 0) {
+      int4 part[kMaxSelectCluster];
 #pragma unroll
-    for (int j = 0; j < kEach; ++j) {
-      const int bin = bins - 1 - (tid * kEach + j);
-      c[j] = 0;
-      if (bin >= 0)
-        for (int r = 0; r < size; ++r) c[j] += ld_cluster(mine + bin, r);
-      sum += c[j];
+      for (int r = 0; r < kMaxSelectCluster; ++r)
+        part[r] = r < size ? ld_cluster4(mine + low, r) : make_int4(0, 0, 0, 0);
+#pragma unroll
+      for (int r = 0; r < kMaxSelectCluster; ++r)
+        c[0] += part[r].w, c[1] += part[r].z, c[2] += part[r].y, c[3] += part[r].x;
+      sum = c[0] + c[1] + c[2] + c[3];
     }
     int over = block_scan(sum, warp_sums);
     if (over < left && over + sum >= left) {
@@ -212,6 +231,7 @@ evict_select_kernel(const __grid_constant__ EvictArgs a) {
         if (over < left && over + c[j] >= left) {
           s_bin = bins - 1 - (tid * kEach + j);
           s_left = left - over;
+          s_count = c[j];
         }
         over += c[j];
       }
@@ -219,7 +239,52 @@ evict_select_kernel(const __grid_constant__ EvictArgs a) {
     __syncthreads();
     prefix |= static_cast<uint32_t>(s_bin) << shift;
     left = s_left;
+    const int count = s_count;
     __syncthreads();
+    if (digit < 2 && count <= kSelectThreads) {
+      const uint32_t found = digit == 0 ? 0xffe00000u : 0xfffffc00u;
+      uint32_t* list = reinterpret_cast<uint32_t*>(hist + 2 * kBins);   // this CTA's, then all keys
+      uint32_t* all = list + kSelectThreads;
+      for_keys([&](uint32_t x, int, bool in) {
+        const unsigned hit = __ballot_sync(0xffffffffu, in && (x & found) == prefix);
+        if (hit == 0) return;
+        int at = 0;
+        if (lane == 0) at = atomicAdd(&s_listed, __popc(hit));
+        at = __shfl_sync(0xffffffffu, at, 0) + __popc(hit & ((1u << lane) - 1));
+        if (hit >> lane & 1) list[at] = x;
+      });
+      if (size > 1) cluster_sync();
+      else __syncthreads();
+      uint32_t x = 0;
+      if (tid < count) {
+        int listed[kMaxSelectCluster], r = 0, i = tid;
+#pragma unroll
+        for (int j = 0; j < kMaxSelectCluster; ++j) listed[j] = j < size ? ld_cluster(&s_listed, j) : 0;
+#pragma unroll
+        for (int j = 0; j < kMaxSelectCluster - 1; ++j)
+          if (r == j && i >= listed[j]) i -= listed[j], ++r;
+        x = static_cast<uint32_t>(ld_cluster(reinterpret_cast<int*>(list + i), r));
+      }
+      all[tid] = x;   // those behind the count are 0: larger than none
+      __syncthreads();
+      if (tid < count) {
+        int larger = 0, same = 0;
+        for (int i = 0; i < count; i += 4) {
+          const uint4 y = *reinterpret_cast<const uint4*>(all + i);
+          larger += (y.x > x) + (y.y > x) + (y.z > x) + (y.w > x);
+          same += (y.x == x) + (y.y == x) + (y.z == x) + (y.w == x);
+        }
+        if (larger < left && left <= larger + same) {   // every thread with this key
+          s_bin = static_cast<int>(x);
+          s_left = left - larger;
+        }
+      }
+      __syncthreads();
+      prefix = static_cast<uint32_t>(s_bin);
+      left = s_left;
+      __syncthreads();
+      break;
+    }
   }
   // every part's larger keys and ties, then the positions in order
   int gt = 0, eq = 0;
@@ -238,7 +303,14 @@ evict_select_kernel(const __grid_constant__ EvictArgs a) {
   if (size > 1) {
     if (tid == kSelectThreads - 1) cta_gt = pos + gt, cta_eq = ties + eq;
     cluster_sync();
-    for (int r = 0; r < rank; ++r) pos += ld_cluster(&cta_gt, r), ties += ld_cluster(&cta_eq, r);
+    int gts[kMaxSelectCluster], eqs[kMaxSelectCluster];
+#pragma unroll
+    for (int r = 0; r < kMaxSelectCluster; ++r) {
+      gts[r] = r < rank ? ld_cluster(&cta_gt, r) : 0;
+      eqs[r] = r < rank ? ld_cluster(&cta_eq, r) : 0;
+    }
+#pragma unroll
+    for (int r = 0; r < kMaxSelectCluster; ++r) pos += gts[r], ties += eqs[r];
   }
   pos += a.first + min(ties, left);
   const unsigned below = (1u << lane) - 1;
@@ -258,10 +330,10 @@ evict_select_kernel(const __grid_constant__ EvictArgs a) {
 }
 
 // --------------------------------------------------------------------- move
-// One CTA per (two or four destination pages, kv head, sequence).  A thread
-// moves one 16-byte chunk of K and of V of two pages; all four loads are made
-// before the stores.
+// A thread moves one 16-byte chunk of K and of V of kDeep pages; all its loads are
+// made before the stores.
 constexpr int kMoveThreads = 256;
+constexpr int kDeep = 4;
 
 template <int D>
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictArgs a) {
@@ -270,13 +342,15 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
   const int h = blockIdx.y, b = blockIdx.z;
   const int L = checked_len(a, b, false);
   const int row = threadIdx.x / C % 16, c = threadIdx.x % C;
-  int dst[2];
+  const int page0 = blockIdx.x * kDeep * kPages + threadIdx.x / (16 * C);
+  const int32_t* spare = a.spare + static_cast<int64_t>(b) * a.spare_blocks;
+  int dst[kDeep];
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int page = (blockIdx.x * 2 + j) * kPages + threadIdx.x / (16 * C);
+  for (int j = 0; j < kDeep; ++j) {
+    const int page = page0 + j * kPages;
     dst[j] = -1;
     if (L > a.keep && page * 16 + row < a.keep) {
-      dst[j] = __ldg(a.spare + static_cast<int64_t>(b) * a.spare_blocks + page);
+      dst[j] = __ldg(spare + page);
       if (dst[j] < 0 || dst[j] >= a.num_blocks) {
         atomicOr(a.status, kStatusBadBlock);
         dst[j] = -1;
@@ -284,31 +358,27 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
     }
   }
   griddep_wait();   // the kept positions are written
-  const int64_t unit = static_cast<int64_t>(b) * a.Hkv + h;
-  int t[2], src[2];
+  const int32_t* kept = a.kept + (static_cast<int64_t>(b) * a.Hkv + h) * a.keep;
+  const int32_t* table = a.block_tables + static_cast<int64_t>(b) * a.mbs;
+  int t[kDeep], src[kDeep];
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int page = (blockIdx.x * 2 + j) * kPages + threadIdx.x / (16 * C);
-    t[j] = dst[j] >= 0 ? a.kept[unit * a.keep + page * 16 + row] : 0;
-  }
+  for (int j = 0; j < kDeep; ++j) t[j] = dst[j] >= 0 ? kept[(page0 + j * kPages) * 16 + row] : 0;
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    src[j] = dst[j] >= 0 ? __ldg(a.block_tables + static_cast<int64_t>(b) * a.mbs + t[j] / 16) : 0;
+  for (int j = 0; j < kDeep; ++j) src[j] = dst[j] >= 0 ? __ldg(table + t[j] / 16) : 0;
+  uint4 kv[kDeep][2];
+#pragma unroll
+  for (int j = 0; j < kDeep; ++j) {
     if (src[j] < 0 || src[j] >= a.num_blocks) {
       atomicOr(a.status, kStatusBadBlock);
       dst[j] = -1;
     }
-  }
-  uint4 kv[2][2];
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
     if (dst[j] < 0) continue;
     const int64_t from = ((static_cast<int64_t>(src[j]) * a.Hkv + h) * 16 + t[j] % 16) * C + c;
     kv[j][0] = __ldcs(static_cast<const uint4*>(a.k_cache) + from);
     kv[j][1] = __ldcs(static_cast<const uint4*>(a.v_cache) + from);
   }
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
+  for (int j = 0; j < kDeep; ++j) {
     if (dst[j] < 0) continue;
     const int64_t to = ((static_cast<int64_t>(dst[j]) * a.Hkv + h) * 16 + row) * C + c;
     static_cast<uint4*>(a.k_cache)[to] = kv[j][0];
@@ -322,14 +392,22 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
 // and above it for certain (four roundings of 2^-24 are half of 2^-21); rounding to
 // a code is monotone, so where both give the same code it is the right one.  About
 // 3 pages in 100 have a code where they differ and are divided out.
+__device__ __forceinline__ float2 mul2(float2 x, float f) {   // one instruction
+  uint64_t a, b, r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(x.x), "f"(x.y));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(b) : "f"(f));
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  float2 out;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(out.x), "=f"(out.y) : "l"(r));
+  return out;
+}
 __device__ __forceinline__ uint32_t recode4(uint32_t codes, float r_lo, float r_hi, uint32_t& differ) {
   const uint32_t h0 = e4m3x2_to_f16x2(codes & 0xffffu), h1 = e4m3x2_to_f16x2(codes >> 16);
   const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h0));
   const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&h1));
-  const uint32_t lo = f32x2_to_e4m3x2(x.x * r_lo, x.y * r_lo) |
-                      f32x2_to_e4m3x2(y.x * r_lo, y.y * r_lo) << 16;
-  const uint32_t hi = f32x2_to_e4m3x2(x.x * r_hi, x.y * r_hi) |
-                      f32x2_to_e4m3x2(y.x * r_hi, y.y * r_hi) << 16;
+  const float2 xl = mul2(x, r_lo), yl = mul2(y, r_lo), xh = mul2(x, r_hi), yh = mul2(y, r_hi);
+  const uint32_t lo = f32x2_to_e4m3x2(xl.x, xl.y) | f32x2_to_e4m3x2(yl.x, yl.y) << 16;
+  const uint32_t hi = f32x2_to_e4m3x2(xh.x, xh.y) | f32x2_to_e4m3x2(yh.x, yh.y) << 16;
   differ |= lo ^ hi;
   return lo;
 }
@@ -348,7 +426,7 @@ __device__ __forceinline__ float amax4(uint32_t codes) {
 constexpr int kMoveE4m3Warps = 4;
 
 template <int D>
-__global__ void __launch_bounds__(kMoveE4m3Warps * 32)
+__global__ void __launch_bounds__(kMoveE4m3Warps * 32, 12)
 evict_move_e4m3_kernel(const __grid_constant__ EvictArgs a) {
   const int h = blockIdx.y, b = blockIdx.z;
   const int lane = threadIdx.x & 31, kv = threadIdx.x >> 5 & 1;
@@ -482,8 +560,8 @@ cudaError_t launch_evict(const EvictArgs& a, bool fp8, cudaStream_t s) {
   if (fp8)
     return launch_move(a.D == 128 ? evict_move_e4m3_kernel<128> : evict_move_e4m3_kernel<64>, a,
                        kMoveE4m3Warps / 2, kMoveE4m3Warps * 32, s);
-  return a.D == 128 ? launch_move(evict_move_kernel<128>, a, 2, kMoveThreads, s)
-                    : launch_move(evict_move_kernel<64>, a, 4, kMoveThreads, s);
+  return a.D == 128 ? launch_move(evict_move_kernel<128>, a, kDeep, kMoveThreads, s)
+                    : launch_move(evict_move_kernel<64>, a, 2 * kDeep, kMoveThreads, s);
 }
 
 }  // namespace pa

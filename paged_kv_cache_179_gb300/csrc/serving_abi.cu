@@ -42,7 +42,7 @@ int check_rope(int T, int Hq, int Hkv, int D, int dtype, const int32_t* position
   if (!is_act(dtype)) return PA_ERR_INVALID_ARG;
   if (D % 8 != 0 || D > 2 * kMaxRopePairs) return PA_ERR_UNSUPPORTED;
   if (positions == nullptr || !aligned(positions, 4)) return PA_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(Hq) + 2 * static_cast<int64_t>(Hkv) > INT_MAX) return PA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(Hq) + 2 * static_cast<int64_t>(Hkv) > 65535) return PA_ERR_UNSUPPORTED;
   return PA_OK;
 }
 
