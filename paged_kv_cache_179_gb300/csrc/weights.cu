@@ -3,20 +3,22 @@
 //   W[b][h][t] = old(t) + sum_r softmax_t(scale q_r . K_t)
 // over the query rows r of (sequence b, kv head h): n_q tokens times the query
 // group.  The weight of a token needs the softmax statistics of the whole
-// context, so one cooperative launch works in two phases:
+// context, so one launch works in two phases:
 //   score:  every page's logits by mma.sync (a page's 16 tokens are the 16 rows
 //           of the MMA's A, the query rows its 8 columns) and, per partition and
 //           row, the running (reference, sum);
 //   finish: per row the statistics of the whole context, joined from those of
 //           its partitions, then each token's weights summed over the rows.
-// A warp waits between them only for the warps that share its first and its last
-// (sequence, kv head), so that slow SMs do not hold up the others.
+// Short contexts take a cluster of CTAs for each unit (sequence, kv head), which joins
+// its statistics through distributed shared memory.  Long ones take a cooperative
+// launch over all units' pages, whose warps wait between the phases for the warps
+// that share their first and their last unit, so that slow SMs do not hold up others.
 // K is read once: 2 D bytes a token and kv head (D for E4M3) are the floor.  A
 // warp keeps the logits of its first pages in shared memory and those behind
 // them in the workspace, where they mostly stay in L2; the old weights come into
 // shared memory while K is read.
 //
-// Work split: the pages of all (sequence, kv head) units form one line, divided
+// Work split of the cooperative launch: the pages of all units form one line, divided
 // evenly among the warps.  A warp's part of a unit is a partition.  Units and
 // warps both grow along the line, so unit + warp numbers every partition
 // uniquely, and a unit's partitions are consecutive.
@@ -343,6 +345,40 @@ __device__ __forceinline__ void stat_join(float& m, float& l, float m2, float l2
   m = top;
 }
 
+// ------------------------------------------------------------------- clusters
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// The cluster's barrier, in two halves, by all its threads; shared memory written
+// before the arrival is seen after the wait.
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  cluster_arrive();
+  cluster_wait();
+}
+// What p (in this CTA's shared memory) is in CTA `rank`'s.
+__device__ __forceinline__ float2 ld_cluster2(const float2* p, uint32_t rank) {
+  uint32_t at;
+  float2 v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at));
+  return v;
+}
+
 // ------------------------------------------------------------------ the kernel
 // Waits until warps [w0, w0 + n) have written their statistics in call `call`;
 // by the threads `first`, first + step, ... of a warp or CTA, each for its share.
@@ -450,88 +486,99 @@ __device__ __forceinline__ void mask(float (&s)[NT][4], int first, int all_see, 
     }
 }
 
-// The logits of one warp's pages [start, end) of the line, and their statistics.
+// The logits of one warp's pages of one unit, n from page at.page on (the first of
+// them page x of the line, of which the warp's own begin at `start`), and their
+// statistics: R pairs at `stats`.
+template <int D, int KV, int NT, typename LogitsAt>
+__device__ __forceinline__ void score_segment(const WeightsArgs& a, const Place& at, int L, int n,
+                                              int64_t x, int64_t start, int lane, int rows,
+                                              float* old_weights, float2* stats,
+                                              const LogitsAt& logits_at) {
+  Query<D, KV> q[NT];
+  float f[NT][2];
+  load_rows<D, KV, NT>(a, at, rows, lane, q, f);
+  const int all_see = L - a.q_tokens + a.q_first + 1;
+  const float* weights = a.weights + (static_cast<int64_t>(at.b) * a.Hkv + at.h) * a.stride;
+  const int old_end = a.decay != 0.f ? L - a.fresh : 0;   // tokens with an old weight
+  // the reference and the sum of the lane's columns over its own tokens
+  float m[NT][2], l[NT][2];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) m[t][c] = kNoScore, l[t][c] = 0.f;
+  auto take = [&](float (&s)[NT][4], float page_scale, int i, bool skip) {
+    const int first = (at.page + i) * 16;
+    if (x - start + i < Shape<NT>::kOld && lane < 16 && first + lane < old_end)
+      cp_async4(smem_u32(old_weights + (x - start + i) * 16 + lane), weights + first + lane);
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        s[t][j] *= Kind<KV>::kE4m3 ? f[t][j & 1] * page_scale : f[t][j & 1];
+    mask<NT>(s, first, all_see, skip, a.group, lane);
+    float* out = logits_at(x + i);
+    // The reference moves only when a score exceeds it by 2^8, so that few pages
+    // pay for a rescale; a sum of up to 2^8 a token is as exact as one of 1.
+    bool grow = false;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      if constexpr (NT == 4) {
+        *reinterpret_cast<float4*>(out + (t * 32 + lane) * 4) =
+            make_float4(s[t][0], s[t][1], s[t][2], s[t][3]);
+      } else {
+        *reinterpret_cast<float2*>(out + logit_at(t, lane >> 2, lane & 3)) =
+            make_float2(s[t][0], s[t][1]);
+        *reinterpret_cast<float2*>(out + logit_at(t, (lane >> 2) + 8, lane & 3)) =
+            make_float2(s[t][2], s[t][3]);
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) grow |= fmaxf(s[t][c], s[t][c + 2]) > m[t][c] + 8.f;
+    }
+    if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float top = fmaxf(m[t][c], fmaxf(s[t][c], s[t][c + 2]));
+          l[t][c] *= fast_exp2(m[t][c] - top);
+          m[t][c] = top;
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        l[t][c] += fast_exp2(s[t][c] - m[t][c]) + fast_exp2(s[t][c + 2] - m[t][c]);
+  };
+  for_pages<D, KV, NT>(a, at, n, lane, q, take);
+  // the partition's statistics: over the 8 lanes that hold the same columns
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1)
+        stat_join(m[t][c], l[t][c], __shfl_xor_sync(0xffffffffu, m[t][c], o),
+                  __shfl_xor_sync(0xffffffffu, l[t][c], o));
+    if (lane < 4)
+      *reinterpret_cast<float4*>(stats + 8 * t + 2 * lane) =
+          make_float4(m[t][0], l[t][0], m[t][1], l[t][1]);
+  }
+}
+
+// One warp's pages [start, end) of the line.
 template <int D, int KV, int NT, typename LogitsAt>
 __device__ __forceinline__ void score_pages(const WeightsArgs& a, const Work& ws, const int* cum,
                                             int64_t start, int64_t end, int w, int lane, int rows,
                                             float* old_weights, const LogitsAt& logits_at) {
-  constexpr int R = 8 * NT;
   int64_t x = start;
   while (x < end) {
     const Place at = find(cum, a.B, a.Hkv, x);
     const int L = __ldg(a.context_lens + at.b);
     const int n = static_cast<int>(min(static_cast<int64_t>(at.pages - at.page), end - x));
-    Query<D, KV> q[NT];
-    float f[NT][2];
-    load_rows<D, KV, NT>(a, at, rows, lane, q, f);
-    const int all_see = L - a.q_tokens + a.q_first + 1;
-    const float* weights = a.weights + (static_cast<int64_t>(at.b) * a.Hkv + at.h) * a.stride;
-    const int old_end = a.decay != 0.f ? L - a.fresh : 0;   // tokens with an old weight
-    // the reference and the sum of the lane's columns over its own tokens
-    float m[NT][2], l[NT][2];
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) m[t][c] = kNoScore, l[t][c] = 0.f;
-    auto take = [&](float (&s)[NT][4], float page_scale, int i, bool skip) {
-      const int first = (at.page + i) * 16;
-      if (x - start + i < Shape<NT>::kOld && lane < 16 && first + lane < old_end)
-        cp_async4(smem_u32(old_weights + (x - start + i) * 16 + lane), weights + first + lane);
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          s[t][j] *= Kind<KV>::kE4m3 ? f[t][j & 1] * page_scale : f[t][j & 1];
-      mask<NT>(s, first, all_see, skip, a.group, lane);
-      float* out = logits_at(x + i);
-      // The reference moves only when a score exceeds it by 2^8, so that few pages
-      // pay for a rescale; a sum of up to 2^8 a token is as exact as one of 1.
-      bool grow = false;
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        if constexpr (NT == 4) {
-          *reinterpret_cast<float4*>(out + (t * 32 + lane) * 4) =
-              make_float4(s[t][0], s[t][1], s[t][2], s[t][3]);
-        } else {
-          *reinterpret_cast<float2*>(out + logit_at(t, lane >> 2, lane & 3)) =
-              make_float2(s[t][0], s[t][1]);
-          *reinterpret_cast<float2*>(out + logit_at(t, (lane >> 2) + 8, lane & 3)) =
-              make_float2(s[t][2], s[t][3]);
-        }
-#pragma unroll
-        for (int c = 0; c < 2; ++c) grow |= fmaxf(s[t][c], s[t][c + 2]) > m[t][c] + 8.f;
-      }
-      if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const float top = fmaxf(m[t][c], fmaxf(s[t][c], s[t][c + 2]));
-            l[t][c] *= fast_exp2(m[t][c] - top);
-            m[t][c] = top;
-          }
-      }
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-          l[t][c] += fast_exp2(s[t][c] - m[t][c]) + fast_exp2(s[t][c + 2] - m[t][c]);
-    };
-    for_pages<D, KV, NT>(a, at, n, lane, q, take);
-    // the partition's statistics: over the 8 lanes that hold the same columns
-    const int64_t index = static_cast<int64_t>(at.b) * a.Hkv + at.h + w;
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1)
-          stat_join(m[t][c], l[t][c], __shfl_xor_sync(0xffffffffu, m[t][c], o),
-                    __shfl_xor_sync(0xffffffffu, l[t][c], o));
-      if (lane < 4)
-        *reinterpret_cast<float4*>(ws.stats + index * R + 8 * t + 2 * lane) =
-            make_float4(m[t][0], l[t][0], m[t][1], l[t][1]);
-    }
+    const int64_t partition = static_cast<int64_t>(at.b) * a.Hkv + at.h + w;
+    score_segment<D, KV, NT>(a, at, L, n, x, start, lane, rows, old_weights,
+                             ws.stats + partition * (8 * NT), logits_at);
     x += n;
   }
 }
@@ -769,6 +816,69 @@ weights_kernel(const __grid_constant__ WeightsArgs a, Work ws) {
   }
 }
 
+// The other kernel: one cluster of CTAs per (kv head, sequence), whose warps divide
+// its pages and join their statistics through distributed shared memory; the
+// hardware deals the clusters out, and none waits for another.  A warp's logits
+// behind the first kKept pages go to the workspace.
+constexpr int kMaxCluster = 8;
+
+template <int D, int KV, int NT>
+__global__ void __launch_bounds__(Shape<NT>::kWarps * 32, Shape<NT>::kCtas)
+weights_unit_kernel(const __grid_constant__ WeightsArgs a, float* spilled, int64_t unit_pages) {
+  using S = Shape<NT>;
+  constexpr int R = 8 * NT;
+  extern __shared__ __align__(16) uint8_t warp_smem[];
+  __shared__ __align__(16) float2 stats[S::kWarps][R];
+  __shared__ __align__(8) float2 cta_stats[R];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = static_cast<int>(cluster_rank()), size = static_cast<int>(cluster_size());
+  const int h = blockIdx.x / size, b = blockIdx.y;
+  const int L = checked_len(a, b, blockIdx.x == 0 && tid == 0);
+  if (L == 0) return;   // the whole cluster
+  const int pages = (L + 15) / 16, rows = a.n_q * a.group;
+  const int w = rank * S::kWarps + warp, warps = size * S::kWarps;
+  const int start = static_cast<int>(static_cast<int64_t>(pages) * w / warps);
+  const int n = static_cast<int>(static_cast<int64_t>(pages) * (w + 1) / warps) - start;
+  const int64_t unit = static_cast<int64_t>(b) * a.Hkv + h;
+  uint8_t* mine = warp_smem + warp * S::kWarpBytes;
+  float* kept = reinterpret_cast<float*>(mine);
+  float* old_weights = reinterpret_cast<float*>(mine + S::kKept * S::kPage * 16);
+  float* behind = spilled + unit * unit_pages * (S::kPage * 4);
+  auto logits_at = [&](int64_t x) {
+    return x - start < S::kKept ? kept + (x - start) * (S::kPage * 4) : behind + x * (S::kPage * 4);
+  };
+  const Place at{b, h, start, pages, 0};
+  if (n > 0)
+    score_segment<D, KV, NT>(a, at, L, n, start, start, lane, rows, old_weights, stats[warp], logits_at);
+  else
+    for (int r = lane; r < R; r += 32) stats[warp][r] = make_float2(kNoScore, 0.f);
+  cp_async_wait_all();
+  __syncthreads();
+  float2 st = stats[0][lane % R];
+#pragma unroll
+  for (int i = 1; i < S::kWarps; ++i)
+    stat_join(st.x, st.y, stats[i][lane % R].x, stats[i][lane % R].y);
+  if (size > 1) {
+    if (tid < R) cta_stats[tid] = st;
+    cluster_sync();
+    float2 all[kMaxCluster];
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r)
+      all[r] = r < size ? ld_cluster2(&cta_stats[lane % R], r) : make_float2(kNoScore, 0.f);
+    st = all[0];
+#pragma unroll
+    for (int r = 1; r < kMaxCluster; ++r) stat_join(st.x, st.y, all[r].x, all[r].y);
+    cluster_arrive();   // nobody's statistics are read any more, once all have arrived
+  }
+  st.y = lane % R < rows && (st.y > 0.f || st.y != st.y) ? 1.f / st.y : 0.f;
+  float* weights = a.weights + unit * a.stride;
+  if constexpr (NT == 4)
+    finish_pages4(a, weights, L, start, n, start, start, st, lane, old_weights, logits_at);
+  else
+    finish_pages<NT>(a, weights, L, start, n, start, start, st, lane, old_weights, logits_at);
+  if (size > 1) cluster_wait();
+}
+
 int tiles_of(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
 
 // CTAs of a launch of `warps` warps each, `ctas` of them an SM; fewer when there
@@ -781,10 +891,28 @@ int weights_grid(const WeightsArgs& a, int warps, int ctas) {
   return static_cast<int>(want < 1 ? 1 : want < most ? want : most);
 }
 
+// CTAs a unit is divided among by the cluster kernel, 0 for the cooperative one.
+// Up to 4096 tokens a cluster a unit: with 400 units of up to 512 and 2048 tokens 14.7
+// and 33.6 us against 23.6 and 45.6, with 96 units 8.3 and 15.1 against 14.2 and 22.2,
+// with 4 units 6.3 and 7.9 against 12.4 (fp16, head_dim 128, 7 rows); longer units
+// divide too unevenly when their lengths differ (512 units, median 1024, bound 8192:
+// 69 us against 57).  Two CTAs and more while all fit the GPU at once and each warp
+// has a page, or while a warp has more than 16.
+int unit_cluster(const WeightsArgs& a, int warps, int ctas) {
+  const int64_t pages = (static_cast<int64_t>(a.max_context_len) + 15) / 16;
+  if (pages > 256) return 0;
+  const int64_t units = static_cast<int64_t>(a.B) * a.Hkv, slots = static_cast<int64_t>(ctas) * device_sm_count();
+  int c = 1;
+  while (c < kMaxCluster && ((units * 2 * c <= slots && pages > warps * c) || pages > 16 * warps * c)) c *= 2;
+  return c;
+}
+
 template <int D, int KV, int NT>
 cudaError_t launch_tiles(const WeightsArgs& a, const Work& ws, cudaStream_t s) {
   using S = Shape<NT>;
+  const int cluster = unit_cluster(a, S::kWarps, S::kCtas);
   auto* kernel = weights_kernel<D, KV, NT>;
+  auto* unit_kernel = weights_unit_kernel<D, KV, NT>;
   {
     // more than 48 KB of shared memory has to be asked for, once per device
     static std::mutex mu;
@@ -797,19 +925,30 @@ cudaError_t launch_tiles(const WeightsArgs& a, const Work& ws, cudaStream_t s) {
       if (cudaError_t e = cudaFuncSetAttribute(
               kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem))
         return e;
+      if (cudaError_t e = cudaFuncSetAttribute(
+              unit_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem))
+        return e;
       raised[dev] = true;
     }
   }
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(weights_grid(a, S::kWarps, S::kCtas));
   cfg.blockDim = dim3(S::kWarps * 32);
   cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeCooperative;   // the CTAs wait for one another
-  attr.val.cooperative = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
+  if (cluster > 0) {
+    cfg.gridDim = dim3(static_cast<unsigned>(a.Hkv) * cluster, a.B);
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = cluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    const int64_t unit_pages = (static_cast<int64_t>(a.max_context_len) + 15) / 16;
+    return cudaLaunchKernelEx(&cfg, unit_kernel, a, ws.logits, unit_pages);
+  }
+  cfg.gridDim = dim3(weights_grid(a, S::kWarps, S::kCtas));
+  attr.id = cudaLaunchAttributeCooperative;   // the CTAs wait for one another
+  attr.val.cooperative = 1;
   return cudaLaunchKernelEx(&cfg, kernel, a, ws);
 }
 

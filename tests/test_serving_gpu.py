@@ -236,6 +236,12 @@ WEIGHTS = [  # lens, Hq, Hkv, D, n_q, pool, dtype, decay, fresh
     ([31, 500], 28, 4, 128, 1, "fp8", F16, .5, 1),
     ([16, 260], 24, 1, 128, 1, "fp8", BF16, 0., 0),             # 24 rows
     ([20000, 1], 4, 1, 128, 1, "16", F16, 1., 1),               # long: every warp has a part of it
+    ([4100, 0, 33, 700], 28, 4, 64, 1, "16", BF16, .5, 1),      # shared by the warps of several units
+    ([4500, 90], 8, 1, 128, 3, "fp8", F16, 1., 3),
+    ([5000, 17], 30, 1, 64, 1, "fp8", BF16, .5, 0),
+    ([4000, 2900, 1], 16, 2, 128, 2, "16", F16, .5, 2),         # clusters, more pages than they keep
+    ([3000, 4096], 28, 1, 128, 1, "16", F16, 0., 0),
+    ([700, 65, 0], 20, 1, 64, 1, "16", BF16, 1., 1),
 ]
 
 
@@ -312,7 +318,7 @@ def test_attention_weights_bad_indexes_are_skipped_and_reported():
 
 
 def test_attention_weights_reports_a_workspace_that_was_not_cleared():
-    q, kc, ks, bt, L, w = weights_case([640, 3], 4, 2, 64, 1, "16", F16, 14)
+    q, kc, ks, bt, L, w = weights_case([4200, 3], 4, 2, 64, 1, "16", F16, 14)   # beyond one cluster
     n = _abi.pa_attention_weights_workspace_size(2, 4, 2, bt.shape[1] * 16, 1)
     ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
     ws[:4] = 0x7f
