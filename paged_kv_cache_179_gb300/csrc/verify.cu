@@ -11,12 +11,12 @@
 // values, so it is not rounded either.
 //
 // Bytes: one row of p and one of q per sequence; which ones is known only after
-// the drafts' own probabilities have been read.  Measured on a GB300: 35 us for
-// 128 sequences of 128000 fp32 tokens with draft probabilities (131 MB, 55 % of
+// the drafts' own probabilities have been read.  Measured on a GB300: 31 to 33 us for
+// 128 sequences of 128000 fp32 tokens with draft probabilities (131 MB, 60 % of
 // the measured copy bandwidth), 8.2 us for one sequence of 32000: that much is
 // the chain launch, drafts, their probabilities, row, cluster barrier, border.
-// CTAs of 256 threads at 32 registers (eight an SM) and four loads in flight:
-// 35 us; 512 threads 40 us; eight loads at 40 registers and more 37 to 41 us;
+// CTAs of 256 threads at 32 registers, eight an SM (six: 39 us; 512 threads 40 us),
+// 16 bytes a lane (4 bytes, four in flight: 35 us; 32 bytes at 40 registers: 35 us);
 // one CTA a sequence 195 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -118,6 +118,7 @@ struct Row {
   const T* p;
   const T* q;       // null: nothing is taken off p, except at `spike`
   int spike;        // a draft without probabilities: 1 is taken off there; or -1
+  bool wide;        // both rows begin at a multiple of 16 bytes
   __device__ __forceinline__ uint64_t at(int j) const {
     const float x = clean(to_f32(p[j]));
     Limbs w;
@@ -143,6 +144,20 @@ struct Row {
       for (int i = 0; i < N; ++i) w.add(clean(to_f32(x[i])), 0.f);
     }
   }
+  // the same for the 16 bytes of tokens from j on
+  static constexpr int kWide = 16 / sizeof(T);
+  __device__ __forceinline__ void add_wide(int j, Limbs& w) const {
+    const uint4 x = __ldcs(reinterpret_cast<const uint4*>(p + j));
+    uint4 y = make_uint4(0, 0, 0, 0);
+    if (q != nullptr) y = __ldcs(reinterpret_cast<const uint4*>(q + j));
+    const T* px = reinterpret_cast<const T*>(&x);
+    const T* qx = reinterpret_cast<const T*>(&y);
+#pragma unroll
+    for (int e = 0; e < kWide; ++e) {
+      const float v = clean(to_f32(px[e]));
+      w.add(v, q != nullptr ? fminf(v, fmaxf(to_f32(qx[e]), 0.f)) : 0.f);
+    }
+  }
 };
 
 // floor(u * total) for u in [0, 1): the token drawn is the first whose
@@ -157,12 +172,22 @@ __device__ __forceinline__ uint64_t threshold(float u, uint64_t total) {
 constexpr int kMaxCluster = 8;
 constexpr int kUnroll = 4;
 
-// Sum of the weights of tokens [lo, hi), taken by one warp (all lanes get it):
-// coalesced loads of one element a lane, kUnroll of them in flight.  Rows of
-// any alignment are served alike.
+// Sum of the weights of tokens [from, hi), taken by one warp (all lanes get it):
+// 16 bytes a lane where the rows' alignment allows it, then, or for rows that begin
+// anywhere, one element a lane, kUnroll of them in flight.
 template <typename T>
-__device__ __forceinline__ uint64_t warp_range_sum(const Row<T>& row, int lo, int hi, int lane) {
+__device__ __forceinline__ uint64_t warp_range_sum(const Row<T>& row, int from, int hi, int lane) {
+  int lo = from;
   uint64_t sum = 0;
+  if (row.wide) {   // lo is a multiple of 8 tokens
+    constexpr int kStep = 32 * Row<T>::kWide;   // of a warp
+    while (lo + kStep <= hi) {
+      Limbs w;
+      for (int i = 0; i < 512 / Row<T>::kWide && lo + kStep <= hi; ++i, lo += kStep)
+        row.add_wide(lo + lane * Row<T>::kWide, w);
+      sum += w.value();
+    }
+  }
   int j = lo + lane;
   constexpr int kBatch = kUnroll * 32;
   while (j + kBatch - 32 < hi) {
@@ -174,7 +199,7 @@ __device__ __forceinline__ uint64_t warp_range_sum(const Row<T>& row, int lo, in
   Limbs w;
   for (; j < hi; j += 32) row.template add<1>(j, w);
   sum += w.value();
-  if (lane == 0 && lo <= row.spike && row.spike < hi) {   // what 1 takes off the spike
+  if (lane == 0 && from <= row.spike && row.spike < hi) {   // what 1 takes off the spike
     const float x = clean(to_f32(row.p[row.spike]));
     Limbs s;
     s.add(fminf(x, 1.f), 0.f);
@@ -237,6 +262,7 @@ verify_kernel(const VerifyArgs a) {
   row.p = p + r * a.p_stride;
   row.q = r < nb && q != nullptr ? q + r * a.q_stride : nullptr;
   row.spike = r < nb && q == nullptr ? __ldg(drafts + r) : -1;
+  row.wide = a.p_stride * sizeof(T) % 16 == 0 && (row.q == nullptr || a.q_stride * sizeof(T) % 16 == 0);
   if (rank == 0) {
     for (int i = tid; i <= a.n; i += kVerifyThreads)
       if (i != r) out[i] = i > r ? -1 : i == tid ? x0 : __ldg(drafts + i);
@@ -244,7 +270,7 @@ verify_kernel(const VerifyArgs a) {
   }
   // part i of the row's size * kVerifyWarps goes to warp i of the cluster
   const int parts = size * kVerifyWarps;
-  const int len = (a.V + parts - 1) / parts;
+  const int len = ((a.V + parts - 1) / parts + 7) / 8 * 8;
   uint64_t total;
   const uint64_t* all = sums[0];
   for (int pass = 0;; ++pass) {
@@ -297,7 +323,7 @@ verify_kernel(const VerifyArgs a) {
   int lo = part * len, hi = min(lo + len, a.V);
   constexpr int kEach = 4;
   while (hi - lo > kEach * kVerifyThreads) {   // a warp's share at a time
-    const int step = (hi - lo + kVerifyWarps - 1) / kVerifyWarps;
+    const int step = ((hi - lo + kVerifyWarps - 1) / kVerifyWarps + 7) / 8 * 8;
     const int l0 = min(lo + warp * step, hi);
     const uint64_t sum = warp_range_sum(row, l0, min(l0 + step, hi), lane);
     if (lane == 0) level[warp] = sum;

@@ -475,6 +475,8 @@ VERIFY = [  # B, n, V, dtype, draft, pad
     (3, 8, 32000, torch.float32, False, 0),
     (40, 3, 129, BF16, True, 0),
     (1, 1, 300001, torch.float32, True, 0),       # a warp's part is narrowed down twice
+    (2, 2, 400000, torch.float32, False, 0),
+    (3, 1, 300008, BF16, True, 0),
     (700, 1, 40, torch.float32, True, 0),         # more sequences than CTAs fit at once
 ]
 
