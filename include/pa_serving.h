@@ -214,7 +214,7 @@ int pa_evict_fp8(uint8_t *k_cache, uint8_t *v_cache, float *k_scale, float *v_sc
  *   values above 2 as 2.  draft_tokens int32 [num_seqs][max_drafts]; num_drafts
  *   int32 [num_seqs], or NULL when all have max_drafts; uniforms fp32
  *   [num_seqs][max_drafts + 1] in [0, 1).  max_drafts 0..1024 (0: a plain draw);
- *   vocab_size at most 2^24.
+ *   vocab_size and num_seqs at most 2^24.
  * Sums are 64-bit fixed-point numbers (2^-60), so a result does not depend on
  * the order of summation.  A row of zeros draws -1.  A draft outside
  * [0, vocab_size) is rejected and sets PA_STATUS_BAD_TOKEN; a num_drafts

@@ -470,7 +470,7 @@ evict_select_kernel(const __grid_constant__ EvictArgs a) {
         static_cast<uint4*>(a.v_cache)[to] = static_cast<const uint4*>(a.v_cache)[from];
       }
     } else {
-      for (int i = tid_all >> 5; i < (a.keep + 15) / 16 * 2; i += threads_all >> 5) {
+      for (int i = tid_all >> 5; i < ((a.keep - 1) / 16 + 1) * 2; i += threads_all >> 5) {
         const int dst = __ldg(spare + (i >> 1));
         if (a.D == 128) move_page_e4m3<128>(a, b, h, i >> 1, i & 1, dst, lane);
         else move_page_e4m3<64>(a, b, h, i >> 1, i & 1, dst, lane);
@@ -584,7 +584,7 @@ cudaError_t launch_select(const EvictArgs& a, int cluster, cudaStream_t s) {
 template <typename Kernel>
 cudaError_t launch_move(Kernel* kernel, const EvictArgs& a, int pages, int threads, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(((a.keep + 15) / 16 + pages - 1) / pages, a.Hkv, a.B);
+  cfg.gridDim = dim3(((a.keep - 1) / 16 + pages) / pages, a.Hkv, a.B);
   cfg.blockDim = dim3(threads);
   cfg.stream = s;
   cudaLaunchAttribute attr{};

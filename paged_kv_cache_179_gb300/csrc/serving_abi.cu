@@ -61,6 +61,8 @@ int rope_append(RopeArgs& a, bool fp8, const pa_rope_spec* spec, int dtype, void
   if (a.block_size <= 0 || a.num_blocks <= 0) return PA_ERR_INVALID_ARG;
   if (fp8 && a.D != 64 && a.D != 128) return PA_ERR_UNSUPPORTED;
   if (fp8 && a.block_size != 16) return PA_ERR_UNSUPPORTED;
+  // CTAs of one launch
+  if (static_cast<int64_t>(a.T) * (1 + a.Hkv) > INT_MAX) return PA_ERR_UNSUPPORTED;
   if (!rope_side(a.q_out, a.q, a.q_stride, a.Hq, a.D) ||
       !rope_side(a.k_cache, a.k, a.k_stride, a.Hkv, a.D) ||
       !rope_side(a.v_cache, a.v, a.v_stride, a.Hkv, a.D))
@@ -351,7 +353,7 @@ int pa_verify_drafts(int32_t* out_tokens, int32_t* num_accepted, const void* tar
   if (num_seqs < 0 || max_drafts < 0 || max_drafts > 1024 || vocab_size <= 0)
     return PA_ERR_INVALID_ARG;
   if (dtype != PA_F32 && !is_act(dtype)) return PA_ERR_INVALID_ARG;
-  if (vocab_size > (1 << 24)) return PA_ERR_UNSUPPORTED;
+  if (vocab_size > (1 << 24) || num_seqs > (1 << 24)) return PA_ERR_UNSUPPORTED;
   if (!out_tokens || !num_accepted || !target_probs || !uniforms) return PA_ERR_INVALID_ARG;
   if (max_drafts > 0 && !draft_tokens) return PA_ERR_INVALID_ARG;
   if (target_stride < vocab_size || (draft_probs && draft_stride < vocab_size))

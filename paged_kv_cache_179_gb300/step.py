@@ -63,6 +63,7 @@ class DecodeStep:
             self.workspace = _abi.alloc_workspace(self.B, self.Hq, self.D, self.split_ctas,
                                                   k_cache.device, query_rows=rows)
         self._bound = {}     # run_from_staging's bound steps
+        self._weights_ws = {}   # accumulate's workspaces
 
     def append(self, k_new, v_new, slot_mapping):
         if self.kv == "fp8":
@@ -82,6 +83,50 @@ class DecodeStep:
                            self.context_lens, self.max_context_len, self.scale,
                            self.split_ctas, self.workspace, window=self.window,
                            early_prologue=self.early_prologue, early_copies=self.early_copies)
+
+    def rope_append(self, q_out, q, k_new, v_new, slot_mapping, positions, spec):
+        """``append`` with rotary positions, in one launch: q rotated into q_out, k
+        rotated into the K pool, v copied into the V pool (``spec``: an
+        ``_abi.RopeSpec``; positions int32 [axes][tokens]).  Any number of
+        tokens; in an E4M3 pool each of another page."""
+        if self.kv == "fp8":
+            _abi.pa_rope_append_fp8(q_out, q, k_new, v_new, self.k_cache, self.v_cache,
+                                    self.k_scale, self.v_scale, slot_mapping, positions, spec)
+        else:
+            _abi.pa_rope_append(q_out, q, k_new, v_new, self.k_cache, self.v_cache, slot_mapping,
+                                positions, spec)
+
+    def accumulate(self, weights, q, *, decay=1.0, fresh_tokens=0):
+        """Add to weights fp32 [B][Hkv][>= max_context_len] the attention weight that
+        each cached token gets from q's rows (as ``decode`` attends, without a
+        window): what ``evict`` goes by."""
+        n_q = 1 if q.dim() == 3 else int(q.shape[1])
+        if n_q not in self._weights_ws:    # one workspace per number of query tokens
+            self._weights_ws[n_q] = _abi.alloc_weights_workspace(
+                self.B, self.Hq, self.Hkv, self.max_context_len, n_q, self.k_cache.device)
+        if self.kv == "fp8":
+            _abi.pa_attention_weights_fp8(weights, q, self.k_cache, self.k_scale,
+                                          self.block_tables, self.context_lens,
+                                          self.max_context_len, self.scale, self._weights_ws[n_q],
+                                          decay=decay, fresh_tokens=fresh_tokens)
+        else:
+            _abi.pa_attention_weights(weights, q, self.k_cache, self.block_tables,
+                                      self.context_lens, self.max_context_len, self.scale,
+                                      self._weights_ws[n_q], decay=decay,
+                                      fresh_tokens=fresh_tokens)
+
+    def evict(self, weights, weights_out, spare_tables, tables_out, new_lens, kept, *,
+              first_tokens=0, recent_tokens=0):
+        """Cut every sequence above kept.shape[2] tokens to its first, its last and its
+        heaviest ones, moved into the blocks of spare_tables; tables_out and
+        new_lens are the tables and lengths to go on with (``_abi.pa_evict``)."""
+        args = (weights, weights_out, self.block_tables, self.context_lens, self.max_context_len,
+                spare_tables, tables_out, new_lens, kept)
+        kw = dict(first_tokens=first_tokens, recent_tokens=recent_tokens)
+        if self.kv == "fp8":
+            _abi.pa_evict_fp8(self.k_cache, self.v_cache, self.k_scale, self.v_scale, *args, **kw)
+        else:
+            _abi.pa_evict(self.k_cache, self.v_cache, *args, **kw)
 
     def fused(self, q, k_new, v_new, slot_mapping, out, sync=None, copies=None):
         """Append and decode in one launch (slot_mapping must hold each

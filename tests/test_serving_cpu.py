@@ -92,6 +92,8 @@ def test_rope_append_refusals(lib):
             assert call(fp8, **bad) == INV, bad
     assert call(True, sc=None) == INV
     assert call(True, bs=32) == UNS
+    assert call(True, T=2 ** 30) == UNS
+    assert call(Hq=65534, qs=65534 * 64) == UNS                   # more rows a token than a CTA counts
     assert call(True, D=80, qs=640, ks=160, vs=160) == UNS
 
 
@@ -167,6 +169,7 @@ def test_verify_refusals(lib):
                 dict(V=0), dict(ps=999), dict(qs=999), dict(dtype=2), dict(dtype=4)):
         assert call(**bad) == INV, bad
     assert call(V=2 ** 24 + 1, ps=2 ** 25, qs=2 ** 25) == UNS
+    assert call(B=2 ** 24 + 1) == UNS
 
 
 @pytest.mark.skipif(torch.cuda.is_available(), reason="only meaningful without a CUDA device")

@@ -332,6 +332,51 @@ def test_attention_weights_reports_a_workspace_that_was_not_cleared():
     assert torch.equal(got, again) and not ws[:4].any()
 
 
+@pytest.mark.parametrize("D,pool,lens", [(128, "16", [100, 33]), (64, "16", [4500, 7]),
+                                         (128, "fp8", [4500, 7]), (64, "fp8", [90])])
+def test_attention_weights_of_a_pool_that_begins_at_16_bytes(D, pool, lens):
+    """Pools are 16-byte aligned, no more."""
+    q, kc, ks, bt, L, w = weights_case(lens, 8, 2, D, 1, pool, F16, 15, garbage=False)
+    want = run_weights(q, kc, ks, bt, L, w, .125, .5, 0)
+    off = 16 // kc.element_size()
+    room = torch.empty(kc.numel() + 64, dtype=kc.dtype, device="cuda")
+    moved = room[off:off + kc.numel()].view(kc.shape)
+    moved.copy_(kc)
+    assert moved.data_ptr() % 32 == 16
+    got = run_weights(q, moved, ks, bt, L, w, .125, .5, 0)
+    ok()
+    assert torch.equal(got, want)
+
+
+def test_attention_weights_long_contexts_in_a_graph():
+    """The cooperative launch, captured: every replay adds what the first call added,
+    and two graphs may use one workspace in turn."""
+    q, kc, ks, bt, L, w = weights_case([6000, 40, 5000], 8, 2, 64, 1, "16", F16, 16)
+    mx = bt.shape[1] * 16
+    ws = _abi.alloc_weights_workspace(3, 8, 2, mx, 1, "cuda")
+    d = [t.cuda() for t in (q, kc, bt, L)]
+    wd = w.cuda()
+    call = lambda decay: _abi.pa_attention_weights(wd, *d, mx, .125, ws, decay=decay)  # noqa: E731
+    call(0.)
+    once = wd.clone()
+    graphs = []
+    for decay in (0., 1.):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call(decay)
+        graphs.append(g)
+    wd.zero_()
+    graphs[0].replay()
+    graphs[1].replay()
+    graphs[1].replay()
+    ok()
+    live = torch.arange(wd.shape[2], device="cuda") < L.cuda()[:, None, None]
+    assert torch.allclose(wd[live.expand_as(wd)], 3 * once[live.expand_as(wd)], rtol=2 ** -22, atol=0)
+    graphs[0].replay()
+    ok()
+    assert torch.equal(wd[live.expand_as(wd)], once[live.expand_as(wd)])
+
+
 def test_attention_weights_workspace_too_small():
     q, kc, ks, bt, L, w = weights_case([64], 4, 2, 64, 1, "16", F16, 13)
     n = _abi.pa_attention_weights_workspace_size(1, 4, 2, 64, 1)
@@ -428,6 +473,56 @@ def test_evict(lens, Hkv, D, keep, first, recent, pool, dtype, kind):
         assert torch.equal(got.cpu().view(torch.uint8), want.view(torch.uint8))
     for got, want in zip(s, scales):
         assert want is None or torch.equal(got.cpu(), want)
+
+
+def test_evict_of_many_small_sequences():
+    lens = [(5 * i) % 61 for i in range(300)]
+    pools, scales, w, bt, L, spare = evict_case(lens, 3, 64, 21, "fp8", F16, 8, "ties")
+    p, s, w_out, tables, new, kept = run_evict(pools, scales, w, bt, L, spare, 21, 2, 3)
+    ok()
+    ref_new, ref_kept, ref_tables = R.evict(pools, scales, w.numpy(), bt, L.numpy(), spare, 21, 2, 3)
+    assert np.array_equal(new.cpu().numpy(), ref_new) and torch.equal(tables.cpu(), ref_tables)
+    kept = kept.cpu().numpy()
+    assert all(np.array_equal(kept[k][:len(v)], v) for k, v in ref_kept.items())
+    assert all(torch.equal(a.cpu(), b) for a, b in zip(p + s, pools + scales))
+
+
+def test_blocks_behind_two_billion_elements():
+    """Block ids whose elements lie behind 2^31: append, weights and eviction."""
+    g = gen(41)
+    Hkv, D, n = 1, 128, 5
+    NB = 2 ** 31 // (16 * D) + 64
+    kc, vc = (torch.empty(NB, Hkv, 16, D, dtype=F16, device="cuda") for _ in "kv")
+    table = torch.arange(NB - n, NB, dtype=torch.int32)[None]
+    spare = torch.arange(NB - 20, NB - 16, dtype=torch.int32)[None]
+    T = 16 * n - 3
+    slots = (table[0].long()[torch.arange(T) // 16] * 16 + torch.arange(T) % 16).cuda()
+    q, k, v = (randn(g, T, 1, D).cuda() for _ in "qkv")
+    spec, inv, axis = spec_for(64, 1, False)
+    pos = torch.arange(T, dtype=torch.int32).cuda()
+    qo, ko = torch.empty_like(q), torch.empty_like(k)
+    _abi.pa_rope_append(qo, q, k, v, kc, vc, slots, pos, spec)
+    _abi.pa_rope(None, None, ko, k, pos, spec)
+    assert torch.equal(kc[-n:].view(-1, D)[:T], ko[:, 0]) and torch.equal(vc[-n:].view(-1, D)[:T], v[:, 0])
+    L = torch.tensor([T], dtype=torch.int32).cuda()
+    w = torch.zeros(1, 1, 16 * n, device="cuda")
+    ws = _abi.alloc_weights_workspace(1, 1, 1, 16 * n, 1, "cuda")
+    _abi.pa_attention_weights(w, qo[-1:], kc, table.cuda(), L, 16 * n, .088, ws, decay=0.)
+    x = R.f64(qo[-1, 0]) @ R.f64(ko[:, 0]).T * np.float64(np.float32(.088))
+    e = np.exp(x - x.max())
+    # tolerances as derived beside R.attention_weights
+    S = .088 * (np.abs(R.f64(ko[:, 0])) @ np.abs(R.f64(qo[-1, 0])))
+    err = 2. ** -19 * S + 2. ** -22 * np.abs(x)
+    assert (np.abs(R.f64(w[0, 0, :T]) - e / e.sum()) <= e / e.sum() * (err + err.max() + 2. ** -18)).all()
+    new, kept = torch.empty(1, dtype=torch.int32, device="cuda"), torch.empty(1, 1, 50, dtype=torch.int32, device="cuda")
+    _abi.pa_evict(kc, vc, w, None, table.cuda(), L, 16 * n, spare.cuda(), None, new, kept,
+                  first_tokens=1, recent_tokens=9)
+    ok()
+    at = R.evict_choice(w[0, 0].cpu().numpy(), T, 50, 1, 9)
+    assert np.array_equal(kept[0, 0].cpu().numpy(), at)
+    at = torch.from_numpy(at).cuda()
+    assert torch.equal(kc[NB - 20:NB - 16].view(-1, D)[:50], ko[at, 0])
+    assert torch.equal(vc[NB - 20:NB - 16].view(-1, D)[:50], v[at, 0])
 
 
 def test_evict_without_the_optional_outputs():
@@ -699,6 +794,48 @@ def test_wrong_shapes_types_and_layouts_are_refused():
         _abi.pa_verify_drafts(out, acc, p, p[:, :3].half(), i, u)
     with pytest.raises(ValueError):
         _abi.pa_verify_drafts(out, acc, p.transpose(0, 1).contiguous().transpose(0, 1), None, i, u)
+
+
+@pytest.mark.parametrize("pool", ["16", "fp8"])
+def test_decode_step_methods_make_these_calls(pool):
+    """DecodeStep.rope_append, accumulate and evict over its own pools and tables."""
+    from paged_kv_cache_179_gb300.step import DecodeStep
+    lens, Hq, Hkv, D, keep = [70, 33], 6, 2, 64, 32
+    g = gen(51)
+    pools, scales, w, bt, L, spare = evict_case(lens, Hkv, D, keep, pool, F16, 51, "random")
+    d = [t.cuda() for t in pools]
+    sc = [None if t is None else t.cuda() for t in scales]
+    kw = {} if pool == "16" else dict(k_scale=sc[0], v_scale=sc[1])
+    step = DecodeStep(k_cache=d[0], v_cache=d[1], block_tables=bt.cuda(), context_lens=L.cuda(),
+                      max_context_len=bt.shape[1] * 16, scale=.125, num_q_heads=Hq, split_ctas=2, **kw)
+    spec, _, _ = spec_for(32, 1, True)
+    q, k, v = randn(g, 2, Hq, D).cuda(), randn(g, 2, Hkv, D).cuda(), randn(g, 2, Hkv, D).cuda()
+    pos = (L - 1).cuda()
+    slots = (bt.gather(1, ((L - 1) // 16).long()[:, None])[:, 0].long() * 16 + (L - 1) % 16).cuda()
+    qo, q2, kr = torch.empty_like(q), torch.empty_like(q), torch.empty_like(k)
+    copies = [t.clone() for t in d], [None if t is None else t.clone() for t in sc]
+    step.rope_append(qo, q, k, v, slots, pos, spec)
+    _abi.pa_rope(q2, q, kr, k, pos, spec)
+    if pool == "16":
+        _abi.pa_cache_append(kr, v, *copies[0], slots)
+    else:
+        _abi.pa_cache_append_fp8(kr, v, *copies[0], *copies[1], slots)
+    ok()
+    assert torch.equal(qo, q2) and all(torch.equal(a, b) for a, b in zip(d, copies[0]))
+    out = torch.empty_like(q)
+    step.decode(qo, out)
+    wd = w.cuda()
+    want = run_weights(qo.cpu()[:, None], d[0].cpu(), None if pool == "16" else sc[0].cpu(), bt, L, w, .125, .5, 1)
+    step.accumulate(wd, qo, decay=.5, fresh_tokens=1)
+    assert torch.equal(wd, want)
+    kept = torch.empty(2, Hkv, keep, dtype=torch.int32, device="cuda")
+    new, tables = torch.empty(2, dtype=torch.int32, device="cuda"), torch.empty_like(spare).cuda()
+    step.evict(wd, None, spare.cuda(), tables, new, kept, first_tokens=1, recent_tokens=4)
+    ok()
+    assert new.tolist() == [keep] * 2 and torch.equal(tables.cpu(), spare)
+    for b in range(2):
+        for h in range(Hkv):
+            assert np.array_equal(kept[b, h].cpu().numpy(), R.evict_choice(wd[b, h].cpu().numpy(), lens[b], keep, 1, 4))
 
 
 # ------------------------------------------------------- the calls together
