@@ -14,7 +14,8 @@
 // shared memory, then walk over the tokens' heads, 32 bytes at a time.  Measured on
 // a GB300 with 28 + 4 + 4 heads of 128: 55.6 us for 16384 bf16 tokens (302 MB, 80 %
 // of the measured copy bandwidth), 6.1 us for 512, 4.3 us for 4 (8 heads of 64).
-// 128 threads and two tokens a CTA; 256 threads 57 to 61 us, one token 63 us, four
+// 16 tokens of the same heads take 4.2 us with 512 threads a CTA, 6.2 us with 128.
+// Prompts: 128 threads and two tokens a CTA; 256 threads 57 to 61 us, one token 63 us, four
 // tokens 57 us, eight 68 us; two and more rows in flight a thread 65 us.
 #include "pa_e4m3.cuh"
 #include "pa_launch.h"
@@ -25,6 +26,7 @@ namespace pa {
 namespace {
 
 constexpr int kRopeThreads = 128;
+constexpr int kRopeFewThreads = 512;   // of a CTA, while the tokens do not fill the GPU
 constexpr int kRopeTokens = 2;   // most a CTA serves
 
 __device__ __forceinline__ float2 rope_sincos(uint64_t turns, int32_t pos, float amplitude) {
@@ -178,7 +180,7 @@ __device__ __forceinline__ void rope_tokens(const RopeArgs& a, const RopeTable& 
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(kRopeThreads)
+__global__ void __launch_bounds__(kRopeFewThreads)
 rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ RopeTable t, int rows,
             uint32_t rows_magic, int toks) {
   __shared__ __align__(16) float2 cs[kRopeTokens * kMaxRopePairs];
@@ -288,7 +290,8 @@ cudaError_t launch_rope(const RopeArgs& a, const RopeTable& t, bool bf16, cudaSt
   int toks = 1;
   while (rows > 1 && toks < kRopeTokens && 2 * toks * rows <= 4096 && a.T / (2 * toks) >= 4 * device_sm_count()) toks *= 2;
   const int items = (a.D + 15) / 16;
-  const int most = kRopeThreads / items;   // rows a full CTA takes at once
+  // rows a CTA takes at once; few tokens are done sooner by more threads each
+  const int most = (a.T <= 2 * device_sm_count() ? kRopeFewThreads : kRopeThreads) / items;
   const int passes = (toks * rows + most - 1) / most;
   const int threads = (toks * rows + passes - 1) / passes * items;
   auto* kernel = bf16 ? rope_kernel<true> : rope_kernel<false>;
