@@ -110,7 +110,8 @@ int pa_rope_append_fp8(void *q_out, const void *q, int64_t q_stride, const void 
  * (those appended since the last call, whose entry still holds what a former
  * token left there).  decay 0 reads no old weight.  Query i sits at position
  * L - n_q + i and attends positions up to its own, as in pa_decode; one before
- * position 0 adds nothing.  Entries behind the context stay as they are.
+ * position 0 adds nothing, nor does one whose logits are all -inf.  Entries behind
+ * the context stay as they are.
  *   weights: fp32 [num_seqs][num_kv_heads][weights_stride], weights_stride >=
  *   max_context_len; a row belongs to its sequence, so sequences that share
  *   blocks keep weights of their own.
@@ -121,8 +122,10 @@ int pa_rope_append_fp8(void *q_out, const void *q, int64_t q_stride, const void 
  *   after call, whatever their sizes.  After a status with PA_STATUS_TIMEOUT or
  *   PA_STATUS_WS_DIRTY (it held what no call leaves; results may be wrong)
  *   zero-fill it again.  Calls that share one must not overlap on the device.
- * One cooperative launch per pass: its warps wait, bounded by 2 s, for one
- * another's softmax statistics.
+ * One launch per pass and 512 sequences.  With max_context_len above 4096 it is
+ * a cooperative one, whose warps wait, bounded by 2 s, for one another's softmax
+ * statistics; only these can set PA_STATUS_TIMEOUT or PA_STATUS_WS_DIRTY.
+ * max_context_len at most 2^30.
  * Results do not depend on the order of execution.
  */
 size_t pa_attention_weights_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads,
@@ -172,6 +175,9 @@ int pa_attention_weights_fp8(float *weights, int64_t weights_stride, const void 
  * [num_seqs][spare_blocks_per_seq], spare_blocks_per_seq >= ceil(keep / 16),
  * and not overlapping block_tables; new_lens must not be context_lens.
  * Keys keep the rotation of the position they were written at.
+ * max_context_len at most 2^30.  The next pa_decode or pa_decode_step over the
+ * moved blocks must not be one with PA_DECODE_EARLY_COPIES, nor with
+ * PA_DECODE_EARLY_PROLOGUE when it reads tables_out or new_lens.
  */
 int pa_evict(void *k_cache, void *v_cache, const float *weights, int64_t weights_stride,
              float *weights_out, int64_t weights_out_stride, const int32_t *block_tables,

@@ -616,6 +616,7 @@ cudaError_t launch_evict(const EvictArgs& a, bool fp8, cudaStream_t s) {
                : (one ? launch_select<true, 1>(a, cluster, s) : launch_select<false, 1>(a, cluster, s));
   if (cudaError_t e = one ? launch_select<true, 0>(a, cluster, s) : launch_select<false, 0>(a, cluster, s))
     return e;
+  if (a.keep >= a.max_context_len) return cudaSuccess;   // nothing can be cut
   if (fp8)
     return launch_move(a.D == 128 ? evict_move_e4m3_kernel<128> : evict_move_e4m3_kernel<64>, a,
                        kMoveE4m3Warps / 2, kMoveE4m3Warps * 32, s);

@@ -13,6 +13,7 @@ namespace {
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? PA_OK : PA_ERR_CUDA; }
+constexpr int kMaxContext = 1 << 30;   // the kernels step beyond a token's index in 32 bits
 bool is_act(int dtype) { return dtype == PA_F16 || dtype == PA_BF16; }
 
 // Checks the rotation's arguments and fills the launch's table.
@@ -95,6 +96,7 @@ int attention_weights(WeightsArgs a, int block_size, float scale, int dtype, siz
   a.group = a.Hq / a.Hkv;
   if (a.group > kWeightsMaxRows) return PA_ERR_UNSUPPORTED;
   if (a.B > 65535 || a.Hkv > 65535) return PA_ERR_UNSUPPORTED;
+  if (a.max_context_len > kMaxContext) return PA_ERR_UNSUPPORTED;
   // the pages of one launch's sequences are counted in 32 bits
   if ((a.max_context_len / 16 + INT64_C(1)) * (a.B < kWeightsMaxBatch ? a.B : kWeightsMaxBatch) > INT_MAX)
     return PA_ERR_UNSUPPORTED;
@@ -127,7 +129,7 @@ int evict(EvictArgs a, int block_size, bool fp8, void* stream) {
     return PA_ERR_INVALID_ARG;
   if (a.D != 64 && a.D != 128) return PA_ERR_UNSUPPORTED;
   if (block_size != 16) return PA_ERR_UNSUPPORTED;
-  if (a.B > 65535 || a.Hkv > 65535) return PA_ERR_UNSUPPORTED;
+  if (a.B > 65535 || a.Hkv > 65535 || a.max_context_len > kMaxContext) return PA_ERR_UNSUPPORTED;
   if (a.spare_blocks < (a.keep + static_cast<int64_t>(15)) / 16) return PA_ERR_INVALID_ARG;
   if (!a.k_cache || !a.v_cache || !a.weights || !a.block_tables || !a.context_lens || !a.spare ||
       !a.new_lens || !a.kept)

@@ -233,7 +233,7 @@ template <int D, int KV>
 struct Query {
   uint32_t w[D / 16][2];   // b0, b1 of each of the D / 16 MMA steps
   // returns what the scores have to be multiplied by (1 unless q was scaled)
-  __device__ __forceinline__ float load(const uint16_t* row, bool live, int lane) {
+  __device__ __forceinline__ float load(const uint16_t* row, int lane) {
     // elements of a K chunk: its bytes over an element's
     constexpr int kRow = Page<D, KV>::kRow;
     constexpr int per = (kRow < 128 ? 16 : 32) / (Kind<KV>::kE4m3 ? 1 : 2);
@@ -241,9 +241,7 @@ struct Query {
     for (int j = 0; j < D / (4 * per); ++j) {
 #pragma unroll
       for (int x = 0; x < per / 8; ++x) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (live)
-          v = __ldg(reinterpret_cast<const uint4*>(row + ((lane & 3) + 4 * j) * per + 8 * x));
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + ((lane & 3) + 4 * j) * per + 8 * x));
         const int s = (j * per + 8 * x) / 4;         // two steps per 8 elements
         w[s][0] = v.x;
         w[s][1] = v.y;
@@ -462,29 +460,30 @@ __device__ __forceinline__ void for_pages(const WeightsArgs& a, const Place& at,
 }
 
 // The query rows of a unit and what turns their scores into log2 units, for the
-// lane's two columns of each tile.
+// lane's two columns of each tile.  Columns behind the rows hold the last row again:
+// they get weight 0 in the second phase, and a score of theirs is infinite or not a
+// number (which no weight makes 0) only where a row's own is.
 template <int D, int KV, int NT>
 __device__ __forceinline__ void load_rows(const WeightsArgs& a, const Place& at, int rows, int lane,
                                           Query<D, KV> (&q)[NT], float (&f)[NT][2]) {
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    const int r = 8 * t + (lane >> 2);
+    const int r = min(8 * t + (lane >> 2), rows - 1);
     const int i = r / a.group, g = r - i * a.group;
     const uint16_t* row = static_cast<const uint16_t*>(a.q) +
         ((static_cast<int64_t>(at.b) * a.q_tokens + a.q_first + i) * a.Hq +
          at.h * a.group + g) * D;
-    const float back = q[t].load(row, r < rows, lane) * a.scale_log2;
+    const float back = q[t].load(row, lane) * a.scale_log2;
     f[t][0] = __shfl_sync(0xffffffffu, back, (lane & 3) * 8);
     f[t][1] = __shfl_sync(0xffffffffu, back, (lane & 3) * 8 + 4);
   }
 }
 
 // Scores of tokens that a row does not attend become -inf: those from all_see +
-// (its query's number) on, and all of a skipped page.  Padding rows (q = 0) get
-// weight 0 in the second phase instead.
+// (its query's number) on, and all of a skipped page.
 template <int NT>
 __device__ __forceinline__ void mask(float (&s)[NT][4], int first, int all_see, bool skip, int group,
-                                     int lane) {
+                                     int n_q, int lane) {
   if (first + 16 <= all_see && !skip) return;
   const int tok = first + (lane >> 2);
 #pragma unroll
@@ -492,7 +491,7 @@ __device__ __forceinline__ void mask(float (&s)[NT][4], int first, int all_see, 
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int col = 8 * t + 2 * (lane & 3) + (j & 1);
-      if (skip || tok + (j & 2 ? 8 : 0) >= all_see + col / group) s[t][j] = -INFINITY;
+      if (skip || tok + (j & 2 ? 8 : 0) >= all_see + min(col / group, n_q - 1)) s[t][j] = -INFINITY;
     }
 }
 
@@ -525,7 +524,7 @@ __device__ __forceinline__ void score_segment(const WeightsArgs& a, const Place&
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         s[t][j] *= Kind<KV>::kE4m3 ? f[t][j & 1] * page_scale : f[t][j & 1];
-    mask<NT>(s, first, all_see, skip, a.group, lane);
+    mask<NT>(s, first, all_see, skip, a.group, a.n_q, lane);
     float* out = logits_at(x + i);
     // The reference moves only when a score exceeds it by 2^8, so that few pages
     // pay for a rescale; a sum of up to 2^8 a token is as exact as one of 1.
@@ -799,6 +798,7 @@ weights_kernel(const __grid_constant__ WeightsArgs a, Work ws) {
       const int parts = part_of(line, at.unit_start + at.pages - 1) - w0 + 1;
       const bool there = await_warps(ws, w0, parts, call, lane, 32, a.status, a.wait_limit_ns);
       if (!__all_sync(0xffffffffu, there)) break;
+      __syncwarp();   // what any lane has waited for is seen by all
       st = join_by_warp<R>(ws.stats + (static_cast<int64_t>(unit) + w0) * R, parts, lane);
     }
     // an empty row's and a padding row's tokens get 0

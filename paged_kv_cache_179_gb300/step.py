@@ -99,9 +99,14 @@ class DecodeStep:
     def accumulate(self, weights, q, *, decay=1.0, fresh_tokens=0):
         """Add to weights fp32 [B][Hkv][>= max_context_len] the attention weight that
         each cached token gets from q's rows (as ``decode`` attends, without a
-        window): what ``evict`` goes by."""
+        window): what ``evict`` goes by.  The first call with a number of query
+        tokens allocates their workspace, so it cannot be one that is captured."""
         n_q = 1 if q.dim() == 3 else int(q.shape[1])
         if n_q not in self._weights_ws:    # one workspace per number of query tokens
+            if torch.cuda.is_current_stream_capturing():
+                # it would be zero-filled by the graph's replays, not now
+                raise RuntimeError(f"accumulate with {n_q} query tokens: make a call before the "
+                                   "capture, it allocates the workspace")
             self._weights_ws[n_q] = _abi.alloc_weights_workspace(
                 self.B, self.Hq, self.Hkv, self.max_context_len, n_q, self.k_cache.device)
         if self.kv == "fp8":
@@ -119,7 +124,9 @@ class DecodeStep:
               first_tokens=0, recent_tokens=0):
         """Cut every sequence above kept.shape[2] tokens to its first, its last and its
         heaviest ones, moved into the blocks of spare_tables; tables_out and
-        new_lens are the tables and lengths to go on with (``_abi.pa_evict``)."""
+        new_lens are the tables and lengths to go on with (``_abi.pa_evict``).  The
+        next decode after it must not use ``early_copies``, nor ``early_prologue``
+        when it reads those two."""
         args = (weights, weights_out, self.block_tables, self.context_lens, self.max_context_len,
                 spare_tables, tables_out, new_lens, kept)
         kw = dict(first_tokens=first_tokens, recent_tokens=recent_tokens)

@@ -121,6 +121,7 @@ def test_attention_weights_refusals(lib):
         for bad in (dict(ws=None), dict(ws=FAKE + 16)):
             assert call(fp8, **bad) == WSP, bad
     assert call(True, ks=None) == INV
+    assert call(mx=2 ** 30 + 1, st=2 ** 31, mbs=2 ** 27, n=1 << 62) == UNS   # indexes end at 2^30
     # 2^31 pages and more in one launch
     assert call(mx=2 ** 31 - 1, st=2 ** 31, mbs=2 ** 27, B=512, n=1 << 62) == UNS
     f = lib.pa_attention_weights_workspace_size
@@ -150,7 +151,8 @@ def test_evict_refusals(lib):
                     dict(kept=None), dict(nl=None), dict(mx=129), dict(B=-1), dict(NB=0),
                     dict(kept=FAKE + 2), dict(first=2 ** 31 - 1, recent=2 ** 31 - 1)):
             assert call(fp8, **bad) == INV, bad
-        for bad in (dict(D=96), dict(bs=32, mbs=4), dict(B=70000)):
+        for bad in (dict(D=96), dict(bs=32, mbs=4), dict(B=70000),
+                    dict(mx=2 ** 30 + 1, st=2 ** 31, mbs=2 ** 27)):
             assert call(fp8, **bad) == UNS, bad
     assert call(dtype=2) == INV
     assert call(True, sc=None) == INV

@@ -274,6 +274,43 @@ def test_attention_weights_of_one_token_and_zero_queries():
     assert torch.equal(got[:, :, 48:], w[:, :, 48:])      # entries behind the context
 
 
+@pytest.mark.parametrize("Hq,n_q,n,max_len", [(9, 1, 100, None), (9, 1, 40, 5008), (15, 2, 200, None), (30, 2, 77, None),
+                                               (30, 4, 90, 5008)])
+def test_attention_weights_of_infinite_keys(Hq, n_q, n, max_len):
+    """A key that makes a logit -inf has weight 0, one that makes it +inf or NaN makes the
+    row's weights NaN, as the softmax has it; rows and passes that do not fill a
+    tile change nothing."""
+    Hkv, D, group = 3, 64, Hq // 3
+    q, kc, ks, bt, L, w = weights_case([n], Hq, Hkv, D, n_q, "16", F16, 17)
+    if max_len:
+        bt = torch.cat([bt, torch.full((1, max_len // 16 - bt.shape[1]), -1, dtype=torch.int32)], 1)
+        w = torch.zeros(1, Hkv, max_len)
+    q[..., 0] = 1
+    q[:, :, 2 * group:, 0] = -1
+    for at in (5, n - 1):                       # the last token: the last query alone sees it
+        kc[int(bt[0, at // 16]), 0, at % 16, 0] = float("-inf")
+    kc[int(bt[0, 1]), 1, 3, 0] = float("nan")
+    kc[int(bt[0, 2]), 2, 3, 0] = float("inf")   # -inf after q's sign
+    got = R.f64(run_weights(q, kc, ks, bt, L, w, .125, 0., 0, max_len=max_len))
+    ok()
+    assert np.isnan(got[0, 1, :n]).all()
+    for h in (0, 2):
+        K = R.keys(kc, ks, bt[0], h, n)
+        size = .125 * (np.abs(np.where(np.isinf(K), 0, K)) @ np.abs(R.f64(q[0, :, h * group:(h + 1) * group])).reshape(-1, D).T)
+        assert size.max() <= 16
+        ref = np.zeros(n)
+        for i in range(n_q):
+            m = n - n_q + 1 + i
+            for j in range(group):
+                s = .125 * (K[:m] @ R.f64(q[0, i, h * group + j]))
+                e = np.exp(s - s.max())
+                ref[:m] += e / e.sum()
+        # as for finite keys: a logit of 4 steps is off by 4 * 2^-22 * 16 + 2^-22 * 16, a weight
+        # by its own and its row's largest, 160 * 2^-22, and 2^-20 for the rest: under 2^-14
+        assert (np.abs(got[0, h, :n] - ref) <= 2. ** -14 * ref).all()
+        assert got[0, h, 5 if h == 0 else 35] == 0
+
+
 def test_attention_weights_is_deterministic_and_shares_blocks():
     """Sequences with the same blocks get what private copies get, bit for bit
     and in every run."""
@@ -473,6 +510,22 @@ def test_evict(lens, Hkv, D, keep, first, recent, pool, dtype, kind):
         assert torch.equal(got.cpu().view(torch.uint8), want.view(torch.uint8))
     for got, want in zip(s, scales):
         assert want is None or torch.equal(got.cpu(), want)
+
+
+@pytest.mark.parametrize("pool", ["16", "fp8"])
+def test_evict_of_a_budget_that_nothing_exceeds(pool):
+    pools, scales, w, bt, L, spare = evict_case([600, 48, 0], 2, 64, 608, pool, F16, 18, "random")
+    p, s, w_out, tables, new, kept = run_evict(pools, scales, w, bt, L, spare, 608, 2, 300)
+    ok()
+    assert new.tolist() == [600, 48, 0]
+    want = torch.full_like(spare, -1)
+    want[:, :bt.shape[1]] = bt[:, :want.shape[1]]
+    assert torch.equal(tables.cpu(), want)
+    for b, n in enumerate(new.tolist()):
+        assert torch.equal(kept[b, :, :n].cpu(), torch.arange(n, dtype=torch.int32).expand(2, n))
+        assert torch.equal(w_out[b, :, :n].cpu(), w[b, :, :n])
+    for a, b in zip(p, pools):
+        assert torch.equal(a.cpu().view(torch.uint8), b.view(torch.uint8))
 
 
 def test_evict_of_many_small_sequences():
@@ -825,6 +878,10 @@ def test_decode_step_methods_make_these_calls(pool):
     out = torch.empty_like(q)
     step.decode(qo, out)
     wd = w.cuda()
+    with torch.cuda.graph(torch.cuda.CUDAGraph()):     # the first call allocates: not in a capture
+        with pytest.raises(RuntimeError, match="before the capture"):
+            step.accumulate(wd, qo, decay=.5, fresh_tokens=1)
+        out.zero_()
     want = run_weights(qo.cpu()[:, None], d[0].cpu(), None if pool == "16" else sc[0].cpu(), bt, L, w, .125, .5, 1)
     step.accumulate(wd, qo, decay=.5, fresh_tokens=1)
     assert torch.equal(wd, want)
