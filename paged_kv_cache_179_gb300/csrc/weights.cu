@@ -49,17 +49,25 @@ namespace {
 
 constexpr int kPrefix = kWeightsMaxBatch + 1;
 constexpr int kMaxWarps = 12;
+constexpr int kOld = 32;   // pages a warp whose old weights are copied ahead
 // Warps of a CTA, CTAs an SM, and what a warp's share of shared memory holds: the
-// logits of kKept pages and the old weights of kOld.  Up to 16 query rows keep 16
-// warps an SM; the q fragments of 32 take 64 registers, which leaves room for 12.
-template <int NT>
+// logits of kKept pages, the old weights of kOld and, at head_dim 128, the query's MMA
+// fragments.  Up to 16 query rows keep 16 warps an SM; 32 need the registers of 12.
+// The fragments of 8, 16 and 32 rows of 128 take 16, 32 and 64 registers, or shared
+// memory that would keep 4 more pages.  Registers against shared memory: 57.6 and 56.8
+// us for 7 rows (128 16-bit contexts), 53.6 and 45.9 for 14 and 73.8 and 55.8 for 28
+// (24 contexts of up to 8000 tokens), 87.5 and 78.7 for 28 rows over two E4M3 contexts
+// of 115k; at head_dim 64 they are half as large, and 32 rows take 47.2 us against 50.6.
+template <int D, int NT>
 struct Shape {
+  static constexpr bool kSharedQ = D == 128;
   static constexpr int kWarps = NT == 4 ? 12 : 8;
   static constexpr int kCtas = NT == 4 ? 1 : 2;
-  static constexpr int kKept = NT == 1 ? 22 : NT == 2 ? 11 : 8;
+  static constexpr int kKept = (NT == 1 ? 22 : NT == 2 ? 11 : 8) - (kSharedQ ? 4 : 0);
   static constexpr int kPage = NT * 32;        // float4s of a page's logits
-  static constexpr int kOld = 32;
-  static constexpr int kWarpBytes = kKept * kPage * 16 + kOld * 64;
+  static constexpr int kOldAt = kKept * kPage * 16;      // bytes
+  static constexpr int kQueryAt = kOldAt + kOld * 64;
+  static constexpr int kWarpBytes = kQueryAt + (kSharedQ ? NT * 8 * D * 2 : 0);
   static constexpr int kSmem = kWarps * kWarpBytes;
 };
 
@@ -275,37 +283,66 @@ struct Query {
   }
 };
 
+// The query rows of a unit as MMA fragments, in registers or in shared memory, where
+// the lane's 16 bytes of tile t and steps 2 s and 2 s + 1 stand at (t * D / 32 + s) * 32
+// (each lane reads only what it has written).
+template <int D, int KV, int NT>
+struct Rows {
+  static constexpr bool kShared = Shape<D, NT>::kSharedQ;
+  Query<D, KV> q[kShared ? 1 : NT];
+  uint4* shared;
+  __device__ __forceinline__ void put(int t) {
+    if constexpr (kShared) {
+#pragma unroll
+      for (int s = 0; s < D / 32; ++s)
+        shared[(t * (D / 32) + s) * 32] = make_uint4(q[0].w[2 * s][0], q[0].w[2 * s][1],
+                                                     q[0].w[2 * s + 1][0], q[0].w[2 * s + 1][1]);
+    }
+  }
+};
+
 template <int D, int KV, int NT>
 __device__ __forceinline__ void page_scores(float (&acc)[NT][4], const Page<D, KV>& k,
-                                            const Query<D, KV> (&q)[NT]) {
+                                            const Rows<D, KV, NT>& rows) {
   constexpr bool BF16 = Kind<KV>::kBf16;
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[t][i] = 0.f;
   // a step takes 4 elements a lane: two words of 16-bit values, one of codes
-  constexpr int kWords = Page<D, KV>::kRow < 128 ? 4 : 8;
-#pragma unroll
-  for (int j = 0; j < Page<D, KV>::NLD; ++j) {
-    const uint32_t* lo = k.lo[j].w;
-    const uint32_t* hi = k.hi[j].w;
+  constexpr int kSteps = (Page<D, KV>::kRow < 128 ? 4 : 8) / (Kind<KV>::kE4m3 ? 1 : 2);   // of a chunk
+  auto fragment = [&](int st, uint32_t (&a)[4]) {
+    const uint32_t* lo = k.lo[st / kSteps].w;
+    const uint32_t* hi = k.hi[st / kSteps].w;
+    const int i = st % kSteps;
     if constexpr (Kind<KV>::kE4m3) {
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) {
-        const uint32_t a0 = e4m3x2_to_f16x2(lo[i] & 0xffffu), a2 = e4m3x2_to_f16x2(lo[i] >> 16);
-        const uint32_t a1 = e4m3x2_to_f16x2(hi[i] & 0xffffu), a3 = e4m3x2_to_f16x2(hi[i] >> 16);
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-          mma16816<BF16>(acc[t], a0, a1, a2, a3, q[t].w[kWords * j + i][0],
-                         q[t].w[kWords * j + i][1]);
-      }
+      a[0] = e4m3x2_to_f16x2(lo[i] & 0xffffu), a[2] = e4m3x2_to_f16x2(lo[i] >> 16);
+      a[1] = e4m3x2_to_f16x2(hi[i] & 0xffffu), a[3] = e4m3x2_to_f16x2(hi[i] >> 16);
     } else {
+      a[0] = lo[2 * i], a[1] = hi[2 * i], a[2] = lo[2 * i + 1], a[3] = hi[2 * i + 1];
+    }
+  };
+  if constexpr (Rows<D, KV, NT>::kShared) {
 #pragma unroll
-      for (int i = 0; i < kWords / 2; ++i)
+    for (int s = 0; s < D / 32; ++s) {
+      uint32_t a0[4], a1[4];
+      fragment(2 * s, a0);
+      fragment(2 * s + 1, a1);
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-          mma16816<BF16>(acc[t], lo[2 * i], hi[2 * i], lo[2 * i + 1], hi[2 * i + 1],
-                         q[t].w[kWords / 2 * j + i][0], q[t].w[kWords / 2 * j + i][1]);
+      for (int t = 0; t < NT; ++t) {
+        const uint4 b = rows.shared[(t * (D / 32) + s) * 32];
+        mma16816<BF16>(acc[t], a0[0], a0[1], a0[2], a0[3], b.x, b.y);
+        mma16816<BF16>(acc[t], a1[0], a1[1], a1[2], a1[3], b.z, b.w);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int st = 0; st < D / 16; ++st) {
+      uint32_t f[4];
+      fragment(st, f);
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        mma16816<BF16>(acc[t], f[0], f[1], f[2], f[3], rows.q[t].w[st][0], rows.q[t].w[st][1]);
     }
   }
 }
@@ -417,7 +454,7 @@ __device__ __forceinline__ int logit_at(int t, int tok, int c) {
 // outside the pool).
 template <int D, int KV, int NT, typename Take>
 __device__ __forceinline__ void for_pages(const WeightsArgs& a, const Place& at, int n, int lane,
-                                          const Query<D, KV> (&q)[NT], const Take& take) {
+                                          const Rows<D, KV, NT>& q, const Take& take) {
   using P = Page<D, KV>;
   // pages in registers, the one at work among them: up to 64 registers
   constexpr int kAhead = P::kRow >= 256 || NT == 4 ? 2 : NT == 1 ? 4 : 3;
@@ -465,7 +502,7 @@ __device__ __forceinline__ void for_pages(const WeightsArgs& a, const Place& at,
 // number (which no weight makes 0) only where a row's own is.
 template <int D, int KV, int NT>
 __device__ __forceinline__ void load_rows(const WeightsArgs& a, const Place& at, int rows, int lane,
-                                          Query<D, KV> (&q)[NT], float (&f)[NT][2]) {
+                                          Rows<D, KV, NT>& to, float (&f)[NT][2]) {
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     const int r = min(8 * t + (lane >> 2), rows - 1);
@@ -473,7 +510,8 @@ __device__ __forceinline__ void load_rows(const WeightsArgs& a, const Place& at,
     const uint16_t* row = static_cast<const uint16_t*>(a.q) +
         ((static_cast<int64_t>(at.b) * a.q_tokens + a.q_first + i) * a.Hq +
          at.h * a.group + g) * D;
-    const float back = q[t].load(row, lane) * a.scale_log2;
+    const float back = to.q[Rows<D, KV, NT>::kShared ? 0 : t].load(row, lane) * a.scale_log2;
+    to.put(t);
     f[t][0] = __shfl_sync(0xffffffffu, back, (lane & 3) * 8);
     f[t][1] = __shfl_sync(0xffffffffu, back, (lane & 3) * 8 + 4);
   }
@@ -501,9 +539,11 @@ __device__ __forceinline__ void mask(float (&s)[NT][4], int first, int all_see, 
 template <int D, int KV, int NT, typename LogitsAt>
 __device__ __forceinline__ void score_segment(const WeightsArgs& a, const Place& at, int L, int n,
                                               int64_t x, int64_t start, int lane, int rows,
-                                              float* old_weights, float2* stats,
+                                              uint8_t* mine, float2* stats,
                                               const LogitsAt& logits_at) {
-  Query<D, KV> q[NT];
+  float* old_weights = reinterpret_cast<float*>(mine + Shape<D, NT>::kOldAt);
+  Rows<D, KV, NT> q;
+  q.shared = reinterpret_cast<uint4*>(mine + Shape<D, NT>::kQueryAt) + lane;
   float f[NT][2];
   load_rows<D, KV, NT>(a, at, rows, lane, q, f);
   const int all_see = L - a.q_tokens + a.q_first + 1;
@@ -517,7 +557,7 @@ __device__ __forceinline__ void score_segment(const WeightsArgs& a, const Place&
     for (int c = 0; c < 2; ++c) m[t][c] = kNoScore, l[t][c] = 0.f;
   auto take = [&](float (&s)[NT][4], float page_scale, int i, bool skip) {
     const int first = (at.page + i) * 16;
-    if (x - start + i < Shape<NT>::kOld && lane < 16 && first + lane < old_end)
+    if (x - start + i < kOld && lane < 16 && first + lane < old_end)
       cp_async4(smem_u32(old_weights + (x - start + i) * 16 + lane), weights + first + lane);
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -579,14 +619,14 @@ __device__ __forceinline__ void score_segment(const WeightsArgs& a, const Place&
 template <int D, int KV, int NT, typename LogitsAt>
 __device__ __forceinline__ void score_pages(const WeightsArgs& a, const Work& ws, const int* cum,
                                             int64_t start, int64_t end, int w, int lane, int rows,
-                                            float* old_weights, const LogitsAt& logits_at) {
+                                            uint8_t* mine, const LogitsAt& logits_at) {
   int64_t x = start;
   while (x < end) {
     const Place at = find(cum, a.B, a.Hkv, x);
     const int L = __ldg(a.context_lens + at.b);
     const int n = static_cast<int>(min(static_cast<int64_t>(at.pages - at.page), end - x));
     const int64_t partition = static_cast<int64_t>(at.b) * a.Hkv + at.h + w;
-    score_segment<D, KV, NT>(a, at, L, n, x, start, lane, rows, old_weights,
+    score_segment<D, KV, NT>(a, at, L, n, x, start, lane, rows, mine,
                              ws.stats + partition * (8 * NT), logits_at);
     x += n;
   }
@@ -602,7 +642,7 @@ __device__ __forceinline__ void finish_pages(const WeightsArgs& a, float* weight
                                              const float* old_weights, const LogitsAt& logits_at) {
   const int old_end = a.decay != 0.f ? L - a.fresh : 0;
   auto old_of = [&](int page, int in_page) {
-    return x0 + page - start < Shape<NT>::kOld ? old_weights[(x0 + page - start) * 16 + in_page]
+    return x0 + page - start < kOld ? old_weights[(x0 + page - start) * 16 + in_page]
                                                : weights[(first + page) * 16 + in_page];
   };
   // a token a lane, two pages a step
@@ -671,7 +711,7 @@ __device__ __forceinline__ void finish_pages4(const WeightsArgs& a, float* weigh
 #pragma unroll
       for (int t = 0; t < 4; ++t) s[j][t] = in[t * 32];
       if ((lane & 2) == 0 && (first + i - j) * 16 + in_page < old_end)
-        old[j] = x0 + i - j - start < Shape<4>::kOld
+        old[j] = x0 + i - j - start < kOld
                      ? old_weights[(x0 + i - j - start) * 16 + in_page]
                      : weights[(first + i - j) * 16 + in_page];
     }
@@ -716,9 +756,9 @@ __device__ __forceinline__ float2 join_by_warp(const float2* st, int n, int lane
 constexpr int kWarpJoin = 16;
 
 template <int D, int KV, int NT>
-__global__ void __launch_bounds__(Shape<NT>::kWarps * 32, Shape<NT>::kCtas)
+__global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kCtas)
 weights_kernel(const __grid_constant__ WeightsArgs a, Work ws) {
-  using S = Shape<NT>;
+  using S = Shape<D, NT>;
   constexpr int R = 8 * NT;
   constexpr int kThreads = S::kWarps * 32;
   extern __shared__ __align__(16) uint8_t warp_smem[];
@@ -738,12 +778,12 @@ weights_kernel(const __grid_constant__ WeightsArgs a, Work ws) {
   const int64_t end = part_start(line, min(w + 1, line.workers));
   uint8_t* mine = warp_smem + (tid >> 5) * S::kWarpBytes;
   float* kept = reinterpret_cast<float*>(mine);
-  float* old_weights = reinterpret_cast<float*>(mine + S::kKept * S::kPage * 16);
+  float* old_weights = reinterpret_cast<float*>(mine + S::kOldAt);
   // the logits of page x: of the warp's first kKept in shared memory
   auto logits_at = [&](int64_t x) {
     return x - start < S::kKept ? kept + (x - start) * (S::kPage * 4) : ws.logits + x * (S::kPage * 4);
   };
-  score_pages<D, KV, NT>(a, ws, cum, start, end, w, lane, rows, old_weights, logits_at);
+  score_pages<D, KV, NT>(a, ws, cum, start, end, w, lane, rows, mine, logits_at);
   __threadfence();
   __syncwarp();
   if (lane == 0 && w < line.workers) st_release_gpu_b32(ws.sync + 2 + w, call);
@@ -833,9 +873,9 @@ weights_kernel(const __grid_constant__ WeightsArgs a, Work ws) {
 constexpr int kMaxCluster = 8;
 
 template <int D, int KV, int NT>
-__global__ void __launch_bounds__(Shape<NT>::kWarps * 32, Shape<NT>::kCtas)
+__global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, Shape<D, NT>::kCtas)
 weights_unit_kernel(const __grid_constant__ WeightsArgs a, float* spilled, int64_t unit_pages) {
-  using S = Shape<NT>;
+  using S = Shape<D, NT>;
   constexpr int R = 8 * NT;
   extern __shared__ __align__(16) uint8_t warp_smem[];
   __shared__ __align__(16) float2 stats[S::kWarps][R];
@@ -852,14 +892,14 @@ weights_unit_kernel(const __grid_constant__ WeightsArgs a, float* spilled, int64
   const int64_t unit = static_cast<int64_t>(b) * a.Hkv + h;
   uint8_t* mine = warp_smem + warp * S::kWarpBytes;
   float* kept = reinterpret_cast<float*>(mine);
-  float* old_weights = reinterpret_cast<float*>(mine + S::kKept * S::kPage * 16);
+  float* old_weights = reinterpret_cast<float*>(mine + S::kOldAt);
   float* behind = spilled + unit * unit_pages * (S::kPage * 4);
   auto logits_at = [&](int64_t x) {
     return x - start < S::kKept ? kept + (x - start) * (S::kPage * 4) : behind + x * (S::kPage * 4);
   };
   const Place at{b, h, start, pages, 0};
   if (n > 0)
-    score_segment<D, KV, NT>(a, at, L, n, start, start, lane, rows, old_weights, stats[warp], logits_at);
+    score_segment<D, KV, NT>(a, at, L, n, start, start, lane, rows, mine, stats[warp], logits_at);
   else
     for (int r = lane; r < R; r += 32) stats[warp][r] = make_float2(kNoScore, 0.f);
   cp_async_wait_all();
@@ -919,7 +959,7 @@ int unit_cluster(const WeightsArgs& a, int warps, int ctas) {
 
 template <int D, int KV, int NT>
 cudaError_t launch_tiles(const WeightsArgs& a, const Work& ws, cudaStream_t s) {
-  using S = Shape<NT>;
+  using S = Shape<D, NT>;
   const int cluster = unit_cluster(a, S::kWarps, S::kCtas);
   auto* kernel = weights_kernel<D, KV, NT>;
   auto* unit_kernel = weights_unit_kernel<D, KV, NT>;
