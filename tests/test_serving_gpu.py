@@ -335,6 +335,37 @@ def test_attention_weights_batch_above_one_launch():
     assert (np.abs(R.f64(got) - ref) <= tol).all()
 
 
+@pytest.mark.parametrize("B,Hq,Hkv,D,n_q,pool,dtype", [
+    (150, 2, 2, 128, 1, "16", F16),     # 34 pages a warp, old weights beyond those copied ahead
+    (150, 2, 2, 64, 1, "fp8", BF16),
+    (35, 20, 2, 128, 1, "16", BF16),    # 10 rows
+    (20, 28, 2, 128, 2, "fp8", BF16),   # 28 rows
+    (20, 28, 2, 128, 2, "16", F16),
+    (60, 40, 2, 64, 1, "16", F16)])     # 20 rows
+def test_attention_weights_of_more_pages_than_a_warp_keeps(B, Hq, Hkv, D, n_q, pool, dtype):
+    _, kc, ks, bt, L, _ = weights_case([4500, 4400, 4097], Hq, Hkv, D, n_q, pool, dtype, 19)
+    g = gen(20)
+    at = torch.arange(B) % 3            # the sequences share blocks
+    bt, L = bt[at].contiguous(), L[at].contiguous()
+    q, w = randn(g, B, n_q, Hq, D, dtype=dtype) * 1.5, torch.rand(B, Hkv, bt.shape[1] * 16, generator=g)
+    scale = float(np.float32(D ** -.5))
+    ref, tol = R.attention_weights(R.f64(w), R.f64(q), kc, ks, bt, L, scale, .5, 1)
+    got = run_weights(q, kc, ks, bt, L, w, scale, .5, 1)
+    ok()
+    assert (np.abs(R.f64(got) - ref) <= tol).all()
+
+
+@pytest.mark.parametrize("Hq", [20, 56])          # 10 and 28 rows
+def test_attention_weights_of_more_pages_than_a_cluster_keeps(Hq):
+    lens = [4096, 2000] + [1] * 80
+    q, kc, ks, bt, L, w = weights_case(lens, Hq, 2, 128, 1, "16", F16, 22)
+    scale = float(np.float32(128 ** -.5))
+    ref, tol = R.attention_weights(R.f64(w), R.f64(q), kc, ks, bt, L, scale, .5, 1)
+    got = run_weights(q, kc, ks, bt, L, w, scale, .5, 1)
+    ok()
+    assert (np.abs(R.f64(got) - ref) <= tol).all()
+
+
 def test_attention_weights_bad_indexes_are_skipped_and_reported():
     q, kc, ks, bt, L, w = weights_case([64, 32, 20], 4, 2, 64, 1, "16", F16, 12, garbage=False)
     bad = bt.clone()
