@@ -23,15 +23,19 @@
 // warps both grow along the line, so unit + warp numbers every partition
 // uniquely, and a unit's partitions are consecutive.
 //
-// Measured on a GB300 (fp16, 28 q and 4 kv heads of 128): 58 us for 128 sequences,
-// median 1024 tokens (214 MB, 54 % of the measured copy bandwidth), of which the
-// first phase, at 5.8 TB/s, takes 37, the wait for the slowest neighbours and the
-// joining 4, the second phase 5 and the launch the rest; 34 us for 100 sequences of
-// up to 2048 tokens by clusters; 74 to 84 us for two 115k-token E4M3 contexts with 28
-// rows (122 MB), bound by instructions (270 a page and phase for 32 MMAs) and by the
-// logits, which are as large as K.  What was slower there: computing the logits again
-// in the second phase 85 to 90 us, K through a ring in shared memory 81 to 90 us
-// (and 87 to 90 us for the 128 sequences), two fp32 values an instruction 86 us.
+// Measured on a GB300 (28 q and 4 kv heads of 128): 53 us for 128 fp16 sequences,
+// median 1024 tokens (214 MB, 59 % of the measured copy bandwidth), of which the first
+// phase, at 5.8 TB/s, takes 37, the wait for the slowest neighbours and the joining 3,
+// the second phase 5 and the launch the rest; 34 us for 100 sequences of up to 2048
+// tokens by clusters; 67.5 us for two 115k-token E4M3 contexts with 28 rows (122 MB):
+// 42 to score, bound by each warp's own chain (2500 cycles a page, the tensor pipe busy
+// for 260 of them, three warps a scheduler), 12 of it for the logits, which are as large
+// as K; 5 to wait and join; 15 for the second phase.  What was slower in that case:
+// three or four pages on their way a warp instead of two 79 and 80 us against 78.7, two
+// pages scored at once 85, 14 or 16 warps (with fewer pages kept) 87 and 85 against 81.
+// Before q's fragments moved to shared memory (84 us): the logits computed again in the
+// second phase 85 to 90 us, K through a ring in shared memory 81 to 90 us (and 87 to 90
+// us for the 128 sequences), two fp32 values an instruction 86 us.
 //
 // K goes from global memory straight into the MMA's registers.  A dot product
 // does not care in which order the dimensions are summed, so lane (r, c) of a
