@@ -109,9 +109,11 @@ int pa_rope_append_fp8(void *q_out, const void *q, int64_t q_stride, const void 
  * with old(t) = decay * weights[b][h][t], or 0 for the last fresh_tokens tokens
  * (those appended since the last call, whose entry still holds what a former
  * token left there).  decay 0 reads no old weight.  Query i sits at position
- * L - n_q + i and attends positions up to its own, as in pa_decode; one before
- * position 0 adds nothing, nor does one whose logits are all -inf.  Entries behind
- * the context stay as they are.
+ * L - n_q + i and attends positions up to its own, as in pa_decode without a
+ * window (there is no window here: the weights are those of the whole context,
+ * and all of its blocks have to be in the table); one before position 0 adds
+ * nothing, nor does one whose logits are all -inf.  Entries behind the context stay
+ * as they are.
  *   weights: fp32 [num_seqs][num_kv_heads][weights_stride], weights_stride >=
  *   max_context_len; a row belongs to its sequence, so sequences that share
  *   blocks keep weights of their own.

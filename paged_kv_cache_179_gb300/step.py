@@ -98,9 +98,15 @@ class DecodeStep:
 
     def accumulate(self, weights, q, *, decay=1.0, fresh_tokens=0):
         """Add to weights fp32 [B][Hkv][>= max_context_len] the attention weight that
-        each cached token gets from q's rows (as ``decode`` attends, without a
-        window): what ``evict`` goes by.  The first call with a number of query
-        tokens allocates their workspace, so it cannot be one that is captured."""
+        each cached token gets from q's rows (as ``decode`` attends): what ``evict``
+        goes by.  A step whose window leaves tokens out is refused: the softmax here is
+        over the whole context, which is not what such a step attended.  The first call
+        with a number of query tokens allocates their workspace, so it cannot be one
+        that is captured; calls with one number of query tokens share it and must not
+        overlap on the device."""
+        if 0 < self.window < self.max_context_len:
+            raise ValueError(f"accumulate weighs the whole context, but this step attends the last "
+                             f"{self.window} of up to {self.max_context_len} tokens")
         n_q = 1 if q.dim() == 3 else int(q.shape[1])
         if n_q not in self._weights_ws:    # one workspace per number of query tokens
             if torch.cuda.is_current_stream_capturing():

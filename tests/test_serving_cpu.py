@@ -192,3 +192,27 @@ def test_bindings_refuse_cpu_tensors_and_wrong_types():
         _abi.pa_evict(x, x, x, x, i, i, 16, i, i, i, i)
     with pytest.raises(TypeError):
         _abi.pa_verify_drafts(i, i, i, None, i, i)
+
+
+def test_accumulate_refuses_a_step_whose_window_leaves_tokens_out(lib, monkeypatch):
+    """The weights are those of the whole context, which is not what a windowed step
+    attended; a window no shorter than the bound leaves nothing out."""
+    from paged_kv_cache_179_gb300.step import DecodeStep
+    pool = torch.zeros(8, 2, 16, 64, dtype=torch.float16)
+    q, w = torch.zeros(2, 4, 64, dtype=torch.float16), torch.zeros(2, 2, 64)
+
+    def step(window):
+        return DecodeStep(k_cache=pool, v_cache=pool, block_tables=torch.zeros(2, 4, dtype=torch.int32),
+                          context_lens=torch.zeros(2, dtype=torch.int32), max_context_len=64, scale=.125,
+                          num_q_heads=4, split_ctas=2, window=window)
+    for window in (1, 16, 63):
+        for x in (q, q[:, None].expand(2, 3, 4, 64).contiguous()):
+            with pytest.raises(ValueError, match="whole context"):
+                step(window).accumulate(w, x)
+    made = []
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(_abi, "alloc_weights_workspace", lambda *a: None)
+    monkeypatch.setattr(_abi, "pa_attention_weights", lambda *a, **kw: made.append(kw))
+    for window in (0, 64, 1000):
+        step(window).accumulate(w, q, decay=.5)
+    assert made == [dict(decay=.5, fresh_tokens=0)] * 3
