@@ -44,8 +44,9 @@ enum { PA_F32 = 3 };
  * cos and sin multiplied by `amplitude` (1 unless a long-context scaling asks
  * for more); elements behind rotary_dim pass through.  The pair is
  * (i, i + rotary_dim / 2) when adjacent is 0, and (2i, 2i + 1) when it is 1.
- * Angles are reduced exactly (64-bit fractions of a turn), so far positions
- * lose nothing; the rotation is made in fp32 and rounded once.
+ * Angles are reduced in 64-bit fractions of a turn: inv_freq's to 2^-63 of a turn
+ * (for |inv_freq| up to 2^40), its product with the position exactly, so far
+ * positions lose nothing; the rotation is made in fp32 and rounded once.
  *   inv_freq: HOST, radians per position, finite; freq_axis: HOST, the axis of
  *   each pair, in [0, num_axes), or NULL when num_axes is 1.  Both are read
  *   during the call.  num_axes 1..4; rotary_dim a multiple of 16 in

@@ -2,7 +2,8 @@
 //
 // Pair i of a head turns by the angle pos[axis(i)] * f_i: x' = x cos - y sin,
 // y' = y cos + x sin.  The angle is reduced in fixed point: f_i is held as a
-// 64-bit fraction of a turn, the 64-bit product with the position drops whole
+// 64-bit fraction of a turn (made on the host to 2^-63 of a turn, whatever the
+// number of whole turns), the 64-bit product with the position drops whole
 // turns by itself, and the upper 32 bits, read as a signed number, are the angle
 // in (-1/2, 1/2] turns to 2^-32.  sincospif takes it from there, so a position
 // of a million costs what position 1 does and loses nothing, without 64-bit

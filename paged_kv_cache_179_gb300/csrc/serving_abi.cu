@@ -16,6 +16,22 @@ int cuda_status(cudaError_t e) { return e == cudaSuccess ? PA_OK : PA_ERR_CUDA; 
 constexpr int kMaxContext = 1 << 30;   // the kernels step beyond a token's index in 32 bits
 bool is_act(int dtype) { return dtype == PA_F16 || dtype == PA_BF16; }
 
+// f radians as a fraction of a turn, modulo 1, in units of 2^-64.  1 / 2 pi as the sum
+// of two doubles and the first product's rounding (the fma gives it exactly) make
+// f / 2 pi to 2^-104 of itself, which is below 2^-64 for every f up to 2^40; one
+// division would leave 2^-53 of it, times the position: 7e-7 rad for 1 radian at
+// position 2^31.
+uint64_t turn_fraction(double f) {
+  constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;   // 1 / 2 pi
+  const double t = f * kHi, rest = std::fma(f, kHi, -t) + f * kLo;
+  auto fixed = [](double x) {
+    x -= std::trunc(x);   // exact
+    const uint64_t m = static_cast<uint64_t>(std::ldexp(std::fabs(x), 64));
+    return x < 0 ? 0 - m : m;
+  };
+  return fixed(t) + fixed(rest);
+}
+
 // Checks the rotation's arguments and fills the launch's table.
 int rope_table(const pa_rope_spec* spec, int head_dim, RopeTable* t) {
   if (spec == nullptr || spec->inv_freq == nullptr) return PA_ERR_INVALID_ARG;
@@ -30,9 +46,7 @@ int rope_table(const pa_rope_spec* spec, int head_dim, RopeTable* t) {
     if (!std::isfinite(f)) return PA_ERR_INVALID_ARG;
     const int axis = spec->freq_axis != nullptr ? spec->freq_axis[i] : 0;
     if (axis < 0 || axis >= spec->num_axes) return PA_ERR_INVALID_ARG;
-    double turns = f / 6.283185307179586476925286766559;
-    turns -= std::floor(turns);                       // whole turns do not matter
-    t->turns[i] = turns >= 1.0 ? 0 : static_cast<uint64_t>(std::ldexp(turns, 64));
+    t->turns[i] = turn_fraction(f);                   // whole turns do not matter
     t->axis[i] = static_cast<uint8_t>(axis);
   }
   return PA_OK;

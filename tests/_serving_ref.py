@@ -2,6 +2,8 @@
 the small pools that their tests share."""
 from __future__ import annotations
 
+from fractions import Fraction
+
 import numpy as np
 import torch
 
@@ -45,6 +47,31 @@ def rope(x, positions, inv_freq, axis, adjacent, amplitude=1.0):
         y[:, :, lo] = x[:, :, lo] * c - x[:, :, hi] * s
         y[:, :, hi] = x[:, :, hi] * c + x[:, :, lo] * s
     return y
+
+
+def inverse_two_pi(bits=320):
+    """1 / 2 pi as a Fraction, to about 2^-bits (Machin: pi / 4 = 4 atan 1/5 - atan 1/239)."""
+    def atan(n):
+        term = (1 << bits) // n
+        total, k = term, 3
+        while term:
+            term //= -n * n
+            total += term // k
+            k += 2
+        return total
+    return Fraction(1 << bits, 8 * (4 * atan(5) - atan(239)))
+
+
+def rope_angles(positions, inv_freq):
+    """positions [T] times inv_freq [pairs] (doubles, as given), reduced to one turn without
+    rounding and then to 64 bits: radians [T][pairs]."""
+    turn = inverse_two_pi()
+    out = np.empty((len(positions), len(inv_freq)))
+    for i, f in enumerate(inv_freq):
+        step = Fraction(float(f)) * turn
+        for t, p in enumerate(positions):
+            out[t, i] = 2 * np.pi * float((int(p) * step + Fraction(1, 2)) % 1 - Fraction(1, 2))
+    return out
 
 
 def keys(k_cache, k_scale, table, h, L):

@@ -79,6 +79,30 @@ def test_rope(T, Hq, Hkv, D, rotary, axes, adjacent, dtype):
     assert torch.equal(dev.cpu(), qkv)                              # the inputs stay as they are
 
 
+@pytest.mark.parametrize("exponents", [(-20, 0), (0, 20), (20, 40)])
+def test_rope_angles_of_any_frequency_at_far_positions(exponents):
+    """Whole turns are dropped without rounding: frequencies up to 2^40 radians a
+    position (of either sign) and positions up to 2^31, against exact fractions.  The
+    tolerance is the rotation's own: the fraction of a frequency is within 2^-63 of a
+    turn, which position 2^31 makes 2^-32, one of the terms that rope_tol counts."""
+    g = gen(61)
+    T, half = 12, 32
+    inv = 2. ** np.linspace(*exponents, half) * (1 + torch.rand(half, generator=g, dtype=torch.float64).numpy())
+    inv = np.minimum(inv, 2. ** 40)
+    inv[1::3] *= -1
+    pos = torch.randint(-2 ** 31, 2 ** 31 - 1, (T,), generator=g, dtype=torch.int64).to(torch.int32)
+    pos[:4] = torch.tensor([2 ** 31 - 1, -2 ** 31, 1, 0], dtype=torch.int32)
+    x = randn(g, T, 3, 2 * half)
+    out = torch.empty(T, 3, 2 * half, dtype=F16, device="cuda")
+    _abi.pa_rope(out, x.cuda(), None, None, pos.cuda(), _abi.RopeSpec(inv))
+    ok()
+    a = R.rope_angles(pos.tolist(), inv)[:, None]
+    v = R.f64(x)
+    lo, hi = v[..., :half], v[..., half:]
+    ref = np.concatenate([lo * np.cos(a) - hi * np.sin(a), hi * np.cos(a) + lo * np.sin(a)], -1)
+    assert (np.abs(R.f64(out) - ref) <= rope_tol(v, ref, F16)).all()
+
+
 def test_rope_in_place_one_side_and_empty():
     g = gen(3)
     spec, inv, axis = spec_for(32, 1, False)
