@@ -233,7 +233,7 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums) {
 template <bool ONE, int MOVE>
 __global__ void __launch_bounds__(kSelectThreads, 2)
 evict_select_kernel(const __grid_constant__ EvictArgs a) {
-  extern __shared__ int smem[];
+  extern __shared__ __align__(16) int smem[];   // read and written 16 bytes at a time
   int* copies = smem;                    // [bin][copy]
   int* hist = smem + kCopies * kBins;    // [digit][bin], of this CTA
   __shared__ int warp_sums[kSelectWarps];
