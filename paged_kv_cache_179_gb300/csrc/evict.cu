@@ -24,29 +24,7 @@
 namespace pa {
 namespace {
 
-// ------------------------------------------------------------------- clusters
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
-// All threads of the cluster; shared memory written before it is seen after it.
-__device__ __forceinline__ void cluster_sync() {
-  __syncwarp();
-  asm volatile("barrier.cluster.arrive.release.aligned;\n"
-               "barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// What p (in this CTA's shared memory) is in CTA `rank`'s.
-__device__ __forceinline__ uint32_t in_cluster(const void* p, uint32_t rank) {
-  uint32_t at;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
-  return at;
-}
+// ------------------------------------------------- distributed shared memory
 __device__ __forceinline__ int ld_cluster(const int* p, uint32_t rank) {
   int v;
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(in_cluster(p, rank)));

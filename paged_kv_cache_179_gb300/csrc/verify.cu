@@ -31,29 +31,9 @@ namespace {
 constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
-// The cluster's barrier, in two halves, by all its threads; shared-memory writes
-// before the arrival are seen after the wait.
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 // Stores v at the address that `p` (this CTA's shared memory) has in CTA `rank`.
 __device__ __forceinline__ void st_cluster(void* p, uint32_t rank, uint64_t v) {
-  uint32_t at;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(v) : "memory");
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(in_cluster(p, rank)), "l"(v) : "memory");
 }
 
 __device__ __forceinline__ float to_f32(float x) { return x; }
@@ -283,9 +263,7 @@ verify_kernel(const VerifyArgs a) {
     } else {
       if (pass == 0) cluster_wait();
       if (lane < size) st_cluster(&sums[pass][mine], lane, sum);
-      __syncwarp();
-      cluster_arrive();
-      cluster_wait();
+      cluster_sync();
     }
     all = sums[pass];
     total = 0;

@@ -23,3 +23,16 @@ def test_dynamic_shared_memory_states_its_alignment():
             stated = re.search(r"__align__\((\d+)\)", decl)
             assert stated and int(stated.group(1)) >= 16, f"{name}: {decl}"
     assert found >= 5
+
+
+def test_cluster_barriers_follow_a_warp_barrier():
+    """barrier.cluster's .aligned forms need all threads of a warp at the same instruction:
+    each one stands right behind a __syncwarp(), which brings them there whatever loop or
+    branch came before."""
+    found = 0
+    for name, text in sources():
+        for m in re.finditer(r'asm volatile\(\s*"barrier\.cluster', text):
+            found += 1
+            before = text[:m.start()].rstrip()
+            assert before.endswith("__syncwarp();"), f"{name}: {before[-60:]!r}"
+    assert found >= 2
