@@ -95,6 +95,11 @@ SERVING_SIGNATURES = {
     "pa_verify_drafts": ([_vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i32, _i32, _i32, _i32,
                           _vp], _i32),
 }
+# the failure-path test of include/pa_serving_test.h
+SERVING_TEST_SIGNATURES = {
+    "pa_test_weights_timeout": ([_vp, _i64, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32,
+                                 _i32, _f32, _i32, _i32, ctypes.c_uint64, _vp, _sz, _vp], _i32),
+}
 
 _lock = threading.Lock()
 _lib = None
@@ -121,7 +126,8 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
                                        "or python -m paged_kv_cache_179_gb300.build")
                 _build.build()
             L = ctypes.CDLL(_build.LIB)
-            for name, (args, res) in (*SIGNATURES.items(), *SERVING_SIGNATURES.items()):
+            for name, (args, res) in (*SIGNATURES.items(), *SERVING_SIGNATURES.items(),
+                                      *SERVING_TEST_SIGNATURES.items()):
                 fn = getattr(L, name)
                 fn.argtypes = args
                 fn.restype = res
@@ -792,6 +798,23 @@ def pa_attention_weights_fp8(weights, q, k_cache, k_scale, block_tables, context
           weights.shape[2], _ptr(q), _ptr(k_cache), _ptr(k_scale), _ptr(block_tables),
           block_tables.shape[1], _ptr(context_lens), int(max_context_len), B, Hq, Hkv, D, bs, NB,
           float(scale), float(decay), int(fresh_tokens), nq, _act_code(q.dtype), _ptr(workspace),
+          _ws_bytes(workspace, dev), _stream(dev))
+
+
+def pa_test_weights_timeout(weights, q, k_cache, block_tables, context_lens, max_context_len: int,
+                            scale: float, workspace, *, silent_warp: int, limit_ns: int) -> None:
+    """Failure-path test: pa_attention_weights (q [B][Hq][D], decay 0) whose warp
+    ``silent_warp`` announces nothing, so that those who wait for it give up after
+    ``limit_ns``, set PA_STATUS_TIMEOUT and leave their weights as they were."""
+    dev = q.device
+    B, nq, Hq, Hkv, D, bs, NB = _weights_args(weights, q, k_cache, block_tables, context_lens,
+                                              None, dev)
+    if nq != 1 or bs != 16:
+        raise ValueError("one query token and blocks of 16 tokens")
+    _call(load().pa_test_weights_timeout, "pa_test_weights_timeout", _ptr(weights),
+          weights.shape[2], _ptr(q), _ptr(k_cache), _ptr(block_tables), block_tables.shape[1],
+          _ptr(context_lens), int(max_context_len), B, Hq, Hkv, D, NB, float(scale),
+          _act_code(q.dtype), int(silent_warp), int(limit_ns), _ptr(workspace),
           _ws_bytes(workspace, dev), _stream(dev))
 
 

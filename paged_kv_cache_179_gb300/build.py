@@ -40,7 +40,7 @@ def nvcc() -> str:
 
 def _inputs():
     return ([os.path.join(CSRC, s) for s in SOURCES] + [os.path.join(CSRC, h) for h in HEADERS]
-            + [os.path.join(INCLUDE, h) for h in ("pa.h", "pa_serving.h")] + [os.path.abspath(__file__)])
+            + [os.path.join(INCLUDE, h) for h in ("pa.h", "pa_serving.h", "pa_serving_test.h")] + [os.path.abspath(__file__)])
 
 
 def up_to_date() -> bool:

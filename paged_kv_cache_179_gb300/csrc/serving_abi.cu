@@ -5,6 +5,7 @@
 
 #include "pa_launch.h"
 #include "pa_serving.h"
+#include "pa_serving_test.h"
 #include "serving_launch.h"
 
 using namespace pa;
@@ -127,7 +128,6 @@ int attention_weights(WeightsArgs a, int block_size, float scale, int dtype, siz
     return PA_ERR_WORKSPACE;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.wide = aligned(a.k_cache, 32);
-  a.wait_limit_ns = kWaitLimitNs;
   return cuda_status(launch_weights(a, fp8, dtype == PA_BF16, static_cast<cudaStream_t>(stream)));
 }
 
@@ -295,6 +295,8 @@ int pa_attention_weights(float* weights, int64_t weights_stride, const void* q,
   a.q_tokens = queries_per_seq;
   a.decay = decay;
   a.fresh = fresh_tokens;
+  a.wait_limit_ns = kWaitLimitNs;
+  a.silent_warp = -1;
   return attention_weights(a, block_size, scale, dtype, workspace_bytes, false, stream);
 }
 
@@ -326,7 +328,40 @@ int pa_attention_weights_fp8(float* weights, int64_t weights_stride, const void*
   a.q_tokens = queries_per_seq;
   a.decay = decay;
   a.fresh = fresh_tokens;
+  a.wait_limit_ns = kWaitLimitNs;
+  a.silent_warp = -1;
   return attention_weights(a, block_size, scale, dtype, workspace_bytes, true, stream);
+}
+
+int pa_test_weights_timeout(float* weights, int64_t weights_stride, const void* q,
+                            const void* k_cache, const int32_t* block_tables,
+                            int max_blocks_per_seq, const int32_t* context_lens,
+                            int max_context_len, int num_seqs, int num_q_heads, int num_kv_heads,
+                            int head_dim, int num_blocks, float scale, int dtype, int silent_warp,
+                            uint64_t limit_ns, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+  if (limit_ns == 0 || limit_ns > kWaitLimitNs) return PA_ERR_INVALID_ARG;
+  if (num_seqs <= 0 || num_seqs > kWeightsMaxBatch || silent_warp < 0) return PA_ERR_INVALID_ARG;
+  if (max_context_len <= kWeightsClusterPages * 16) return PA_ERR_UNSUPPORTED;   // no warp waits
+  WeightsArgs a{};
+  a.weights = weights;
+  a.stride = weights_stride;
+  a.q = q;
+  a.k_cache = k_cache;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.workspace = workspace;
+  a.mbs = max_blocks_per_seq;
+  a.B = num_seqs;
+  a.Hq = num_q_heads;
+  a.Hkv = num_kv_heads;
+  a.D = head_dim;
+  a.num_blocks = num_blocks;
+  a.max_context_len = max_context_len;
+  a.q_tokens = 1;
+  a.wait_limit_ns = limit_ns;
+  a.silent_warp = silent_warp;
+  return attention_weights(a, 16, scale, dtype, workspace_bytes, false, stream);
 }
 
 int pa_evict(void* k_cache, void* v_cache, const float* weights, int64_t weights_stride,

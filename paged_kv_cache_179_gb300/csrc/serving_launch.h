@@ -66,8 +66,10 @@ struct WeightsArgs {
   int fresh;                   // tokens whose old weight is 0
   bool wide;                   // k_cache is 32-byte aligned
   uint64_t wait_limit_ns;      // time limit of a warp's wait for others
+  int silent_warp;             // of the launch, whose statistics are not announced (-1: none)
 };
-constexpr int kWeightsMaxBatch = 512;    // sequences per launch pair
+constexpr int kWeightsMaxBatch = 512;    // sequences per launch
+constexpr int kWeightsClusterPages = 256;   // a longer bound takes the cooperative launch
 constexpr int kWeightsMaxRows = 32;      // query rows per pass
 size_t weights_workspace_bytes(int B, int Hkv, int max_context_len, int rows);
 cudaError_t launch_weights(const WeightsArgs& a, bool fp8, bool bf16, cudaStream_t s);

@@ -792,7 +792,7 @@ weights_kernel(const __grid_constant__ WeightsArgs a, Work ws) {
   };
   score_pages<D, KV, NT>(a, ws, cum, start, end, w, lane, rows, mine, logits_at);
   __syncwarp();   // the release covers what the other lanes have written
-  if (lane == 0 && w < line.workers) st_release_gpu_b32(ws.sync + 2 + w, call);
+  if (lane == 0 && w < line.workers && w != a.silent_warp) st_release_gpu_b32(ws.sync + 2 + w, call);
   cp_async_wait_all();   // the old weights, each lane's own copies
   __syncwarp();
 
@@ -952,7 +952,7 @@ int weights_grid(const WeightsArgs& a, int warps, int ctas) {
 // has a page, or while a warp has more than 16.
 int unit_cluster(const WeightsArgs& a, int warps, int ctas) {
   const int64_t pages = (static_cast<int64_t>(a.max_context_len) + 15) / 16;
-  if (pages > 256) return 0;
+  if (pages > kWeightsClusterPages) return 0;
   const int64_t units = static_cast<int64_t>(a.B) * a.Hkv, slots = static_cast<int64_t>(ctas) * device_sm_count();
   int c = 1;
   while (c < kMaxCluster && ((units * 2 * c <= slots && pages > warps * c) || pages > 16 * warps * c)) c *= 2;

@@ -216,3 +216,27 @@ def test_accumulate_refuses_a_step_whose_window_leaves_tokens_out(lib, monkeypat
     for window in (0, 64, 1000):
         step(window).accumulate(w, q, decay=.5)
     assert made == [dict(decay=.5, fresh_tokens=0)] * 3
+
+
+def test_weights_timeout_hook(lib):
+    """Declared in a header of its own, bound and exported; what it refuses on the host."""
+    text = open(os.path.join(ROOT, "include", "pa_serving_test.h")).read()
+    text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
+    decl = re.search(r"pa_test_weights_timeout\s*\((.*?)\);", text, flags=re.S).group(1)
+    assert set(re.findall(r"\b(pa_[a-z0-9_]+)\s*\(", text)) == set(_abi.SERVING_TEST_SIGNATURES)
+    assert len(_abi.SERVING_TEST_SIGNATURES["pa_test_weights_timeout"][0]) == len(decl.split(","))
+
+    def call(**kw):
+        a = dict(w=FAKE, st=8000, q=FAKE, k=FAKE, bt=FAKE, mbs=500, cl=FAKE, mx=5000, B=2, Hq=8, Hkv=2,
+                 D=64, NB=32, scale=.125, dtype=0, silent=0, limit=1000, ws=FAKE, n=1 << 40)
+        a.update(kw)
+        return lib.pa_test_weights_timeout(
+            a["w"], a["st"], a["q"], a["k"], a["bt"], a["mbs"], a["cl"], a["mx"], a["B"], a["Hq"],
+            a["Hkv"], a["D"], a["NB"], a["scale"], a["dtype"], a["silent"], a["limit"], a["ws"],
+            a["n"], None)
+    for bad in (dict(limit=0), dict(limit=3_000_000_000), dict(B=0), dict(B=513), dict(silent=-1),
+                dict(w=None), dict(q=ODD), dict(st=4999), dict(mx=8001)):
+        assert call(**bad) == INV, bad
+    for bad in (dict(mx=4096), dict(D=96), dict(Hq=66)):
+        assert call(**bad) == UNS, bad
+    assert call(ws=None) == WSP
