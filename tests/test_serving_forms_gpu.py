@@ -115,3 +115,135 @@ def test_rope_append_fp8_of_many_tokens():
         _abi.pa_cache_append_fp8(kr, v.contiguous(), *other, slots)
         ok()
         assert torch.equal(qo, q2) and all(torch.equal(x, y) for x, y in zip(state, other))
+
+
+# ------------------------------------------------------------------ eviction
+# A cut is moved within the selection's launch while keep x head_dim is at most 16384 a
+# CTA of the unit (1, 2, 4 or 8 for bounds to 8192, 16384, 32768 and longer), else by a
+# launch of its own; a selection over more than 65536 tokens reads its weights anew.
+CUTS = [  # lens, Hkv, D, keep, first, recent, pool, kind; the last page of a cut is not full
+    ([2000, 600, 40, 515], 2, 128, 515, 4, 100, "fp8", "random"),
+    ([2000, 600, 40, 515], 2, 64, 515, 4, 100, "fp8", "ties"),
+    ([1500, 129], 3, 128, 129, 0, 0, "fp8", "odd"),            # nine pages, the last of one row
+    ([1500, 1023, 1024, 0], 2, 128, 1023, 4, 100, "16", "random"),
+    ([1500, 1300], 1, 64, 1029, 0, 1029, "16", "random"),      # the recent ones alone
+    ([900, 70], 2, 128, 131, 131, 0, "16", "ties"),            # the first ones alone
+    ([30000, 20000], 1, 128, 777, 5, 20, "fp8", "odd"),        # four CTAs a unit
+    ([9000, 8193], 1, 128, 401, 0, 7, "16", "equal"),          # two
+    ([70000, 66000, 9], 1, 64, 2101, 1, 2, "16", "ties"),      # more than the registers hold
+    ([70000, 65537], 1, 128, 1111, 3, 64, "fp8", "random"),
+    ([66000, 900], 2, 64, 130, 3, 64, "fp8", "odd"),           # the same, moved within the selection
+]
+
+
+def moves_along(max_len, keep, D):
+    cluster = 1
+    while cluster < 8 and max_len > cluster * 8192:
+        cluster *= 2
+    return keep * D <= 16384 * cluster
+
+
+def check_evict(got, pools, scales, w, bt, L, spare, keep, first, recent):
+    p, s, w_out, tables, new, kept = got
+    ref_new, ref_kept, ref_tables = R.evict(pools, scales, w.numpy(), bt, L.numpy(), spare, keep, first, recent)
+    assert np.array_equal(new.cpu().numpy(), ref_new)
+    assert torch.equal(tables.cpu(), ref_tables)
+    kept, w_out = kept.cpu().numpy(), w_out.cpu().numpy()
+    for (b, h), at in ref_kept.items():
+        assert np.array_equal(kept[b, h, :len(at)], at) and (kept[b, h, len(at):] == -3).all()
+        assert np.array_equal(w_out[b, h, :len(at)], w[b, h].numpy()[at], equal_nan=True)
+        assert (w_out[b, h, len(at):] == -7).all()
+    for a, b in zip(p, pools):                                  # whole pools, bit for bit
+        assert torch.equal(a.cpu().view(torch.uint8), b.view(torch.uint8))
+    for a, b in zip(s, scales):
+        assert b is None or torch.equal(a.cpu(), b)
+
+
+@pytest.mark.parametrize("lens,Hkv,D,keep,first,recent,pool,kind", CUTS)
+def test_evict_in_two_launches(lens, Hkv, D, keep, first, recent, pool, kind):
+    case = evict_case(lens, Hkv, D, keep, pool, F16, keep, kind)
+    pools, scales, w, bt, L, spare = case
+    assert moves_along(bt.shape[1] * 16, keep, D) == (keep == 130)
+    check_evict(run_evict(*case, keep, first, recent), *case, keep, first, recent)
+    ok()
+
+
+def test_evict_forms_are_what_the_comment_says():
+    """Of the cuts above, each of the two moves of either pool and head size, and all three
+    selections of long and of short bounds, are made by some."""
+    made = {(pool, D, moves_along(max(lens), keep, D)) for lens, _, D, keep, _, _, pool, _ in CUTS}
+    assert {(pool, D, False) for pool in ("16", "fp8") for D in (64, 128)} <= made
+    assert {moves_along(max(lens), keep, D) for lens, _, D, keep, *_ in CUTS if max(lens) > 65536} == {True, False}
+
+
+@pytest.mark.parametrize("pool,D", [("16", 128), ("fp8", 64)])
+def test_evict_in_two_launches_captured_and_on_another_stream(pool, D):
+    """The move is a programmatic dependent of the selection: replayed from a graph, with
+    other weights in the same tensors, and behind other work of its stream."""
+    lens, Hkv, keep = [3000, 700, 610], 2, 613
+    pools, scales, w, bt, L, spare = evict_case(lens, Hkv, D, keep, pool, F16, 5, "random")
+    assert not moves_along(bt.shape[1] * 16, keep, D)
+    d, sc = [t.cuda() for t in pools], [None if t is None else t.cuda() for t in scales]
+    wd, btd, Ld, spd = w.cuda(), bt.cuda(), L.cuda(), spare.cuda()
+    w_out = torch.empty(3, Hkv, keep + 3, device="cuda")
+    tables, new = torch.empty_like(spd), torch.empty(3, dtype=torch.int32, device="cuda")
+    kept = torch.empty(3, Hkv, keep, dtype=torch.int32, device="cuda")
+
+    def call():
+        args = (wd, w_out, btd, Ld, bt.shape[1] * 16, spd, tables, new, kept)
+        kw = dict(first_tokens=3, recent_tokens=50)
+        if pool == "16":
+            _abi.pa_evict(*d, *args, **kw)
+        else:
+            _abi.pa_evict_fp8(*d, *sc, *args, **kw)
+
+    def fresh(weights):
+        for t, x in zip(d + [t for t in sc if t is not None], pools + [t for t in scales if t is not None]):
+            t.copy_(x)
+        wd.copy_(weights)
+        for t, x in ((w_out, -7), (tables, -9), (new, -5), (kept, -3)):
+            t.fill_(x)
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    side = torch.cuda.Stream()
+    for i, weights in enumerate((w, w.flip(-1).contiguous(), w)):
+        fresh(weights)
+        if i == 2:
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                call()
+            torch.cuda.current_stream().wait_stream(side)
+        else:
+            graph.replay()
+        check_evict((d, sc, w_out, tables, new, kept), [t.clone() for t in pools],
+                    [None if t is None else t.clone() for t in scales], weights, bt, L, spare, keep, 3, 50)
+        ok()
+
+
+@pytest.mark.parametrize("pool", ["16", "fp8"])
+def test_evict_in_two_launches_skips_and_reports_bad_blocks(pool):
+    keep = 611
+    pools, scales, w, bt, L, spare = evict_case([1500, 900], 1, 64, keep, pool, F16, 6, "random")
+    NB = pools[0].shape[0]
+    want = [t.clone() for t in pools], [None if t is None else t.clone() for t in scales]
+    R.evict(*want, w.numpy(), bt, L.numpy(), spare, keep, 0, 0)
+    bad = spare.clone()
+    bad[0, 1], bad[1, keep // 16] = NB, -1          # two pages that are not written
+    p, s, _, tables, new, kept = run_evict(pools, scales, w, bt, L, bad, keep, 0, 0)
+    assert _abi.pa_get_status() == (_abi.PA_ERR_BOUNDS, _abi.PA_STATUS_BAD_BLOCK)
+    for got, start, full in zip(p, pools, want[0]):
+        full = full.clone()
+        for d in (spare[0, 1], spare[1, keep // 16]):
+            full[int(d)] = start[int(d)]
+        assert torch.equal(got.cpu(), full)
+    assert new.tolist() == [keep, keep] and torch.equal(tables.cpu(), bad)
+    none = bt.clone()
+    none[1] = NB + 5                                # nothing of the second one can be read
+    p, s, *_ = run_evict(pools, scales, w, none, L, spare, keep, 0, 0)
+    assert _abi.pa_get_status() == (_abi.PA_ERR_BOUNDS, _abi.PA_STATUS_BAD_BLOCK)
+    for got, start, full in zip(p, pools, want[0]):
+        full = full.clone()
+        full[spare[1].long()] = start[spare[1].long()]
+        assert torch.equal(got.cpu(), full)
