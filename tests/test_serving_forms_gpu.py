@@ -247,3 +247,24 @@ def test_evict_in_two_launches_skips_and_reports_bad_blocks(pool):
         full = full.clone()
         full[spare[1].long()] = start[spare[1].long()]
         assert torch.equal(got.cpu(), full)
+
+
+# ---------------------------------------------------------- attention weights
+# Bounds up to 4096 take clusters, longer ones the cooperative launch; 8, 16 and 32 query
+# rows, both head sizes, and four kinds of pool and query: 48 kernels.
+@pytest.mark.parametrize("bound", [512, 5008])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("pool,dtype", [("16", F16), ("16", BF16), ("fp8", F16), ("fp8", BF16)])
+@pytest.mark.parametrize("group,n_q", [(7, 1), (5, 3), (7, 4)])
+def test_attention_weights_of_every_kind(bound, D, pool, dtype, group, n_q):
+    lens, Hkv = [500, 33, 0, 272, 2], 2
+    q, kc, ks, bt, L, w = weights_case(lens, Hkv * group, Hkv, D, n_q, pool, dtype, D + group + n_q)
+    wide = torch.full((len(lens), bound // 16), -1, dtype=torch.int32)
+    wide[:, :bt.shape[1]] = bt
+    w = torch.rand(len(lens), Hkv, bound + 4, generator=gen(3))
+    scale = float(np.float32(D ** -.5))
+    ref, tol = R.attention_weights(R.f64(w), R.f64(q), kc, ks, wide, L, scale, .5, n_q)
+    got = R.f64(run_weights(q, kc, ks, wide, L, w, scale, .5, n_q))
+    ok()
+    assert (np.abs(got - ref) <= tol).all()
+    assert np.array_equal(got[1, :, 33:], R.f64(w)[1, :, 33:])      # entries behind the context
