@@ -268,3 +268,51 @@ def test_attention_weights_of_every_kind(bound, D, pool, dtype, group, n_q):
     ok()
     assert (np.abs(got - ref) <= tol).all()
     assert np.array_equal(got[1, :, 33:], R.f64(w)[1, :, 33:])      # entries behind the context
+
+
+# -------------------------------------------------------------- calls at once
+def test_calls_at_once_on_two_streams():
+    """Two long weights calls (cooperative launches) with a workspace each, an eviction and
+    a verification, on two streams that do not wait for each other, many times over: each
+    gives what it gives alone."""
+    sides = []
+    for i in range(2):
+        lens, Hkv, D, keep = [20000 - 7000 * i, 300, 9000], 2, 64, 700
+        q, kc, ks, bt, L, w = weights_case(lens, 8, Hkv, D, 1, "16", F16, 30 + i, garbage=False)
+        nb, kb = kc.shape[0], (keep + 15) // 16
+        room = torch.zeros(3 * kb, Hkv, 16, D, dtype=F16)
+        spare = torch.arange(nb, nb + 3 * kb, dtype=torch.int32).view(3, kb)
+        p = torch.softmax(torch.randn(5, 3, 33000, generator=gen(i)) * 3, -1)
+        sides.append(dict(
+            stream=torch.cuda.Stream(), mx=bt.shape[1] * 16, w=torch.zeros_like(w).cuda(), q=q.cuda(), bt=bt.cuda(),
+            L=L.cuda(), k=torch.cat([kc, room]).cuda(), v=torch.cat([kc, room]).cuda(), spare=spare.cuda(),
+            new=torch.empty(3, dtype=torch.int32, device="cuda"), p=p.cuda(), u=torch.rand(5, 3, generator=gen(i)).cuda(),
+            kept=torch.empty(3, Hkv, keep, dtype=torch.int32, device="cuda"),
+            x=torch.randint(0, 33000, (5, 2), generator=gen(i), dtype=torch.int32).cuda(),
+            out=torch.empty(5, 3, dtype=torch.int32, device="cuda"), acc=torch.empty(5, dtype=torch.int32, device="cuda"),
+            ws=_abi.alloc_weights_workspace(3, 8, Hkv, bt.shape[1] * 16, 1, "cuda")))
+
+    def calls(s):
+        for n in ("w", "kept", "out"):      # entries behind a sequence's own are left as they are
+            s[n].zero_()
+        _abi.pa_attention_weights(s["w"], s["q"], s["k"], s["bt"], s["L"], s["mx"], .125, s["ws"], decay=0.)
+        _abi.pa_evict(s["k"], s["v"], s["w"], None, s["bt"], s["L"], s["mx"], s["spare"], None, s["new"], s["kept"],
+                      first_tokens=2, recent_tokens=50)
+        _abi.pa_verify_drafts(s["out"], s["acc"], s["p"], None, s["x"], s["u"])
+
+    results = ("w", "k", "v", "new", "kept", "out", "acc")
+    alone = []
+    for s in sides:
+        calls(s)
+        ok()
+        alone.append({n: s[n].clone() for n in results})
+    torch.cuda.synchronize()
+    for _ in range(50):
+        for s in sides:
+            with torch.cuda.stream(s["stream"]):
+                calls(s)
+    torch.cuda.synchronize()
+    ok()
+    for s, want in zip(sides, alone):
+        for n in results:
+            assert torch.equal(s[n], want[n]), n
