@@ -316,3 +316,34 @@ def test_calls_at_once_on_two_streams():
     for s, want in zip(sides, alone):
         for n in results:
             assert torch.equal(s[n], want[n]), n
+
+
+# --------------------------------------------------------------- verification
+def test_verify_shares_over_a_product_grid():
+    """The first token out has the target's distribution, whatever the drafts: over every
+    pair of an N x N grid of u's the shares are those of p to the grid's steps.  The
+    acceptance of draft x is u q(x) < p(x): its share min(1, p(x) / q(x)) is met to 1 / N
+    (N (+-1 / 2) of N points, and one more for a point on the border); a rejected row draws
+    from the rest over the same even grid of the second u, each token to 1 / N again.
+    Token t gets its share as a draft, weighted by q(t) (1 / N), and from the rejections, whose
+    weights add up to at most 1 (the acceptances' 1 / N and the draw's 1 / N): 3 / N."""
+    N, V = 64, 6
+    p = torch.tensor([.4, .3, .15, .1, .05, 0.])
+    q = torch.tensor([.05, .1, .15, .3, .1, .3])
+    grid = (torch.arange(N) + .5) / N
+    u = torch.cartesian_prod(grid, grid).cuda()
+    count = torch.zeros(V, dtype=torch.float64)
+    for x in range(V):
+        out = torch.empty(N * N, 2, dtype=torch.int32, device="cuda")
+        acc = torch.empty(N * N, dtype=torch.int32, device="cuda")
+        _abi.pa_verify_drafts(out, acc, p.expand(N * N, 2, V).contiguous().cuda(),
+                              q.expand(N * N, 1, V).contiguous().cuda(),
+                              torch.full((N * N, 1), x, dtype=torch.int32, device="cuda"), u)
+        ok()
+        first = torch.bincount(out[:, 0].cpu().long(), minlength=V)
+        assert first.sum() == N * N and first[5] == 0          # a token without weight is never drawn
+        taken = int(acc.sum())
+        assert abs(taken / N ** 2 - min(1., float(p[x] / q[x]))) <= 1 / N
+        assert first[x] == taken or p[x] > q[x]                # a rejected draft is not drawn again
+        count += float(q[x]) * first.double() / N ** 2
+    assert (count - p.double()).abs().max() <= 3 / N
