@@ -296,8 +296,8 @@ cudaError_t launch_rope(const RopeArgs& a, const RopeTable& t, bool bf16, cudaSt
   const int passes = (toks * rows + most - 1) / most;
   const int threads = (toks * rows + passes - 1) / passes * items;
   auto* kernel = bf16 ? rope_kernel<true> : rope_kernel<false>;
-  kernel<<<static_cast<unsigned>((a.T + toks - 1) / toks), threads, 0, s>>>(a, t, rows, rope_magic(rows),
-                                                                           toks);
+  const int ctas = a.T / toks + (a.T % toks != 0);   // T + toks - 1 may pass 32 bits
+  kernel<<<static_cast<unsigned>(ctas), threads, 0, s>>>(a, t, rows, rope_magic(rows), toks);
   return cudaGetLastError();
 }
 
