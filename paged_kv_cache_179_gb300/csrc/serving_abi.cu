@@ -26,8 +26,8 @@ uint64_t turn_fraction(double f) {
   constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;   // 1 / 2 pi
   const double t = f * kHi, rest = std::fma(f, kHi, -t) + f * kLo;
   auto fixed = [](double x) {
-    x -= std::trunc(x);   // exact
-    const uint64_t m = static_cast<uint64_t>(std::ldexp(std::fabs(x), 64));
+    x -= std::trunc(x);   // exact, as the product with a power of two is
+    const uint64_t m = static_cast<uint64_t>(std::fabs(x) * 0x1p64);
     return x < 0 ? 0 - m : m;
   };
   return fixed(t) + fixed(rest);
