@@ -125,9 +125,15 @@ int pa_rope_append_fp8(void *q_out, const void *q, int64_t q_stride, const void 
  *   after call, whatever their sizes.  After a status with PA_STATUS_TIMEOUT or
  *   PA_STATUS_WS_DIRTY (it held what no call leaves; results may be wrong)
  *   zero-fill it again.  Calls that share one must not overlap on the device.
+ *   Its size goes by the bounds: 512 bytes for every 16 tokens of max_context_len
+ *   of each (sequence, kv head) with up to 8 query rows a pass, twice that with up
+ *   to 16, four times with more (of at most 512 sequences).
  * One launch per pass and 512 sequences.  With max_context_len above 4096 it is
  * a cooperative one, whose warps wait, bounded by 2 s, for one another's softmax
- * statistics; only these can set PA_STATUS_TIMEOUT or PA_STATUS_WS_DIRTY.
+ * statistics; only these can set PA_STATUS_TIMEOUT or PA_STATUS_WS_DIRTY.  Its
+ * grid is sized for all SMs of the device: in a context limited to some of them
+ * it may be refused (PA_ERR_CUDA).  The launch is chosen by max_context_len, not by
+ * the lengths, so a tight bound makes short contexts faster.
  * max_context_len at most 2^30.
  * Results do not depend on the order of execution.
  */

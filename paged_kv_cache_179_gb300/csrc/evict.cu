@@ -10,9 +10,9 @@
 // Bytes: the weights once (4 a token), the kept rows of K and V read once and
 // written once.  Measured on a GB300: 29 us for 48 sequences of 1100 to 4096 tokens
 // cut to 1024 (2 fp16 kv heads of 128, 102 MB): 8.5 us to select, 16 us to move at 93
-// % of the measured copy bandwidth, the rest launches; 42 us for 8 E4M3 sequences of
+// % of the measured copy bandwidth, the rest launches; 43 us for 8 E4M3 sequences of
 // 20000 to 32768 cut to 4099 (4 kv heads of 128, 72 MB): 18 us to select, 23 us to
-// move, bound by the re-encoding's instructions (1050 a page and pool); 10.4 us for
+// move, bound by the re-encoding's instructions (1050 a page and pool); 12 to 13 us for
 // four small sequences in one launch.
 #include <mutex>
 

@@ -13,7 +13,7 @@
 // operations a pair.  HBM-bound for prompts, launch-bound for decode steps.
 // One CTA serves one or two tokens: its threads compute their cos and sin once into
 // shared memory, then walk over the tokens' heads, 32 bytes at a time.  Measured on
-// a GB300 with 28 + 4 + 4 heads of 128: 55.6 us for 16384 bf16 tokens (302 MB, 80 %
+// a GB300 with 28 + 4 + 4 heads of 128: 56.6 us for 16384 bf16 tokens (302 MB, 79 %
 // of the measured copy bandwidth), 6.1 us for 512, 4.3 us for 4 (8 heads of 64).
 // 16 tokens of the same heads take 4.2 us with 512 threads a CTA, 6.2 us with 128.
 // Prompts: 128 threads and two tokens a CTA; 256 threads 57 to 61 us, one token 63 us, four

@@ -11,8 +11,8 @@
 // values, so it is not rounded either.
 //
 // Bytes: one row of p and one of q per sequence; which ones is known only after
-// the drafts' own probabilities have been read.  Measured on a GB300: 31 to 33 us for
-// 128 sequences of 128000 fp32 tokens with draft probabilities (131 MB, 60 % of
+// the drafts' own probabilities have been read.  Measured on a GB300: 33 us for
+// 128 sequences of 128000 fp32 tokens with draft probabilities (131 MB, 58 % of
 // the measured copy bandwidth), 8.2 us for one sequence of 32000: that much is
 // the chain launch, drafts, their probabilities, row, cluster barrier, border.
 // CTAs of 256 threads at 32 registers, eight an SM (six: 39 us; 512 threads 40 us),

@@ -23,11 +23,11 @@
 // warps both grow along the line, so unit + warp numbers every partition
 // uniquely, and a unit's partitions are consecutive.
 //
-// Measured on a GB300 (28 q and 4 kv heads of 128): 53 us for 128 fp16 sequences,
-// median 1024 tokens (214 MB, 59 % of the measured copy bandwidth), of which the first
+// Measured on a GB300 (28 q and 4 kv heads of 128): 54 to 59 us for 128 fp16 sequences,
+// median 1024 tokens (212 MB, 53 to 58 % of the measured copy bandwidth), of which the first
 // phase, at 5.8 TB/s, takes 37, the wait for the slowest neighbours and the joining 3,
 // the second phase 5 and the launch the rest; 34 us for 100 sequences of up to 2048
-// tokens by clusters; 67.5 us for two 115k-token E4M3 contexts with 28 rows (122 MB):
+// tokens by clusters; 71 to 73 us for two 115k-token E4M3 contexts with 28 rows (122 MB):
 // 42 to score, bound by each warp's own chain (2500 cycles a page, the tensor pipe busy
 // for 260 of them, three warps a scheduler), 12 of it for the logits, which are as large
 // as K; 5 to wait and join; 15 for the second phase.  What was slower in that case:

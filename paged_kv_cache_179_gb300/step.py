@@ -88,7 +88,9 @@ class DecodeStep:
         """``append`` with rotary positions, in one launch: q rotated into q_out, k
         rotated into the K pool, v copied into the V pool (``spec``: an
         ``_abi.RopeSpec``; positions int32 [axes][tokens]).  Any number of
-        tokens; in an E4M3 pool each of another page."""
+        tokens; in an E4M3 pool each of another page.  With ``early_copies`` the next
+        decode must find new rows in each sequence's last two blocks alone, so it
+        may follow the append of up to 17 tokens a sequence."""
         if self.kv == "fp8":
             _abi.pa_rope_append_fp8(q_out, q, k_new, v_new, self.k_cache, self.v_cache,
                                     self.k_scale, self.v_scale, slot_mapping, positions, spec)
