@@ -24,7 +24,7 @@ SOURCES = ["abi.cu", "append.cu", "quantize.cu", "decode.cu", "decode_t2.cu",
            "decode_t4_16bit.cu", "decode_t4_e4m3.cu", "decode_tc.cu", "noalloc.cu", "copy.cu",
            "serving_abi.cu", "rope.cu", "weights.cu", "evict.cu", "verify.cu"]
 HEADERS = ["pa_launch.h", "pa_ptx.cuh", "pa_e4m3.cuh", "pa_tc.cuh", "decode_kernels.cuh",
-           "serving_launch.h"]
+           "pa_cluster.cuh", "serving_launch.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v",

@@ -16,6 +16,7 @@
 // four small sequences in one launch.
 #include <mutex>
 
+#include "pa_cluster.cuh"
 #include "pa_e4m3.cuh"
 #include "pa_launch.h"
 #include "pa_ptx.cuh"

@@ -21,6 +21,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "pa_cluster.cuh"
 #include "pa_launch.h"
 #include "pa_ptx.cuh"
 #include "serving_launch.h"

@@ -43,6 +43,7 @@
 // fragments are loaded with the same permutation.
 #include <mutex>
 
+#include "pa_cluster.cuh"
 #include "pa_e4m3.cuh"
 #include "pa_launch.h"
 #include "pa_ptx.cuh"
