@@ -1,5 +1,5 @@
-"""Thin ctypes binding of libpa (include/pa.h, include/pa_serving.h): argument
-marshalling only.
+"""Thin ctypes binding of libpa (include/pa.h, include/pa_serving.h,
+include/pa_request.h): argument marshalling only.
 
 Every function takes torch tensors, checks that they are CUDA, contiguous and
 of the expected dtype and shape, passes their device pointers and the current
@@ -27,6 +27,7 @@ PA_STATUS_NO_WORKSPACE = 16
 PA_STATUS_WS_DIRTY = 32
 PA_F32 = 3
 PA_STATUS_BAD_TOKEN = 64
+PA_STATUS_BAD_ROW = 128
 PA_DECODE_EARLY_PROLOGUE = 1
 PA_DECODE_EARLY_COPIES = 2
 
@@ -95,6 +96,22 @@ SERVING_SIGNATURES = {
     "pa_verify_drafts": ([_vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i32, _i32, _i32, _i32,
                           _vp], _i32),
 }
+# the entry points of include/pa_request.h
+_PREFILL_TAIL = [_vp, _i32, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _i32, _i32,
+                 _vp, _sz, _vp]
+REQUEST_SIGNATURES = {
+    "pa_prefill_workspace_size": ([_i32, _i32, _i32, _i32, _i32], _sz),
+    "pa_prefill": ([_vp, _vp, _i64, _vp, _vp, *_PREFILL_TAIL], _i32),
+    "pa_prefill_fp8": ([_vp, _vp, _i64, _vp, _vp, _vp, _vp, *_PREFILL_TAIL], _i32),
+    "pa_alloc_pages": ([_vp, _i32, _vp, _i32, _vp, _vp, _i32, _vp, _i32, _i32, _vp, _vp], _i32),
+    "pa_free_pages": ([_vp, _i32, _vp, _i32, _vp, _i32, _vp, _i32, _vp], _i32),
+    "pa_fork_pages": ([_vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _vp, _vp, _i32, _vp, _i32, _i32,
+                       _i32, _i32, _i32, _vp, _vp], _i32),
+    "pa_compact_workspace_size": ([_i32], _sz),
+    "pa_compact_pages": ([_vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32,
+                          _vp, _vp, _vp, _vp, _vp, _sz, _vp], _i32),
+    "pa_process_logits": ([_vp, _i64, _vp, _i64, _vp, _i32, _i32, _i32, _i32, _i32, _vp], _i32),
+}
 # the failure-path test of include/pa_serving_test.h
 SERVING_TEST_SIGNATURES = {
     "pa_test_weights_timeout": ([_vp, _i64, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32,
@@ -127,6 +144,7 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
                 _build.build()
             L = ctypes.CDLL(_build.LIB)
             for name, (args, res) in (*SIGNATURES.items(), *SERVING_SIGNATURES.items(),
+                                      *REQUEST_SIGNATURES.items(),
                                       *SERVING_TEST_SIGNATURES.items()):
                 fn = getattr(L, name)
                 fn.argtypes = args
@@ -932,3 +950,253 @@ def pa_verify_drafts(out_tokens, num_accepted, target_probs, draft_probs, draft_
     _call(load().pa_verify_drafts, "pa_verify_drafts", _ptr(out_tokens), _ptr(num_accepted),
           _ptr(target_probs), ps, _ptr(draft_probs), qs, _ptr(draft_tokens), _ptr(num_drafts),
           _ptr(uniforms), B, n, V, codes[target_probs.dtype], _stream(dev))
+
+
+# ------------------------------------------------- whole requests (pa_request.h)
+def pa_prefill_workspace_size(num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim) -> int:
+    return int(load().pa_prefill_workspace_size(int(num_seqs), int(num_tokens), int(num_q_heads),
+                                                int(num_kv_heads), int(head_dim)))
+
+
+def alloc_prefill_workspace(num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim, device):
+    """Caller-owned workspace for pa_prefill calls of up to these sizes (of any contents)."""
+    n = pa_prefill_workspace_size(num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def _prefill_args(out, q, k_cache, v_cache, block_tables, context_lens, max_context_len,
+                  query_starts, scale, workspace, window, pool_dtype, scales):
+    dev = k_cache.device
+    sq = _rows(q, "q", (torch.float16, torch.bfloat16), dev)
+    _need(out, "out", q.dtype, 3, dev)
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _need(t, n, pool_dtype or q.dtype, 4, dev)
+    for t, n in zip(scales, ("k_scale", "v_scale")):
+        _need(t, n, torch.float32, 2, dev)
+        if t.shape != k_cache.shape[:2]:
+            raise ValueError("shape mismatch")
+    _need(block_tables, "block_tables", torch.int32, 2, dev)
+    _need(context_lens, "context_lens", torch.int32, 1, dev)
+    _need(query_starts, "query_starts", torch.int32, 1, dev)
+    T, Hq, D = q.shape
+    NB, Hkv, bs, D2 = k_cache.shape
+    B = block_tables.shape[0]
+    if out.shape != q.shape or v_cache.shape != k_cache.shape or D2 != D or \
+            context_lens.shape[0] != B or query_starts.shape[0] != B + 1:
+        raise ValueError("shape mismatch")
+    _here(dev)
+    return ((_ptr(out), _ptr(q), sq, _ptr(k_cache), _ptr(v_cache), *(_ptr(t) for t in scales)),
+            (_ptr(block_tables), block_tables.shape[1], _ptr(context_lens), int(max_context_len),
+             _ptr(query_starts), T, B, Hq, Hkv, D, bs, NB, float(scale), int(window),
+             _act_code(q.dtype), _ptr(workspace), _ws_bytes(workspace, dev), _stream(dev)))
+
+
+def pa_prefill(out, q, k_cache, v_cache, block_tables, context_lens, max_context_len: int,
+               query_starts, scale: float, workspace, *, window: int = 0) -> None:
+    """out [T][Hq][D]: the causal attention of each sequence's last query tokens,
+    q[query_starts[b]:query_starts[b + 1]] (int32 [B + 1]; any number, 0 too), over
+    its cached context, their own keys and values included (16-bit pools).  q may be a
+    view of one projection.  window: the last so many positions only (0: all)."""
+    a, b = _prefill_args(out, q, k_cache, v_cache, block_tables, context_lens, max_context_len,
+                         query_starts, scale, workspace, window, None, ())
+    _call(load().pa_prefill, "pa_prefill", *a, *b)
+
+
+def pa_prefill_fp8(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+                   max_context_len: int, query_starts, scale: float, workspace, *,
+                   window: int = 0) -> None:
+    """As pa_prefill over E4M3 pools with [NB][Hkv] scales."""
+    a, b = _prefill_args(out, q, k_cache, v_cache, block_tables, context_lens, max_context_len,
+                         query_starts, scale, workspace, window, torch.uint8, (k_scale, v_scale))
+    _call(load().pa_prefill_fp8, "pa_prefill_fp8", *a, *b)
+
+
+def _page_state(block_tables, num_pages, ref_counts):
+    dev = block_tables.device
+    _need(block_tables, "block_tables", torch.int32, 2, dev)
+    _need(num_pages, "num_pages", torch.int32, 1, dev)
+    _need(ref_counts, "ref_counts", torch.int32, 1, dev)
+    if num_pages.shape[0] != block_tables.shape[0]:
+        raise ValueError("shape mismatch")
+    _here(dev)
+    return dev
+
+
+def _items(dev, n, **tensors):
+    for name, t in tensors.items():
+        _need(t, name, torch.int32, 1, dev)
+        if t.shape[0] != n:
+            raise ValueError("shape mismatch")
+
+
+def pa_alloc_pages(block_tables, num_pages, rows, new_lens, ref_counts, granted) -> None:
+    """Give each row of ``rows`` the pages that new_lens tokens need, the lowest
+    free ones (ref_counts [NB] 0) first; granted[i] 0 where the pool did not hold
+    enough for it or one before it.  All int32, all kept on the device."""
+    dev = _page_state(block_tables, num_pages, ref_counts)
+    _items(dev, rows.shape[0], rows=rows, new_lens=new_lens, granted=granted)
+    _call(load().pa_alloc_pages, "pa_alloc_pages", _ptr(block_tables), block_tables.shape[1],
+          _ptr(num_pages), block_tables.shape[0], _ptr(rows), _ptr(new_lens), rows.shape[0],
+          _ptr(ref_counts), ref_counts.shape[0], 16, _ptr(granted), _stream(dev))
+
+
+def pa_free_pages(block_tables, num_pages, rows, ref_counts) -> None:
+    """The pages of each row of ``rows`` lose one owner; the row is empty afterwards."""
+    dev = _page_state(block_tables, num_pages, ref_counts)
+    _items(dev, rows.shape[0], rows=rows)
+    _call(load().pa_free_pages, "pa_free_pages", _ptr(block_tables), block_tables.shape[1],
+          _ptr(num_pages), block_tables.shape[0], _ptr(rows), rows.shape[0], _ptr(ref_counts),
+          ref_counts.shape[0], _stream(dev))
+
+
+def _page_pools(k_cache, v_cache, k_scale, v_scale, dev, NB):
+    fp8 = k_cache.dtype == torch.uint8
+    _need(k_cache, "k_cache", (torch.float16, torch.bfloat16, torch.uint8), 4, dev)
+    _need(v_cache, "v_cache", k_cache.dtype, 4, dev)
+    if v_cache.shape != k_cache.shape or k_cache.shape[0] != NB:
+        raise ValueError("shape mismatch")
+    if not fp8 and (k_scale is not None or v_scale is not None):
+        raise ValueError("scales are for E4M3 pools only")
+    if fp8:
+        for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            _need(t, n, torch.float32, 2, dev)
+            if t.shape != k_cache.shape[:2]:
+                raise ValueError("shape mismatch")
+    _, Hkv, bs, D = k_cache.shape
+    return Hkv, D, bs, PA_E4M3 if fp8 else _act_code(k_cache.dtype)
+
+
+def pa_fork_pages(k_cache, v_cache, block_tables, num_pages, context_lens, src_rows, dst_rows,
+                  ref_counts, granted, *, k_scale=None, v_scale=None) -> None:
+    """Make row dst_rows[i] a fork of row src_rows[i]: the full pages shared, a
+    part-full last one copied to a free page, the context length taken over."""
+    dev = _page_state(block_tables, num_pages, ref_counts)
+    shape = _page_pools(k_cache, v_cache, k_scale, v_scale, dev, ref_counts.shape[0])
+    _items(dev, block_tables.shape[0], context_lens=context_lens)
+    _items(dev, src_rows.shape[0], src_rows=src_rows, dst_rows=dst_rows, granted=granted)
+    _call(load().pa_fork_pages, "pa_fork_pages", _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+          _ptr(v_scale), _ptr(block_tables), block_tables.shape[1], _ptr(num_pages),
+          _ptr(context_lens), block_tables.shape[0], _ptr(src_rows), _ptr(dst_rows),
+          src_rows.shape[0], _ptr(ref_counts), ref_counts.shape[0], *shape, _ptr(granted),
+          _stream(dev))
+
+
+def pa_compact_workspace_size(num_blocks) -> int:
+    return int(load().pa_compact_workspace_size(int(num_blocks)))
+
+
+def alloc_compact_workspace(num_blocks, device):
+    """Caller-owned workspace for pa_compact_pages of a pool of num_blocks pages."""
+    return torch.empty(max(pa_compact_workspace_size(num_blocks), 256), dtype=torch.uint8,
+                       device=device)
+
+
+def pa_compact_pages(k_cache, v_cache, block_tables, num_pages, ref_counts, tables_out,
+                     ref_counts_out, moved_to, num_live, workspace, *, k_scale=None,
+                     v_scale=None) -> None:
+    """Move the live pages together at the front of the pool; tables_out and
+    ref_counts_out (which may be the inputs) hold the new ids and counts, moved_to
+    [NB] where each page went (-1: it was free), num_live [1] how many there are."""
+    dev = _page_state(block_tables, num_pages, ref_counts)
+    NB = ref_counts.shape[0]
+    shape = _page_pools(k_cache, v_cache, k_scale, v_scale, dev, NB)
+    _need(tables_out, "tables_out", torch.int32, 2, dev)
+    if tables_out.shape != block_tables.shape:
+        raise ValueError("shape mismatch")
+    _items(dev, NB, ref_counts_out=ref_counts_out, moved_to=moved_to)
+    _items(dev, 1, num_live=num_live)
+    _call(load().pa_compact_pages, "pa_compact_pages", _ptr(k_cache), _ptr(v_cache),
+          _ptr(k_scale), _ptr(v_scale), _ptr(block_tables), block_tables.shape[1],
+          _ptr(num_pages), block_tables.shape[0], _ptr(ref_counts), NB, *shape,
+          _ptr(tables_out), _ptr(ref_counts_out), _ptr(moved_to), _ptr(num_live),
+          _ptr(workspace), _ws_bytes(workspace, dev), _stream(dev))
+
+
+class _LogitsStruct(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "history", "history_lens", "prompt_lens", "draft_tokens", "repetition", "presence",
+        "frequency", "temperature", "bias_tokens", "bias_values", "allowed")] + [
+        ("history_stride", ctypes.c_int64), ("allowed_stride", ctypes.c_int64),
+        ("num_bias", ctypes.c_int)]
+
+
+class LogitsSpec:
+    """What pa_process_logits does to logits (pa_logits_spec); every part may be
+    left out.  history int32 [B][H] with history_lens int32 [B] (prompt first, then
+    output) and prompt_lens int32 [B]; draft_tokens int32 [B][rows - 1]; repetition,
+    presence, frequency, temperature fp32 [B]; bias_tokens int32 and bias_values
+    fp32 [B][n]; allowed int32 [B][rows][words] or [B][words] (bit t % 32 of word
+    t / 32).  Keeps the tensors; their contents are read by each call."""
+
+    def __init__(self, *, history=None, history_lens=None, prompt_lens=None, draft_tokens=None,
+                 repetition=None, presence=None, frequency=None, temperature=None,
+                 bias_tokens=None, bias_values=None, allowed=None):
+        self.tensors = dict(history=history, history_lens=history_lens, prompt_lens=prompt_lens,
+                            draft_tokens=draft_tokens, repetition=repetition, presence=presence,
+                            frequency=frequency, temperature=temperature, bias_tokens=bias_tokens,
+                            bias_values=bias_values, allowed=allowed)
+        if (history is None) != (history_lens is None):
+            raise ValueError("history and history_lens go together")
+        if (bias_tokens is None) != (bias_values is None):
+            raise ValueError("bias_tokens and bias_values go together")
+        if prompt_lens is not None and history is None:
+            raise ValueError("prompt_lens needs a history")
+
+    def _pointer(self, B, rows, V, dev):
+        t = self.tensors
+        for name, x in t.items():
+            if x is None:
+                continue
+            _need(x, name, torch.float32 if name in ("repetition", "presence", "frequency",
+                                                     "temperature", "bias_values") else torch.int32,
+                  None, dev)
+            shape = tuple(x.shape)
+            n = t["bias_tokens"].shape[-1] if t["bias_tokens"] is not None else 0
+            good = {"history": shape[:1] == (B,) and len(shape) == 2,
+                    "draft_tokens": shape == (B, rows - 1),
+                    "bias_tokens": shape == (B, n), "bias_values": shape == (B, n),
+                    "allowed": shape[:-1] in ((B, rows),) + (((B,),) if rows == 1 else ()) and
+                    shape[-1] >= (V + 31) // 32}
+            if not good.get(name, shape == (B,)):
+                raise ValueError(f"{name} has shape {shape}")
+        if rows > 1 and t["draft_tokens"] is None and t["history"] is not None:
+            raise ValueError("several rows a sequence need the draft_tokens between them")
+        st = _LogitsStruct(*(None if x is None else x.data_ptr() for x in t.values()),
+                           0 if t["history"] is None else t["history"].shape[1],
+                           0 if t["allowed"] is None else t["allowed"].shape[-1],
+                           0 if t["bias_tokens"] is None else t["bias_tokens"].shape[1])
+        p = ctypes.c_void_p(ctypes.addressof(st))
+        p.owner = (self, st)          # a recorded call keeps the struct and the tensors alive
+        return p
+
+
+def _logit_rows(t, name, dtypes, dev):
+    """Checks [B][V] or [B][rows][V] logits whose rows may be padded; (B, rows, V, row stride)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() not in (2, 3):
+        raise ValueError(f"{name} must be [B][V] or [B][rows][V]")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    x = t if t.dim() == 3 else t[:, None]
+    return (*x.shape, _prob_rows(x, name, t.dtype, dev, x.shape[1]))
+
+
+def pa_process_logits(out, logits, spec: LogitsSpec, *, probs: bool = False) -> None:
+    """out = logits [B][V] or [B][rows][V] (fp32, fp16 or bf16) with spec's penalties,
+    biases and mask, in the logits' dtype (out may be the logits); with probs
+    softmax(out / temperature) in fp32, as pa_verify_drafts takes it."""
+    if not isinstance(spec, LogitsSpec):
+        raise TypeError("spec must be a LogitsSpec")
+    codes = {torch.float32: PA_F32, torch.float16: PA_F16, torch.bfloat16: PA_BF16}
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits must be a torch.Tensor")
+    dev = logits.device
+    B, rows, V, stride = _logit_rows(logits, "logits", tuple(codes), dev)
+    *shape, out_stride = _logit_rows(out, "out", (torch.float32 if probs else logits.dtype,), dev)
+    if shape != [B, rows, V]:
+        raise ValueError("shape mismatch")
+    _here(dev)
+    _call(load().pa_process_logits, "pa_process_logits", _ptr(out), out_stride, _ptr(logits),
+          stride, spec._pointer(B, rows, V, dev), B, rows, V, codes[logits.dtype], int(bool(probs)),
+          _stream(dev))

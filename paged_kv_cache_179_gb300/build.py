@@ -22,9 +22,10 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpa.so")
 SOURCES = ["abi.cu", "append.cu", "quantize.cu", "decode.cu", "decode_t2.cu",
            "decode_t4_16bit.cu", "decode_t4_e4m3.cu", "decode_tc.cu", "noalloc.cu", "copy.cu",
-           "serving_abi.cu", "rope.cu", "weights.cu", "evict.cu", "verify.cu"]
+           "serving_abi.cu", "rope.cu", "weights.cu", "evict.cu", "verify.cu",
+           "request_abi.cu", "prefill.cu", "pages.cu", "logits.cu"]
 HEADERS = ["pa_launch.h", "pa_ptx.cuh", "pa_e4m3.cuh", "pa_tc.cuh", "decode_kernels.cuh",
-           "pa_cluster.cuh", "serving_launch.h"]
+           "pa_cluster.cuh", "serving_launch.h", "request_launch.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
@@ -40,7 +41,8 @@ def nvcc() -> str:
 
 def _inputs():
     return ([os.path.join(CSRC, s) for s in SOURCES] + [os.path.join(CSRC, h) for h in HEADERS]
-            + [os.path.join(INCLUDE, h) for h in ("pa.h", "pa_serving.h", "pa_serving_test.h")] + [os.path.abspath(__file__)])
+            + [os.path.join(INCLUDE, h) for h in ("pa.h", "pa_serving.h", "pa_serving_test.h",
+                                                    "pa_request.h")] + [os.path.abspath(__file__)])
 
 
 def up_to_date() -> bool:

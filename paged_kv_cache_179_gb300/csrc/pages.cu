@@ -1,0 +1,494 @@
+// pages.cu -- the pool's pages by reference counts: taken, given back, shared by
+// forks, moved together.
+//
+// The counts are the only record of which pages are free, so every call that
+// takes or moves pages ranks them by one pass over the counts:
+//   rank(p) = number of free (or live) pages below p.
+// A cluster of CTAs does that: each warp counts its own contiguous part, the CTAs'
+// totals are exchanged through distributed shared memory, and a second pass
+// (from L2 now) has every page's rank without a second launch or a workspace.
+// The page of rank k goes to the item whose needs' prefix sum holds k, found by
+// bisection: the lowest free pages, in the items' order, whatever order the
+// warps run in.
+#include <algorithm>
+#include <climits>
+
+#include "pa_cluster.cuh"
+#include "pa_launch.h"
+#include "pa_ptx.cuh"
+#include "request_launch.h"
+
+namespace pa {
+namespace {
+
+constexpr int kScanThreads = 1024;
+constexpr int kScanWarps = kScanThreads / 32;
+constexpr int kScanCtas = 8;                       // a portable cluster
+constexpr unsigned kMany = (1u << 30) + 1u;        // sums of needs saturate above any pool
+
+__device__ __forceinline__ void st_cluster_u32(void* p, uint32_t rank, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(in_cluster(p, rank)), "r"(v) : "memory");
+}
+
+// The counts of pages 4g .. 4g + 3; those behind the pool's end are `behind`.
+__device__ __forceinline__ int4 counts_at(const int32_t* ref, int g, int num_blocks, int behind) {
+  const int p = 4 * g;
+  if (p + 4 <= num_blocks) return *reinterpret_cast<const int4*>(ref + p);
+  int4 c = make_int4(behind, behind, behind, behind);
+  if (p < num_blocks) c.x = ref[p];
+  if (p + 1 < num_blocks) c.y = ref[p + 1];
+  if (p + 2 < num_blocks) c.z = ref[p + 2];
+  return c;
+}
+// Bit i: page 4g + i is free / live.
+__device__ __forceinline__ unsigned free_bits(int4 c) {
+  return (c.x <= 0) | (c.y <= 0) << 1 | (c.z <= 0) << 2 | (c.w <= 0) << 3;
+}
+__device__ __forceinline__ unsigned live_bits(int4 c) {
+  return (c.x > 0) | (c.y > 0) << 1 | (c.z > 0) << 2 | (c.w > 0) << 3;
+}
+
+// This warp's part of the groups of four pages: an equal contiguous share.
+struct Part {
+  int g0, g1;
+};
+__device__ __forceinline__ Part my_part(int num_blocks, uint32_t rank, int warp) {
+  const int groups = (num_blocks + 3) / 4;
+  const int parts = kScanCtas * kScanWarps;
+  const int per = (groups + parts - 1) / parts;
+  const int64_t w = static_cast<int64_t>(rank) * kScanWarps + warp;
+  const int g0 = static_cast<int>(min(w * per, static_cast<int64_t>(groups)));
+  return Part{g0, min(g0 + per, groups)};
+}
+
+// What the warps count, summed: each warp's own `n` in; out, the sum over all
+// warps before it and the sum over all of them.  `box` [kScanCtas] and `mine`
+// [kScanWarps] in shared memory; a cluster barrier inside.  All CTAs of the cluster
+// have started (one reaches into the others' shared memory).
+struct Before {
+  unsigned before, total;
+};
+__device__ __forceinline__ Before cluster_prefix(unsigned n, unsigned* mine, unsigned* box, int warp,
+                                                 int lane, uint32_t rank) {
+  if (lane == 0) mine[warp] = n;
+  __syncthreads();
+  unsigned sum = mine[lane];                       // kScanWarps == 32
+  unsigned inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned t = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += t;
+  }
+  const unsigned all = __shfl_sync(0xffffffffu, inc, 31);
+  const unsigned in_cta = __shfl_sync(0xffffffffu, inc - sum, warp);
+  if (warp == 0 && lane < kScanCtas) st_cluster_u32(box + rank, lane, all);
+  cluster_sync();
+  Before b{in_cta, 0u};
+#pragma unroll
+  for (int r = 0; r < kScanCtas; ++r) {
+    const unsigned v = box[r];
+    b.before += static_cast<uint32_t>(r) < rank ? v : 0u;
+    b.total += v;
+  }
+  return b;
+}
+
+__device__ __forceinline__ unsigned warp_sum(unsigned v) {
+  return __reduce_add_sync(0xffffffffu, v);
+}
+__device__ __forceinline__ unsigned warp_prefix(unsigned v, int lane) {   // exclusive
+  unsigned inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned t = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += t;
+  }
+  return inc - v;
+}
+
+// ---------------------------------------------------------------------- taking
+// What item i needs: pages (-1: it is passed over), in which row, from which
+// entry of its table on, and how many the row holds with them.
+struct Need {
+  int pages, row, entry, holds;
+};
+template <bool FORK>
+__device__ __forceinline__ Need need_of(const TakeArgs& a, int i, bool report) {
+  Need n{-1, a.rows[i], 0, 0};
+  unsigned bad = 0u;
+  if (n.row < 0 || n.row >= a.num_rows) {
+    bad = kStatusBadRow;
+  } else if (FORK) {
+    const int src = a.src_rows[i];
+    if (src < 0 || src >= a.num_rows || src == n.row) {
+      bad = kStatusBadRow;
+    } else {
+      const int L = a.lens[src], have = a.num_pages[src];
+      if (have < 0 || have > a.mbs || L < 0 || L > static_cast<int64_t>(have) * 16) {
+        bad = kStatusBadLen;
+      } else {
+        n.pages = (L & 15) != 0;
+        n.entry = L >> 4;
+        n.holds = n.entry + n.pages;
+      }
+    }
+  } else {
+    const int L = a.lens[i], have = a.num_pages[n.row];
+    const int want = static_cast<int>((static_cast<int64_t>(L) + 15) >> 4);
+    if (have < 0 || have > a.mbs || L < 0 || want > a.mbs) {
+      bad = kStatusBadLen;
+    } else {
+      n.pages = max(want - have, 0);
+      n.entry = have;
+      n.holds = max(want, have);
+    }
+  }
+  if (bad && report) atomicOr(a.status, bad);
+  return n;
+}
+
+template <bool FORK>
+__global__ void __launch_bounds__(kScanThreads, 1) take_kernel(const TakeArgs a) {
+  extern __shared__ __align__(16) int first[];     // [items + 1]: needs before each item
+  __shared__ unsigned mine[kScanWarps], box[kScanCtas], sums[kScanWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_rank();
+  cluster_arrive();                                // (this CTA has started)
+  // ---- the free pages of this warp's part
+  const Part part = my_part(a.num_blocks, rank, warp);
+  unsigned n_free = 0;
+  for (int g = part.g0 + lane; g < part.g1; g += 32)
+    n_free += __popc(free_bits(counts_at(a.ref_counts, g, a.num_blocks, 1)));
+  n_free = warp_sum(n_free);
+  // ---- the needs and their prefix sums, by every CTA for itself
+  const int per = (a.items + kScanThreads - 1) / kScanThreads;
+  const int i0 = min(a.items, tid * per), i1 = min(a.items, i0 + per);
+  unsigned sum = 0;
+  for (int i = i0; i < i1; ++i) {
+    const int pages = max(need_of<FORK>(a, i, rank == 0).pages, 0);
+    first[i] = pages;
+    sum = min(sum + pages, kMany);
+  }
+  unsigned inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned t = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc = min(inc + t, kMany);
+  }
+  if (lane == 31) sums[warp] = inc;
+  const unsigned up = __shfl_up_sync(0xffffffffu, inc, 1);
+  cluster_wait();
+  const Before at = cluster_prefix(n_free, mine, box, warp, lane, rank);   // (syncs: sums are there)
+  unsigned ex = lane > 0 ? up : 0u;
+  for (int w = 0; w < warp; ++w) ex = min(ex + sums[w], kMany);
+  for (int i = i0; i < i1; ++i) {
+    const unsigned pages = first[i];
+    first[i] = ex;
+    ex = min(ex + pages, kMany);
+  }
+  if (tid == kScanThreads - 1) first[a.items] = ex;
+  __syncthreads();
+  // ---- items are granted while their last page's rank is there
+  auto last_at_most = [&](int v) {                 // the last j with first[j] <= v
+    int l = 0, r = a.items + 1;
+    while (r - l > 1) {
+      const int m = (l + r) >> 1;
+      if (first[m] <= v) l = m;
+      else r = m;
+    }
+    return l;
+  };
+  const unsigned limit = first[last_at_most(static_cast<int>(at.total))];
+  unsigned k0 = at.before;
+  for (int g = part.g0; g < part.g1 && k0 < limit; g += 32) {
+    const int4 c = counts_at(a.ref_counts, min(g + lane, part.g1 - 1), a.num_blocks, 1);
+    unsigned bits = g + lane < part.g1 ? free_bits(c) : 0u;
+    const unsigned mine_n = __popc(bits);
+    unsigned k = k0 + warp_prefix(mine_n, lane);
+    for (; bits != 0u && k < limit; bits &= bits - 1, ++k) {
+      const int page = 4 * (g + lane) + __ffs(bits) - 1;
+      const int i = last_at_most(static_cast<int>(k));
+      const Need n = need_of<FORK>(a, i, false);
+      a.block_tables[static_cast<int64_t>(n.row) * a.mbs + n.entry + (k - first[i])] = page;
+      a.ref_counts[page] = 1;
+    }
+    k0 += warp_sum(mine_n);
+  }
+  // ---- what the items hold now, once no CTA reads num_pages any more
+  cluster_sync();
+  if (rank != 0) return;
+  for (int i = tid; i < a.items; i += kScanThreads) {
+    const Need n = need_of<FORK>(a, i, false);
+    const bool ok = n.pages >= 0 && static_cast<unsigned>(first[i] + n.pages) <= at.total;
+    a.granted[i] = ok;
+    if (!FORK && ok) a.num_pages[n.row] = n.holds;
+  }
+}
+
+template <bool FORK>
+cudaError_t launch_take(const TakeArgs& a, cudaStream_t s) {
+  auto* kern = take_kernel<FORK>;
+  const size_t smem = (static_cast<size_t>(a.items) + 1) * 4;
+  if (smem > 47 * 1024) {                          // (the default limit is 48 KB with the static arrays)
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (kPagesMaxItems + 1) * 4);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kScanCtas);
+  cfg.blockDim = dim3(kScanThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kScanCtas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+// -------------------------------------------------------------------- giving back
+constexpr int kFreeThreads = 256;
+__global__ void __launch_bounds__(kFreeThreads)
+free_kernel(int32_t* tables, int mbs, int32_t* num_pages, int num_rows, const int32_t* rows,
+            int32_t* ref, int num_blocks, unsigned* status) {
+  __shared__ int held;
+  const int row = rows[blockIdx.x];
+  if (row < 0 || row >= num_rows) {
+    if (threadIdx.x == 0) atomicOr(status, kStatusBadRow);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    const int n = num_pages[row];
+    const bool ok = n >= 0 && n <= mbs;
+    // the exchange: a row that is listed twice is freed by one of its CTAs
+    held = ok ? atomicExch(num_pages + row, 0) : 0;
+    if (!ok) atomicOr(status, kStatusBadLen);
+  }
+  __syncthreads();
+  int32_t* t = tables + static_cast<int64_t>(row) * mbs;
+  for (int j = threadIdx.x; j < held; j += kFreeThreads) {
+    const int id = t[j];
+    t[j] = -1;
+    bool bad = id < 0 || id >= num_blocks;
+    if (!bad && atomicSub(ref + id, 1) <= 0) {     // it was free: back to what it was
+      atomicAdd(ref + id, 1);
+      bad = true;
+    }
+    if (bad) atomicOr(status, kStatusBadBlock);
+  }
+}
+
+// ------------------------------------------------------------------------- copies
+constexpr int kPieceChunks = 256;                  // 16-byte chunks a warp has in flight: 4 KB
+
+// Piece `piece` of a page of one pool, by a warp.
+__device__ __forceinline__ void copy_piece(uint4* pool, int64_t chunks, int src, int dst, int piece,
+                                           int lane) {
+  const uint4* from = pool + src * chunks;
+  uint4* to = pool + dst * chunks;
+  const int64_t c0 = static_cast<int64_t>(piece) * kPieceChunks + lane;
+  uint4 r[kPieceChunks / 32];
+#pragma unroll
+  for (int j = 0; j < kPieceChunks / 32; ++j)
+    if (c0 + 32 * j < chunks) r[j] = __ldcs(from + c0 + 32 * j);
+#pragma unroll
+  for (int j = 0; j < kPieceChunks / 32; ++j)
+    if (c0 + 32 * j < chunks) __stcs(to + c0 + 32 * j, r[j]);
+}
+__device__ __forceinline__ void copy_scales(const PagePools& p, int src, int dst, int lane) {
+  for (int h = lane; h < p.Hkv; h += 32) {
+    p.k_scale[static_cast<int64_t>(dst) * p.Hkv + h] = p.k_scale[static_cast<int64_t>(src) * p.Hkv + h];
+    p.v_scale[static_cast<int64_t>(dst) * p.Hkv + h] = p.v_scale[static_cast<int64_t>(src) * p.Hkv + h];
+  }
+}
+
+constexpr int kForkThreads = 256;
+// One CTA a pair, after its part-full page was taken: the shared pages' ids and
+// counts, then the copy.
+__global__ void __launch_bounds__(kForkThreads)
+fork_kernel(const TakeArgs a, int32_t* context_lens, const PagePools p) {
+  const int i = blockIdx.x;
+  if (!a.granted[i]) return;
+  const int src = a.src_rows[i], dst = a.rows[i], L = context_lens[src];
+  const int full = L >> 4, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int32_t* from = a.block_tables + static_cast<int64_t>(src) * a.mbs;
+  int32_t* to = a.block_tables + static_cast<int64_t>(dst) * a.mbs;
+  if (L & 15) {
+    const int old = from[full], mine = to[full];
+    if (old < 0 || old >= a.num_blocks) {
+      if (threadIdx.x == 0) atomicOr(a.status, kStatusBadBlock);
+    } else {
+      const int64_t chunks = p.page_bytes / 16;
+      const int pieces = static_cast<int>((chunks + kPieceChunks - 1) / kPieceChunks);
+      for (int u = warp; u < 2 * pieces; u += kForkThreads / 32)
+        copy_piece(static_cast<uint4*>(u < pieces ? p.k_cache : p.v_cache), chunks, old, mine,
+                   u < pieces ? u : u - pieces, lane);
+      if (p.k_scale != nullptr && warp == 0) copy_scales(p, old, mine, lane);
+    }
+  }
+  for (int j = threadIdx.x; j < full; j += kForkThreads) {
+    const int id = from[j];
+    to[j] = id;
+    if (id >= 0 && id < a.num_blocks) atomicAdd(a.ref_counts + id, 1);
+    else atomicOr(a.status, kStatusBadBlock);
+  }
+  if (threadIdx.x == 0) {
+    a.num_pages[dst] = full + ((L & 15) != 0);
+    context_lens[dst] = L;
+  }
+}
+
+// --------------------------------------------------------------------- compaction
+// Workspace: the number of moves, then the free pages below num_live in order
+// (`holes`) and the live pages by their rank, as far as they move (`movers`).
+struct CompactSpace {
+  int32_t* moves;
+  int32_t* holes;
+  int32_t* movers;
+};
+__host__ __device__ inline int64_t holes_room(int num_blocks) {
+  return (static_cast<int64_t>(num_blocks) + 63) / 64 * 64;
+}
+__host__ __device__ inline CompactSpace compact_space(void* ws, int num_blocks) {
+  int32_t* w = static_cast<int32_t*>(ws);
+  return CompactSpace{w, w + 64, w + 64 + holes_room(num_blocks)};
+}
+
+// Ranks the live pages; writes num_live, moved_to, ref_counts_out and the lists.
+__global__ void __launch_bounds__(kScanThreads, 1) compact_plan_kernel(const CompactArgs a) {
+  __shared__ unsigned mine[kScanWarps], box[2][kScanCtas];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  cluster_arrive();                                // (this CTA has started)
+  const CompactSpace ws = compact_space(a.workspace, a.num_blocks);
+  const Part part = my_part(a.num_blocks, rank, warp);
+  unsigned n = 0;
+  for (int g = part.g0 + lane; g < part.g1; g += 32)
+    n += __popc(live_bits(counts_at(a.ref_counts, g, a.num_blocks, 0)));
+  n = warp_sum(n);
+  cluster_wait();
+  const Before at = cluster_prefix(n, mine, box[0], warp, lane, rank);
+  const int live = static_cast<int>(at.total);
+  // ---- pages that stay, holes (rank: free pages below) and movers (live ones below)
+  unsigned k0 = at.before, holes = 0;
+  for (int g = part.g0; g < part.g1; g += 32) {
+    const bool here = g + lane < part.g1;
+    const int4 c = counts_at(a.ref_counts, min(g + lane, part.g1 - 1), a.num_blocks, 0);
+    const unsigned bits = here ? live_bits(c) : 0u;
+    unsigned k = k0 + warp_prefix(__popc(bits), lane);
+    const int cs[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int page = 4 * (g + lane) + j;
+      if (!here || page >= a.num_blocks) continue;
+      const bool used = (bits >> j) & 1u;
+      if (used && page >= live) {
+        ws.movers[k] = page;
+      } else {
+        a.moved_to[page] = used ? page : -1;
+        if (!used && page < live) {
+          ws.holes[page - static_cast<int>(k)] = page;
+          ++holes;
+        } else if (a.ref_counts_out != a.ref_counts) {
+          a.ref_counts_out[page] = cs[j];
+        }
+      }
+      k += used;
+    }
+    k0 += warp_sum(__popc(bits));
+  }
+  holes = warp_sum(holes);
+  __syncthreads();                                 // `mine` has been read by all
+  const int moves = static_cast<int>(cluster_prefix(holes, mine, box[1], warp, lane, rank).total);
+  // (the barrier inside: the lists are whole) movers take the holes, in order
+  for (int m = static_cast<int>(rank) * kScanThreads + threadIdx.x; m < moves;
+       m += kScanCtas * kScanThreads) {
+    const int src = ws.movers[live - moves + m], dst = ws.holes[m];
+    const int count = a.ref_counts[src];
+    a.moved_to[src] = dst;
+    a.ref_counts_out[dst] = count;
+    a.ref_counts_out[src] = 0;
+  }
+  if (rank == 0 && threadIdx.x == 0) {
+    *a.num_live = live;
+    *ws.moves = moves;
+  }
+}
+
+constexpr int kMoveThreads = 256;
+__global__ void __launch_bounds__(kMoveThreads)
+compact_move_kernel(const CompactArgs a, const PagePools p) {
+  const CompactSpace ws = compact_space(a.workspace, a.num_blocks);
+  const int moves = *ws.moves, live = *a.num_live;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t chunks = p.page_bytes / 16;
+  const int pieces = static_cast<int>((chunks + kPieceChunks - 1) / kPieceChunks);
+  const int64_t units = static_cast<int64_t>(moves) * 2 * pieces;
+  for (int64_t u = static_cast<int64_t>(blockIdx.x) * (kMoveThreads / 32) + warp; u < units;
+       u += static_cast<int64_t>(gridDim.x) * (kMoveThreads / 32)) {
+    const int m = static_cast<int>(u / (2 * pieces)), r = static_cast<int>(u - static_cast<int64_t>(m) * 2 * pieces);
+    const int src = ws.movers[live - moves + m], dst = ws.holes[m];
+    copy_piece(static_cast<uint4*>(r < pieces ? p.k_cache : p.v_cache), chunks, src, dst,
+               r < pieces ? r : r - pieces, lane);
+    if (r == 0 && p.k_scale != nullptr) copy_scales(p, src, dst, lane);
+  }
+  for (int row = blockIdx.x; row < a.num_rows; row += gridDim.x) {
+    const int held = a.num_pages[row];
+    const bool ok = held >= 0 && held <= a.mbs;
+    if (!ok && threadIdx.x == 0) atomicOr(a.status, kStatusBadLen);
+    const int32_t* t = a.block_tables + static_cast<int64_t>(row) * a.mbs;
+    int32_t* o = a.tables_out + static_cast<int64_t>(row) * a.mbs;
+    for (int j = threadIdx.x; j < a.mbs; j += kMoveThreads) {
+      int id = t[j];
+      if (ok && j < held) {
+        const bool in = id >= 0 && id < a.num_blocks;
+        if (in) id = a.moved_to[id];
+        if (!in || id < 0) atomicOr(a.status, kStatusBadBlock);
+      }
+      o[j] = id;
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_alloc_pages(const TakeArgs& a, cudaStream_t s) { return launch_take<false>(a, s); }
+
+cudaError_t launch_free_pages(int32_t* tables, int mbs, int32_t* num_pages, int num_rows,
+                              const int32_t* rows, int items, int32_t* ref_counts, int num_blocks,
+                              unsigned* status, cudaStream_t s) {
+  free_kernel<<<items, kFreeThreads, 0, s>>>(tables, mbs, num_pages, num_rows, rows, ref_counts,
+                                             num_blocks, status);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_fork_pages(const TakeArgs& a, int32_t* context_lens, const PagePools& p,
+                              cudaStream_t s) {
+  if (const cudaError_t e = launch_take<true>(a, s)) return e;
+  fork_kernel<<<a.items, kForkThreads, 0, s>>>(a, context_lens, p);
+  return cudaGetLastError();
+}
+
+size_t compact_workspace_bytes(int num_blocks) {
+  return static_cast<size_t>(64 + 2 * holes_room(num_blocks)) * 4;
+}
+
+cudaError_t launch_compact_pages(const CompactArgs& a, const PagePools& p, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kScanCtas);
+  cfg.blockDim = dim3(kScanThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kScanCtas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (const cudaError_t e = cudaLaunchKernelEx(&cfg, compact_plan_kernel, a)) return e;
+  compact_move_kernel<<<device_sm_count() * 8, kMoveThreads, 0, s>>>(a, p);
+  return cudaGetLastError();
+}
+
+}  // namespace pa
