@@ -1,131 +1,1178 @@
-// prefill.cu -- attention of prompts over the paged cache: the plain form, which
-// the checks hold faster ones to.  A CTA takes 64 query rows (token, head of the
-// group) of one (sequence, kv head), eight a warp, and walks the pages they see:
-// keys and values as fp32 in shared memory, a lane holding D / 32 elements of each
-// row's query and result, an online softmax in fp32.
+// prefill.cu -- attention of prompts over the paged cache, on the fifth-generation
+// tensor cores (tcgen05.mma, accumulators in tensor memory).
+//
+//   out[t][hq] = sum_j softmax_j(scale q[t][hq] . K_j) V_j,  j up to t's own position
+//
+// The query rows of one (sequence, kv head) are its tokens times the group's heads:
+// all of them read the same keys.  An item is 2 subtiles of floor(128 / group) tokens
+// (up to 128 rows each) of one of them, and the 128-token tiles of keys that they see.
+// Per tile and subtile:
+//   S[128 rows][128 tokens]  = Q . K^T       (both K-major in shared memory)
+//   O[128 rows][D]          += P . V         (P in tensor memory, in S's place)
+//
+// Roles of a CTA, one an SM:
+//   warps 0-3, 4-7   the softmax of one subtile each, a thread a row: S is read twice
+//                    from tensor memory (maximum, then weights), so a thread holds 32
+//                    of its values at a time; P goes back as 16-bit pairs;
+//   warp 8           walks the CTA's pieces, copies Q, K and V (TMA);
+//   warp 9           one thread issues the products, each as soon as its operands are
+//                    there.  A subtile's Q.K of the next tile follows its P.V in the
+//                    same queue, so S needs no second buffer: the tensor cores work on
+//                    one subtile while the other's softmax runs;
+//   warps 10-13      E4M3 pools: codes to f16 (exact) between two shared-memory rings.
+//
+// The softmax offset of a row moves only when a score exceeds it by more than kSlack
+// (log2 units): any standing offset gives the same softmax, weights stay below
+// 2^kSlack, and O is scaled in tensor memory a few times a row instead of every tile.
+// Page scales: K's multiply the scores of their 16 columns, V's the weights (relative
+// to a power of two that follows the largest seen, so that P stays in f16's range).
+//
+// The batch's items, each as long as its tiles, are laid end to end and cut into one
+// share a CTA; a cut within kSnap tiles of an item's border moves there.  An item that
+// is cut all the same leaves its parts (O, maximum, sum) in the workspace, which a
+// second launch joins in their order.
+//
+// A tile that some row of the subtile sees in part is an edge: masks are applied, V's
+// rows without data (behind the context, pages with a bad id) are zeroed, and when a
+// value of V is not finite, which a weight of 0 does not take away, the subtile's
+// threads add up that tile's visible rows themselves.
+//
+// Every wait is bounded in time: a wait that gives up sets kStatusTimeout and a
+// CTA-wide flag, at which every role leaves; copies and products in flight are waited
+// for and tensor memory is freed first.
+#include <climits>
+#include <mutex>
+
+#include <cudaTypedefs.h>
+
 #include "pa_launch.h"
 #include "pa_ptx.cuh"
+#include "pa_tc.cuh"
 #include "request_launch.h"
 
 namespace pa {
 namespace {
 
-constexpr int kRows = 64, kWarps = 8, kPer = kRows / kWarps;
+constexpr int kTile = 128;                 // tokens of a tile, rows of a subtile
+constexpr int kPages = kTile / 16;
+constexpr float kSlack = 8.f;              // log2 units
+constexpr int kSnap = 4;                   // tiles
+constexpr int kMaxSeqs = 512;              // sequences a launch sorts
+constexpr int kDescs = 4;                  // pieces known ahead
+constexpr int kMetas = 8;                  // tiles whose pages' validity and scales are kept
+constexpr int kCopyWarp = 8, kMmaWarp = 9, kConvWarp = 10, kConvWarps = 4;
+constexpr int kHeader = 16;                // ints a CTA's header in the workspace
 
-template <int D, bool BF16>
-__device__ __forceinline__ float load16(const void* p, int64_t i) {
-  const uint16_t w = static_cast<const uint16_t*>(p)[i];
-  if constexpr (BF16) return __uint_as_float(static_cast<uint32_t>(w) << 16);
-  else return __half2float(*reinterpret_cast<const __half*>(&w));
+struct Args {
+  PrefillArgs a;
+  CUtensorMap tm_q, tm_k, tm_v;
+  float* ws_acc;                           // [grid][2 parts][256 rows][D]
+  float2* ws_ml;                           // [grid][2][256]: offset (log2 units), sum
+  int* ws_head;                            // [grid][kHeader]
+  float sl2;                               // |scale| log2(e), above 0
+  int negative;                            // scale < 0
+  int sub;                                 // tokens of a subtile
+  uint64_t wait_limit_ns;
+};
+
+// Header: what the CTA leaves in the workspace.
+enum { kHasTail, kHasHead, kHeadEnds, kTailT0, kTailH, kTailTokens };
+
+template <int D, bool FP8>
+struct Cfg {
+  static constexpr int kHalves = D / 64;                   // 128-byte columns of a row
+  static constexpr int kSub = kTile * 128;                 // one half of a slot: 16 KB
+  static constexpr int kSlot = kHalves * kSub;             // K or V of a tile, 16-bit
+  static constexpr int kRaw = FP8 ? kTile * D : 0;         // its codes
+  static constexpr int kRaws = FP8 ? 2 : 0;
+  // Q of both subtiles, the ring, the codes: 224 KB at head_dim 128, 160 KB at 64
+  static constexpr int kSlots = FP8 ? (D == 128 ? 4 : 6) : (D == 128 ? 5 : 8);
+  static constexpr int kThreads = FP8 ? 448 : 320;
+  static constexpr int kQ = 2 * kSlot;
+  static constexpr int kBig = kQ + kSlots * kSlot + kRaws * kRaw;
+};
+
+struct Desc {                              // a piece, or the end (h < 0)
+  int h, b, t0, n, L, i0, tokens;          // t0: q's first token; i0, tokens: of the sequence
+  int k_lo, k_hi, g0;                      // tiles, and the number of the first in the CTA's stream
+  int whole, part;                         // the whole item, or which part of the workspace
+};
+
+struct Meta {
+  unsigned valid;                          // bit j: page j of the tile has a valid id
+  float ks[kPages], vs[kPages];
+};
+
+enum : int {                               // mbarriers
+  kFull = 0,
+  kEmpty = kFull + 8,
+  kRawFull = kEmpty + 8,
+  kRawEmpty = kRawFull + 2,
+  kQFull = kRawEmpty + 2,                  // by subtile, as those below
+  kQEmpty = kQFull + 2,
+  kQConv = kQEmpty + 2,
+  kSFull = kQConv + 2,
+  kPFull = kSFull + 2,
+  kODone = kPFull + 2,
+  kVote = kODone + 2,
+  kDFull = kVote + 2,
+  kDEmpty = kDFull + kDescs,
+  kFin = kDEmpty + kDescs,
+  kBars = kFin + 1
+};
+
+struct Small {                             // shared memory behind the operands
+  uint64_t bar[kBars];
+  Desc desc[kDescs];
+  Meta meta[kMetas];
+  int tmem, dead, raw_end;
+  int skip[2];                             // the subtile's threads made this product themselves
+  int flag[2][4];                          // by warp: a value of V is not finite
+  int64_t lo, hi;                          // the CTA's share
+  int b, h, j, off;                        // where it begins
+};
+
+struct Setup {                             // in the operands' place, before the copies start
+  int n[kMaxSeqs], L[kMaxSeqs];
+  int64_t before[kMaxSeqs + 1];            // units of the sequences before
+};
+
+__device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, volatile int* dead,
+                                             uint64_t limit, unsigned* status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  for (;;) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*dead) return false;
+    if (global_ns() - t0 > limit) {
+      *dead = 1;
+      atomicOr(status, kStatusTimeout);
+      return false;
+    }
+  }
+}
+
+// Whether a phase is complete, without waiting.
+__device__ __forceinline__ bool test_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// A box of a tensor map into shared memory (K and V of a prompt are read by many CTAs:
+// no eviction hint).
+__device__ __forceinline__ void box_g2s(uint32_t dst, const void* tmap, int x0, int x1, int x2,
+                                        uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(tmap), "r"(x0), "r"(x1), "r"(x2), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void page_g2s(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+// D[tmem] (+)= A[tmem] . B[smem]: A's 16-bit pairs along K in the columns from tmem_a on.
+__device__ __forceinline__ void umma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t db,
+                                            uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(db), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+constexpr uint32_t kBMajorN = 1u << 16;    // B MN-major (V: tokens along K, its rows along N)
+
+// Units of item j (its tiles; 1 when it sees none, for its zeros) of a sequence with n
+// query tokens and L cached ones; *lo: the first tile.
+__device__ __forceinline__ int item_units(int n, int L, int j, int sub, int window, int* lo) {
+  const int i0 = j * 2 * sub, i1 = min(n, i0 + 2 * sub) - 1;
+  const int last = L - n + i1, first = L - n + i0;
+  *lo = 0;
+  if (last < 0) return 1;
+  if (window > 0) *lo = max(0, first - window + 1) / kTile;
+  return last / kTile + 1 - *lo;
+}
+// The tiles that subtile w of a piece sees, within the piece's.
+__device__ __forceinline__ int2 sub_tiles(const Desc& d, int w, int sub, int window) {
+  const int cnt = min(max(d.tokens - w * sub, 0), sub);
+  const int first = d.L - d.n + d.i0 + w * sub, last = first + cnt - 1;
+  if (cnt == 0 || last < 0) return make_int2(0, 0);
+  const int lo = window > 0 ? max(0, first - window + 1) / kTile : 0;
+  const int a = max(lo, d.k_lo), e = min(last / kTile + 1, d.k_hi);
+  return a < e ? make_int2(a, e) : make_int2(0, 0);
+}
+
+template <int N>
+__device__ __forceinline__ float max_of(const float (&v)[32], int from, float m) {
+#pragma unroll
+  for (int j = 0; j < N; j += 2) m = fmaxf(m, fmaxf(v[from + j], v[from + j + 1]));
+  return m;
 }
 
 template <int D, bool BF16, bool FP8>
-__global__ void __launch_bounds__(kWarps * 32) prefill_kernel(const PrefillArgs a) {
-  constexpr int E = D / 32;
-  __shared__ float sk[16][D], sv[16][D];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, h = blockIdx.y;
-  // the tile: blockIdx.x counts 64-row tiles over all sequences
-  int tile = blockIdx.x, b = 0, n = 0;
-  for (; b < a.B; ++b) {
-    const int s0 = a.starts[b], s1 = a.starts[b + 1];
-    const bool ok = s0 >= 0 && s1 >= s0 && s1 <= a.T;
-    if (!ok && tile == 0 && tid == 0 && h == 0) atomicOr(a.status, kStatusBadLen);
-    n = ok ? s1 - s0 : 0;
-    const int tiles = (n * a.group + kRows - 1) / kRows;
-    if (tile < tiles) break;
-    tile -= tiles;
-  }
-  if (b == a.B) return;
-  int L = a.context_lens[b];
-  if (L < 0 || L > a.max_context_len) {
-    if (tid == 0) atomicOr(a.status, kStatusBadLen);
-    L = 0;
-  }
-  const int t0 = a.starts[b];
-  float q[kPer][E], o[kPer][E], m[kPer], l[kPer];
-  int pos[kPer];
-  int first = INT32_MAX, last = -1;
-  for (int r = 0; r < kPer; ++r) {
-    const int row = tile * kRows + warp * kPer + r, i = row / a.group, g = row % a.group;
-    pos[r] = row < n * a.group ? L - n + i : -1;
-    m[r] = -INFINITY;
-    l[r] = 0.f;
-    for (int e = 0; e < E; ++e) {
-      o[r][e] = 0.f;
-      q[r][e] = pos[r] >= 0 ? load16<D, BF16>(a.q, (t0 + i) * a.q_stride + (h * a.group + g) * D + lane * E + e) * a.scale : 0.f;
-    }
-  }
+__global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
+prefill_kernel(const __grid_constant__ Args ka) {
+  using C = Cfg<D, FP8>;
+  constexpr bool kMmaBf16 = BF16 && !FP8;  // the products' operand type
+  // weights of f16 products are kept 2^6 larger, so that small ones stay in its normal
+  // range (2^(6 + kSlack) times a page scale up to twice the reference: below 2^16)
+  constexpr float kLift = kMmaBf16 ? 0.f : 6.f;
+  const PrefillArgs& a = ka.a;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t base = smem_u32(smem);
+  const uint32_t q_at = base, ring = base + C::kQ, raw = ring + C::kSlots * C::kSlot;
+  Small& sm = *reinterpret_cast<Small*>(smem + C::kBig);
+  const uint32_t bars = smem_u32(sm.bar);
+  auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
+  volatile int* dead = &sm.dead;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = a.group, sub = ka.sub, cta = blockIdx.x;
+  auto wait = [&](int b, int n) {          // the n-th completion (from 0) of barrier b
+    return bounded_wait(bar(b), n & 1, dead, ka.wait_limit_ns, a.status);
+  };
+  auto wait_warp = [&](int b, int n) { return __all_sync(0xffffffffu, wait(b, n)); };
+
+  // ---- 1. the items' lengths, and this CTA's share of them
   {
-    const int i0 = tile * kRows / a.group, i1 = min(n - 1, (tile * kRows + kRows - 1) / a.group);
-    last = L - n + i1;
-    first = a.window > 0 ? max(0, L - n + i0 - a.window + 1) : 0;
-  }
-  for (int p = first / 16; p <= last / 16 && last >= 0; ++p) {
-    const int id = a.block_tables[static_cast<int64_t>(b) * a.mbs + p];
-    const bool ok = id >= 0 && id < a.num_blocks;
-    if (!ok) {
-      if (tid == 0) atomicOr(a.status, kStatusBadBlock);
-      continue;
+    Setup& su = *reinterpret_cast<Setup*>(smem);
+    for (int b = tid; b < a.B; b += C::kThreads) {
+      const int s0 = a.starts[b], s1 = a.starts[b + 1], L = a.context_lens[b];
+      const bool good = s0 >= 0 && s1 >= s0 && s1 <= a.T, fits = L >= 0 && L <= a.max_context_len;
+      if (cta == 0 && (!good || (!fits && s1 > s0))) atomicOr(a.status, kStatusBadLen);
+      su.n[b] = good ? s1 - s0 : 0;
+      su.L[b] = fits ? L : 0;
+    }
+    if (tid == 0) {
+      sm.dead = 0;
+      sm.raw_end = INT_MAX;
+      su.before[0] = 0;
+      for (int i = 0; i < kBars; ++i) {
+        int n = 1;
+        if (FP8 && i >= kFull && i < kFull + 8) n = kConvWarps;
+        if (i == kRawEmpty || i == kRawEmpty + 1) n = kConvWarps;
+        if (i >= kQConv && i < kQConv + 2) n = 4;
+        if (i >= kSFull && i < kSFull + 2) n = 2;
+        if (i >= kPFull && i < kPFull + 2) n = 4;
+        if (i >= kVote && i < kVote + 2) n = 4;
+        if (i >= kDEmpty && i < kDEmpty + kDescs) n = 2 + 8;
+        mbar_init(bar(i), n);
+      }
+      mbar_init_fence();
     }
     __syncthreads();
-    const int64_t page = (static_cast<int64_t>(id) * a.Hkv + h) * 16 * D;
-    const float ks = FP8 ? a.k_scale[static_cast<int64_t>(id) * a.Hkv + h] : 1.f;
-    const float vs = FP8 ? a.v_scale[static_cast<int64_t>(id) * a.Hkv + h] : 1.f;
-    for (int e = tid; e < 16 * D; e += kWarps * 32) {
-      const bool in = p * 16 + e / D < L;
-      float k, v;
+    for (int b = warp; b < a.B; b += C::kThreads / 32) {
+      const int n = su.n[b], L = su.L[b], items = (n + 2 * sub - 1) / (2 * sub);
+      int64_t u = 0;
+      int lo;
+      for (int j = lane; j < items; j += 32) u += item_units(n, L, j, sub, a.window, &lo);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
+      if (lane == 0) su.before[b + 1] = u * a.Hkv;
+    }
+    __syncthreads();
+    if (warp == 0) {                       // their prefix sums
+      int64_t run = 0;
+      for (int b0 = 0; b0 < a.B; b0 += 32) {
+        int64_t v = b0 + lane < a.B ? su.before[b0 + lane + 1] : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t t = __shfl_up_sync(0xffffffffu, v, o);
+          if (lane >= o) v += t;
+        }
+        if (b0 + lane < a.B) su.before[b0 + lane + 1] = run + v;
+        run += __shfl_sync(0xffffffffu, v, 31);
+      }
+    }
+    __syncthreads();
+    const int64_t U = su.before[a.B];
+    const int64_t NW = min(static_cast<int64_t>(gridDim.x), U);
+    if (warp < 2) {                        // warp 0: where the share begins, warp 1: where it ends
+      const int64_t k = min(static_cast<int64_t>(cta) + warp, NW);
+      int64_t x = NW > 0 ? k * U / NW : 0;
+      int b = 0, h = 0, j = 0, off = 0;
+      if (x < U) {
+        int l = 0, r = a.B;                // before[l] <= x < before[r]
+        while (r - l > 1) {
+          const int m = (l + r) >> 1;
+          if (su.before[m] <= x) l = m;
+          else r = m;
+        }
+        b = l;
+        const int64_t per_head = (su.before[b + 1] - su.before[b]) / a.Hkv;
+        int64_t rest = x - su.before[b];
+        h = static_cast<int>(rest / per_head);
+        rest -= h * per_head;
+        const int n = su.n[b], L = su.L[b], items = (n + 2 * sub - 1) / (2 * sub);
+        int units = 0;
+        for (int j0 = 0; j0 < items; j0 += 32) {
+          int lo;
+          const int u = j0 + lane < items ? item_units(n, L, j0 + lane, sub, a.window, &lo) : 0;
+          int64_t inc = u;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int64_t t = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += t;
+          }
+          const unsigned m = __ballot_sync(0xffffffffu, inc > rest);
+          if (m != 0u) {
+            const int at = __ffs(m) - 1;
+            units = __shfl_sync(0xffffffffu, u, at);
+            off = static_cast<int>(rest - (__shfl_sync(0xffffffffu, inc, at) - units));
+            j = j0 + at;
+            break;
+          }
+          rest -= __shfl_sync(0xffffffffu, inc, 31);
+        }
+        // a cut near an item's border moves there
+        const int left = units - off;
+        if (off > 0 && k < NW && (off < kSnap || left <= kSnap)) {
+          if (off <= left) {
+            x -= off;
+            off = 0;
+          } else {
+            x += left;
+            off = 0;
+            const int all = (n + 2 * sub - 1) / (2 * sub);
+            if (++j == all) {
+              j = 0;
+              if (++h == a.Hkv) {
+                h = 0;
+                do ++b;
+                while (b < a.B && su.n[b] == 0);
+              }
+            }
+          }
+        }
+      }
+      if (lane == 0) {
+        if (warp == 0) {
+          sm.lo = static_cast<int64_t>(cta) < NW ? x : U;
+          sm.b = b;
+          sm.h = h;
+          sm.j = j;
+          sm.off = off;
+        } else {
+          sm.hi = x;
+        }
+      }
+    }
+  }
+  if (warp == kMmaWarp) tmem_alloc(smem_u32(&sm.tmem), 512);
+  fence_proxy_async_smem();                // the setup's place is the copies' now
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = static_cast<uint32_t>(sm.tmem);
+  const uint32_t tmem_o = tmem + 2 * kTile;
+  auto slot_at = [&](int i) { return ring + (i % C::kSlots) * C::kSlot; };   // i: K 2g, V 2g + 1
+
+  if (warp == kCopyWarp) {
+    // ================================================================ copies
+    const int64_t lo = sm.lo, hi = sm.hi;
+    int64_t pos = lo;
+    int b = sm.b, h = sm.h, j = sm.j, off = sm.off;
+    int d = 0, g = 0, q_fills[2] = {0, 0}, raws = 0;
+    int n = 0, L = 0, t0 = 0, loaded = -1;
+    int head[6] = {0, 0, 0, 0, 0, 0};
+    bool ok = true;
+    // K (kv 0) or V of tile g, whose page ids are the first lanes' `id`
+    auto copy_tile = [&](int kv, int id, bool valid, int hh) {
+      const int i = 2 * g + kv;
+      uint32_t full, dst;
       if constexpr (FP8) {
-        const uint32_t two = static_cast<const uint8_t*>(a.k_cache)[page + e] |
-                             static_cast<const uint8_t*>(a.v_cache)[page + e] << 8;
-        const uint32_t w = e4m3x2_to_f16x2(two);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
-        k = f.x * ks;
-        v = f.y * vs;
+        if (raws >= C::kRaws && !wait_warp(kRawEmpty + raws % 2, raws / 2 - 1)) return false;
+        full = bar(kRawFull + raws % 2);
+        dst = raw + (raws % 2) * C::kRaw;
+        ++raws;
       } else {
-        k = load16<D, BF16>(a.k_cache, page + e);
-        v = load16<D, BF16>(a.v_cache, page + e);
+        if (i >= C::kSlots && !wait_warp(kEmpty + i % C::kSlots, i / C::kSlots - 1)) return false;
+        full = bar(kFull + i % C::kSlots);
+        dst = slot_at(i);
       }
-      sk[e / D][e % D] = in ? k : 0.f;
-      sv[e / D][e % D] = in ? v : 0.f;
+      const unsigned m = __ballot_sync(0xffffffffu, valid);
+      if (lane == 0)
+        mbar_arrive_expect_tx(full, static_cast<uint32_t>(__popc(m)) * (FP8 ? 16u * D : 32u * D));
+      __syncwarp();
+      if (valid) {
+        const int64_t page = static_cast<int64_t>(id) * a.Hkv + hh;
+        if constexpr (FP8) {
+          const uint8_t* pool = static_cast<const uint8_t*>(kv ? a.v_cache : a.k_cache);
+          page_g2s(dst + lane * 16 * D, pool + page * 16 * D, 16 * D, full);
+        } else {
+#pragma unroll
+          for (int x = 0; x < C::kHalves; ++x)
+            box_g2s(dst + x * C::kSub + lane * 2048, kv ? &ka.tm_v : &ka.tm_k, 64 * x, 0,
+                    static_cast<int>(page), full);
+        }
+      }
+      return true;
+    };
+    while (ok && pos < hi) {
+      if (b != loaded) {                   // (bad starts and lengths were reported above)
+        const int s0 = a.starts[b], s1 = a.starts[b + 1];
+        n = s0 >= 0 && s1 >= s0 && s1 <= a.T ? s1 - s0 : 0;
+        L = a.context_lens[b];
+        L = L >= 0 && L <= a.max_context_len ? L : 0;
+        t0 = s0;
+        loaded = b;
+      }
+      const int items = (n + 2 * sub - 1) / (2 * sub);
+      if (items == 0) {
+        ++b;
+        continue;
+      }
+      int k0;
+      const int u = item_units(n, L, j, sub, a.window, &k0);
+      const int take = static_cast<int>(min(static_cast<int64_t>(u - off), hi - pos));
+      Desc x;
+      x.h = h;
+      x.b = b;
+      x.n = n;
+      x.L = L;
+      x.i0 = j * 2 * sub;
+      x.tokens = min(n - x.i0, 2 * sub);
+      x.t0 = t0 + x.i0;
+      const bool sees = L - n + x.i0 + x.tokens - 1 >= 0;
+      x.k_lo = sees ? k0 + off : 0;
+      x.k_hi = sees ? k0 + off + take : 0;
+      x.g0 = g;
+      x.whole = take == u;
+      x.part = off > 0 ? 0 : 1;
+      if (!x.whole) {
+        if (off > 0) {
+          head[kHasHead] = 1;
+          head[kHeadEnds] = off + take == u;
+        } else {
+          head[kHasTail] = 1;
+          head[kTailT0] = x.t0;
+          head[kTailH] = h;
+          head[kTailTokens] = x.tokens;
+        }
+      }
+      if (d >= kDescs && !wait_warp(kDEmpty + d % kDescs, d / kDescs - 1)) break;
+      if (lane == 0) {
+        sm.desc[d % kDescs] = x;
+        mbar_arrive(bar(kDFull + d % kDescs));
+      }
+      ++d;
+      __syncwarp();
+      // ---- its query rows
+      for (int w = 0; w < 2 && ok; ++w) {
+        const int2 r = sub_tiles(x, w, sub, a.window);
+        if (r.x == r.y) continue;
+        if (q_fills[w] > 0 && !wait_warp(kQEmpty + w, q_fills[w] - 1)) ok = false;
+        if (ok && lane == 0) {
+          mbar_arrive_expect_tx(bar(kQFull + w), static_cast<uint32_t>(C::kHalves * 128 * sub * G));
+#pragma unroll
+          for (int y = 0; y < C::kHalves; ++y)
+            box_g2s(q_at + w * C::kSlot + y * C::kSub, &ka.tm_q, 64 * y, h * G, x.t0 + w * sub,
+                    bar(kQFull + w));
+        }
+        ++q_fills[w];
+        __syncwarp();
+      }
+      // ---- its tiles: four tiles' page ids at a time, one tile ahead of the copies
+      const int32_t* table = a.block_tables + static_cast<int64_t>(b) * a.mbs;
+      const int last_page = (L + 15) / 16 - 1;
+      int ids = -1;
+      for (int t = x.k_lo; ok && t < x.k_hi; ++t, ++g) {
+        const int in4 = (t - x.k_lo) & 3;
+        if (in4 == 0) {
+          const int p = t * kPages + lane;
+          ids = p <= last_page && t + (lane >> 3) < x.k_hi ? table[p] : -1;
+        }
+        const int id = __shfl_sync(0xffffffffu, ids, in4 * 8 + (lane & 7));
+        const bool mine = lane < kPages && t * kPages + lane <= last_page;
+        const bool valid = mine && id >= 0 && id < a.num_blocks;
+        if (mine && !valid) atomicOr(a.status, kStatusBadBlock);
+        const unsigned m = __ballot_sync(0xffffffffu, valid);
+        Meta& mt = sm.meta[g % kMetas];
+        if (lane == 0) mt.valid = m;
+        if (FP8 && lane < kPages) {
+          const int64_t page = static_cast<int64_t>(valid ? id : 0) * a.Hkv + h;
+          mt.ks[lane] = valid ? a.k_scale[page] : 0.f;
+          mt.vs[lane] = valid ? a.v_scale[page] : 0.f;
+        }
+        __syncwarp();
+        ok = copy_tile(0, id, valid, h) && copy_tile(1, id, valid, h);
+      }
+      // ---- the next item
+      pos += take;
+      off = 0;
+      if (++j == items) {
+        j = 0;
+        if (++h == a.Hkv) {
+          h = 0;
+          ++b;
+        }
+      }
     }
-    __syncthreads();
-    for (int r = 0; r < kPer; ++r) {
-      for (int j = 0; j < 16; ++j) {
-        const int at = p * 16 + j;
-        if (at > pos[r] || (a.window > 0 && at <= pos[r] - a.window)) continue;
-        float s = 0.f;
-        for (int e = 0; e < E; ++e) s = fmaf(q[r][e], sk[j][lane * E + e], s);
-        for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-        const float mn = fmaxf(m[r], s);
-        if (mn == -INFINITY) continue;
-        const float f = expf(m[r] - mn), x = expf(s - mn);
-        m[r] = mn;
-        l[r] = l[r] * f + x;
-        for (int e = 0; e < E; ++e) o[r][e] = o[r][e] * f + x * sv[j][lane * E + e];
+    if (ok && (d < kDescs || wait_warp(kDEmpty + d % kDescs, d / kDescs - 1))) {
+      if (lane == 0) {
+        sm.desc[d % kDescs].h = -1;
+        mbar_arrive(bar(kDFull + d % kDescs));
       }
+    }
+    if (FP8 && lane == 0) {                // the converting warps' end
+      *reinterpret_cast<volatile int*>(&sm.raw_end) = raws;
+      __threadfence_block();
+    }
+    if (lane == 0)
+      for (int i = 0; i < 6; ++i) ka.ws_head[cta * kHeader + i] = head[i];
+    // no copy outlives the CTA
+    if (lane == 0) {
+      const uint64_t since = global_ns();
+      const uint64_t limit = ka.wait_limit_ns > kWaitLimitNs ? ka.wait_limit_ns : kWaitLimitNs;
+      auto settle = [&](int bb, int fills) {
+        while (fills > 0 && !mbar_try_wait(bar(bb), (fills - 1) & 1) && global_ns() - since < limit) {
+        }
+      };
+      for (int w = 0; w < 2; ++w) settle(kQFull + w, q_fills[w]);
+      if (FP8) {
+        for (int r = 0; r < 2; ++r) settle(kRawFull + r, (raws - r + 1) / 2);
+      } else {
+        for (int s = 0; s < C::kSlots; ++s) settle(kFull + s, (2 * g - s + C::kSlots - 1) / C::kSlots);
+      }
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    // ================================================================ products
+    if (lane == 0) {
+      constexpr uint32_t kIdQK = umma_idesc_f16<kMmaBf16>(kTile, kTile, false);
+      constexpr uint32_t kIdPV = umma_idesc_f16<kMmaBf16>(kTile, D, false) | kBMajorN;
+      struct Cursor {
+        int d = 0, t = 0, e = 0, k_lo = 0, g0 = 0, g_end = 0, q = 0, p = 0;
+        bool open = false, end = false, pv = false, first = true;
+      } cur[2];
+      int k_pos[2] = {0, 0}, v_pos[2] = {0, 0}, k_rel = 0, v_rel = 0;   // tiles passed, slots released
+      bool issued = false;
+      uint64_t idle_since = 0;
+      auto ready = [&](int b, int n) { return test_wait(bar(b), n & 1); };
+      auto full = [&](int i) { return ready(kFull + i % C::kSlots, i / C::kSlots); };
+      while (!(cur[0].end && cur[1].end)) {
+        bool did = false;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          Cursor& c = cur[w];
+          if (c.end) continue;
+          if (!c.open) {
+            if (!ready(kDFull + c.d % kDescs, c.d / kDescs)) continue;
+            const Desc& x = sm.desc[c.d % kDescs];
+            did = true;
+            if (x.h < 0) {
+              c.end = true;
+              k_pos[w] = v_pos[w] = INT_MAX;
+              continue;
+            }
+            const int2 r = sub_tiles(x, w, sub, a.window);
+            c.open = true;
+            c.first = true;
+            c.pv = false;
+            c.k_lo = x.k_lo;
+            c.g0 = x.g0;
+            c.g_end = x.g0 + x.k_hi - x.k_lo;
+            c.t = r.x;
+            c.e = r.y;
+            if (r.x < r.y) k_pos[w] = v_pos[w] = c.g0 + c.t - c.k_lo;
+          }
+          const uint32_t ts = tmem + w * kTile, to = tmem_o + w * D;
+          if (c.pv) {
+            const int i = 2 * (c.g0 + c.t - c.k_lo) + 1;
+            if (ready(kPFull + w, c.p) && full(i)) {
+              tc_fence_after();
+              if (!*reinterpret_cast<volatile int*>(&sm.skip[w])) {
+                const uint64_t dv = umma_desc_sw128(slot_at(i), C::kSub, 1024);
+#pragma unroll
+                for (int k = 0; k < kTile / 16; ++k)
+                  umma_f16_ts(to, ts + 8 * k, dv + static_cast<uint64_t>(k * (2048 >> 4)), kIdPV,
+                              !(c.first && k == 0));
+              }
+              issued = true;
+              c.first = false;
+              c.pv = false;
+              ++c.p;
+              v_pos[w] = c.g0 + c.t - c.k_lo + 1;
+              if (++c.t == c.e) umma_commit(bar(kODone + w));
+              did = true;
+            }
+          }
+          if (!c.pv && c.t < c.e) {
+            const int i = 2 * (c.g0 + c.t - c.k_lo);
+            if ((!c.first || ready((FP8 && BF16 ? kQConv : kQFull) + w, c.q)) && full(i)) {
+              mbar_arrive(bar(kSFull + w));   // (orders the tile's meta before the softmax's reads)
+              tc_fence_after();
+              const uint64_t dq = umma_desc_sw128(q_at + w * C::kSlot, 16, 1024);
+              const uint64_t dk = umma_desc_sw128(slot_at(i), 16, 1024);
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k) {
+                const uint64_t o = static_cast<uint64_t>(((k >> 2) * C::kSub + (k & 3) * 32) >> 4);
+                umma_f16(ts, dq + o, dk + o, kIdQK, k > 0);
+              }
+              umma_commit(bar(kSFull + w));
+              issued = true;
+              if (c.t + 1 == c.e) {
+                umma_commit(bar(kQEmpty + w));
+                ++c.q;
+              }
+              k_pos[w] = c.g0 + c.t - c.k_lo + 1;
+              c.pv = true;
+              did = true;
+            }
+          }
+          if (!c.pv && c.t == c.e) {       // the piece is through for this subtile
+            k_pos[w] = v_pos[w] = c.g_end;
+            c.open = false;
+            mbar_arrive(bar(kDEmpty + c.d % kDescs));
+            ++c.d;
+            did = true;
+          }
+        }
+        // slots that both subtiles have passed
+        const int k_min = min(min(k_pos[0], k_pos[1]), max(k_pos[0] == INT_MAX ? 0 : k_pos[0], k_pos[1] == INT_MAX ? 0 : k_pos[1]));
+        const int v_min = min(min(v_pos[0], v_pos[1]), max(v_pos[0] == INT_MAX ? 0 : v_pos[0], v_pos[1] == INT_MAX ? 0 : v_pos[1]));
+        for (; k_rel < k_min; ++k_rel) umma_commit(bar(kEmpty + (2 * k_rel) % C::kSlots));
+        for (; v_rel < v_min; ++v_rel) umma_commit(bar(kEmpty + (2 * v_rel + 1) % C::kSlots));
+        if (did) {
+          idle_since = 0;
+          continue;
+        }
+        if (*dead) break;
+        const uint64_t now = global_ns();
+        if (idle_since == 0) {
+          idle_since = now;
+        } else if (now - idle_since > ka.wait_limit_ns) {
+          *dead = 1;
+          atomicOr(a.status, kStatusTimeout);
+          break;
+        }
+      }
+      if (issued) {                        // no product outlives the CTA
+        umma_commit(bar(kFin));
+        const uint64_t since = global_ns();
+        const uint64_t limit = ka.wait_limit_ns > kWaitLimitNs ? ka.wait_limit_ns : kWaitLimitNs;
+        while (!mbar_try_wait(bar(kFin), 0) && global_ns() - since < limit) {
+        }
+      }
+    }
+    __syncwarp();
+  } else if (FP8 && warp >= kConvWarp) {
+    // ================================================================ codes to f16
+    const int ct = tid - kConvWarp * 32;
+    for (int f = 0;; ++f) {
+      // the next fill, or the end
+      const uint64_t since = global_ns();
+      bool got = false, end = false;
+      while (!got && !end) {
+        got = mbar_try_wait(bar(kRawFull + f % 2), (f / 2) & 1);
+        if (!got) {
+          end = f >= *reinterpret_cast<volatile int*>(&sm.raw_end) || *dead;
+          if (!end && global_ns() - since > ka.wait_limit_ns) {
+            *dead = 1;
+            atomicOr(a.status, kStatusTimeout);
+            end = true;
+          }
+        }
+      }
+      if (!__all_sync(0xffffffffu, got)) break;
+      if (f >= C::kSlots && !wait_warp(kEmpty + f % C::kSlots, f / C::kSlots - 1)) break;
+      const uint32_t src = raw + (f % 2) * C::kRaw, dst = slot_at(f);
+      constexpr int kChunks = D / 16;      // 16 codes each, of a row
+#pragma unroll 4
+      for (int i = ct; i < kTile * kChunks; i += kConvWarps * 32) {
+        const uint4 codes = lds128(src + 16 * i);
+        const int row = i / kChunks, c = i % kChunks, half = c / 4, p = (c % 4) * 2;
+        uint4 lo, hi;
+        lo.x = e4m3x2_to_f16x2(codes.x & 0xffffu);
+        lo.y = e4m3x2_to_f16x2(codes.x >> 16);
+        lo.z = e4m3x2_to_f16x2(codes.y & 0xffffu);
+        lo.w = e4m3x2_to_f16x2(codes.y >> 16);
+        hi.x = e4m3x2_to_f16x2(codes.z & 0xffffu);
+        hi.y = e4m3x2_to_f16x2(codes.z >> 16);
+        hi.z = e4m3x2_to_f16x2(codes.w & 0xffffu);
+        hi.w = e4m3x2_to_f16x2(codes.w >> 16);
+        const uint32_t at = dst + half * C::kSub + row * 128;
+        // (the other half's lanes store their two chunks in the other order: no bank twice)
+        const int p0 = half ? p + 1 : p, p1 = half ? p : p + 1;
+        sts128(at + ((p0 ^ (row & 7)) << 4), half ? hi : lo);
+        sts128(at + ((p1 ^ (row & 7)) << 4), half ? lo : hi);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar(kFull + f % C::kSlots));
+        mbar_arrive(bar(kRawEmpty + f % 2));
+      }
+    }
+  } else if (warp < 8) {
+    // ================================================================ softmax
+    const int w = warp >> 2, wq = warp & 3, r = tid & 127;
+    const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
+    const uint32_t ts = tmem + lanes + w * kTile, to = tmem_o + lanes + w * D;
+    const int tok = r / G, hd = r - tok * G;
+    int s_n = 0, o_n = 0, q_n = 0, votes = 0;   // completions seen
+    bool ok = true;
+    for (int d = 0; ok; ++d) {
+      if (!wait_warp(kDFull + d % kDescs, d / kDescs)) break;
+      const Desc x = sm.desc[d % kDescs];
+      if (x.h < 0) break;
+      const int2 tiles = sub_tiles(x, w, sub, a.window);
+      const int cnt = min(max(x.tokens - w * sub, 0), sub);
+      const int first = x.L - x.n + x.i0 + w * sub, last = first + cnt - 1;
+      const int pos = first + tok;         // this row's (rows behind the subtile's: any)
+      float off = -INFINITY, l = 0.f, ref = 1.f;
+      float sl2 = ka.sl2;
+      if (FP8 && BF16 && tiles.x < tiles.y) {
+        // bf16 rows to f16, scaled by a power of two so that the row's largest element lies
+        // in [2^14, 2^15)
+        if (!wait_warp(kQFull + w, q_n)) break;
+        const uint32_t row = q_at + w * C::kSlot + r * 128;
+        float big = 0.f;
+#pragma unroll
+        for (int y = 0; y < C::kHalves; ++y)
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const uint4 v = lds128(row + y * C::kSub + c * 16);
+            for (const uint32_t u : {v.x, v.y, v.z, v.w})
+              big = fmaxf(big, fmaxf(fabsf(__uint_as_float(u << 16)), fabsf(__uint_as_float(u & 0xffff0000u))));
+          }
+        const int e = big > 0.f && big < INFINITY ? 14 - ilogbf(big) : 0;
+        // 2^e in two factors: e reaches 147
+        const float f0 = __uint_as_float(static_cast<uint32_t>(127 + e / 2) << 23);
+        const float f1 = __uint_as_float(static_cast<uint32_t>(127 + e - e / 2) << 23);
+#pragma unroll
+        for (int y = 0; y < C::kHalves; ++y)
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            uint4 v = lds128(row + y * C::kSub + c * 16);
+            for (uint32_t* u : {&v.x, &v.y, &v.z, &v.w})
+              *u = pack2<false>(__uint_as_float(*u << 16) * f0 * f1, __uint_as_float(*u & 0xffff0000u) * f0 * f1);
+            sts128(row + y * C::kSub + c * 16, v);
+          }
+        sl2 = fmaxf(sl2 / f0 / f1, 1e-37f);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kQConv + w));
+        ++q_n;
+      }
+      for (int t = tiles.x; t < tiles.y; ++t) {
+        const int g = x.g0 + t - x.k_lo;
+        if (!wait_warp(kSFull + w, s_n)) {
+          ok = false;
+          break;
+        }
+        ++s_n;
+        tc_fence_after();
+        const Meta& mt = sm.meta[g % kMetas];
+        const unsigned valid = mt.valid;
+        const int p0 = t * kTile;
+        const bool edge = valid != 0xffu || p0 + kTile - 1 > first ||
+                          (a.window > 0 && p0 < last - a.window + 1);
+        // columns [jl, jh) of the tile are this row's
+        const int jh = pos + 1 - p0, jl = a.window > 0 ? pos - a.window + 1 - p0 : 0;
+        auto sees = [&](int j) { return j >= jl && j < jh && ((valid >> (j >> 4)) & 1u); };
+        auto scores = [&](int c, float (&v)[32]) {   // columns 32c .. 32c + 31
+          tmem_ld<32>(ts + 32 * c, v);
+          tmem_wait_ld();
+          if (ka.negative) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = -v[j];
+          }
+          if (edge) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (!sees(32 * c + j)) v[j] = -INFINITY;
+          }
+        };
+        // ---- the row's maximum
+        float m = -INFINITY, v_big = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float v[32];
+          scores(c, v);
+          if constexpr (FP8) {
+            m = fmaxf(m, max_of<16>(v, 0, -INFINITY) * fmaxf(mt.ks[2 * c], 1e-37f));
+            m = fmaxf(m, max_of<16>(v, 16, -INFINITY) * fmaxf(mt.ks[2 * c + 1], 1e-37f));
+            v_big = fmaxf(v_big, fmaxf(mt.vs[2 * c], mt.vs[2 * c + 1]));
+          } else {
+            m = max_of<32>(v, 0, m);
+          }
+        }
+        m *= sl2;
+        // ---- a new offset (and reference of V's scales) where the standing one does not do
+        const bool start = t == tiles.x;
+        const bool move = m > off + kSlack || (FP8 && v_big > 2.f * ref) || start;
+        if (__any_sync(0xffffffffu, move)) {
+          float f = 1.f;
+          if (move) {
+            const float to_off = fmaxf(off, m);
+            const float fl = off == to_off ? 1.f : fast_exp2(off - to_off);
+            f = fl;
+            if (FP8) {
+              // a power of two at or above the largest scale so far
+              const float top = fmaxf(v_big, 1e-30f);
+              const float new_ref = start ? __uint_as_float((__float_as_uint(top) + 0x7fffffu) & 0x7f800000u)
+                                          : fmaxf(ref, __uint_as_float((__float_as_uint(top) + 0x7fffffu) & 0x7f800000u));
+              f *= ref / new_ref;
+              ref = new_ref;
+            }
+            off = to_off;
+            l *= fl;
+          }
+          if (!start) {                    // O, whose last product is done (S came after it)
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              float o[32];
+              tmem_ld<32>(to + 32 * c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] *= f;
+              tmem_st<32>(to + 32 * c, o);
+            }
+            tmem_wait_st();
+          }
+        }
+        // ---- the weights, in S's place
+        const float sub_off = (off == -INFINITY ? 0.f : off) - kLift;
+        const float inv_ref = FP8 ? 1.f / ref : 1.f;
+        float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float v[32], p[16];
+          scores(c, v);
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            float k = sl2, u = 1.f;
+            if constexpr (FP8) {
+              k = fmaxf(sl2 * mt.ks[2 * c + j / 16], 1e-37f);
+              u = mt.vs[2 * c + j / 16] * inv_ref;
+            }
+            float e0 = fast_exp2(fmaf(v[j], k, -sub_off));
+            float e1 = fast_exp2(fmaf(v[j + 1], k, -sub_off));
+            l0 += e0;
+            l1 += e1;
+            if constexpr (FP8) {
+              e0 *= u;
+              e1 *= u;
+            }
+            p[j / 2] = __uint_as_float(pack2<kMmaBf16>(e0, e1));
+          }
+          tmem_st<16>(ts + 16 * c, p);
+        }
+        l += l0 + l1;
+        tmem_wait_st();
+        if (edge) {
+          // token r of the tile: no data, a row of zeros; else is every value finite?
+          const int i = 2 * g + 1;
+          if (!wait_warp(kFull + i % C::kSlots, i / C::kSlots)) {
+            ok = false;
+            break;
+          }
+          const bool data = p0 + r < x.L && ((valid >> (r >> 4)) & 1u);
+          const uint32_t vrow = slot_at(i) + r * 128;
+          bool odd = false;
+#pragma unroll
+          for (int y = 0; y < C::kHalves; ++y)
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              const uint4 v = lds128(vrow + y * C::kSub + c * 16);
+              constexpr uint32_t kExp = kMmaBf16 ? 0x7f80u : 0x7c00u;
+              for (const uint32_t u : {v.x, v.y, v.z, v.w})
+                odd |= (u & kExp) == kExp || ((u >> 16) & kExp) == kExp;
+              if (!data && (v.x | v.y | v.z | v.w) != 0u)
+                sts128(vrow + y * C::kSub + c * 16, make_uint4(0u, 0u, 0u, 0u));
+            }
+          fence_proxy_async_smem();
+          const bool any = __any_sync(0xffffffffu, odd && data);
+          if (lane == 0) {
+            sm.flag[w][wq] = any;
+            mbar_arrive(bar(kVote + w));
+          }
+          if (!wait_warp(kVote + w, votes++)) {
+            ok = false;
+            break;
+          }
+          const volatile int* fl = sm.flag[w];
+          const bool self = fl[0] | fl[1] | fl[2] | fl[3];
+          if (self) {
+            // this tile's product by the rows' own threads, over the tokens that they see
+            for (int c0 = 0; c0 < D; c0 += 8) {
+              float o[8];
+              if (start) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) o[j] = 0.f;
+              } else {
+                tmem_ld<8>(to + c0, o);
+              }
+              const uint32_t col = slot_at(i) + (c0 / 64) * C::kSub;
+              for (int j0 = 0; j0 < kTile; j0 += 8) {
+                float p[4];
+                tmem_ld<4>(ts + j0 / 2, p);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                  const int at = j0 + j;
+                  const uint32_t two = __float_as_uint(p[j / 2]);
+                  const uint32_t one = j & 1 ? two >> 16 : two & 0xffffu;
+                  const float pf = kMmaBf16 ? __uint_as_float(one << 16)
+                                            : __half2float(__ushort_as_half(static_cast<unsigned short>(one)));
+                  const uint4 v = lds128(col + at * 128 + ((((c0 % 64) / 8) ^ (at & 7)) << 4));
+                  if (!sees(at)) continue;
+                  const uint32_t us[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    float2 f;
+                    if constexpr (kMmaBf16)
+                      f = make_float2(__uint_as_float(us[k] << 16), __uint_as_float(us[k] & 0xffff0000u));
+                    else
+                      f = __half22float2(*reinterpret_cast<const __half2*>(&us[k]));
+                    o[2 * k] = fmaf(pf, f.x, o[2 * k]);
+                    o[2 * k + 1] = fmaf(pf, f.y, o[2 * k + 1]);
+                  }
+                }
+              }
+              __syncwarp();
+              tmem_st<8>(to + c0, o);
+            }
+            tmem_wait_st();
+          }
+          if (wq == 0 && lane == 0) sm.skip[w] = self;
+        } else if (wq == 0 && lane == 0) {
+          sm.skip[w] = 0;
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kPFull + w));
+      }
+      if (!ok) break;
+      // ---- the piece's result
+      const bool some = tiles.x < tiles.y;
+      if (some) {
+        if (!wait_warp(kODone + w, o_n)) break;
+        ++o_n;
+        tc_fence_after();
+      }
+      const bool row_live = r < cnt * G;
+      if (x.whole) {
+        const float inv = l == 0.f ? 0.f : ref / l;   // (a NaN stays one)
+        uint16_t* out = static_cast<uint16_t*>(a.out) +
+                        ((static_cast<int64_t>(x.t0) + w * sub + tok) * a.Hq + x.h * G + hd) * D;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          float o[32];
+          if (some) {
+            tmem_ld<32>(to + 32 * c, o);
+            tmem_wait_ld();
+          }
+          if (row_live) {
+            uint32_t p[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              p[j] = some && l != 0.f ? pack2<BF16>(o[2 * j] * inv, o[2 * j + 1] * inv) : 0u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<uint4*>(out + 32 * c + 8 * j) =
+                  make_uint4(p[4 * j], p[4 * j + 1], p[4 * j + 2], p[4 * j + 3]);
+          }
+          __syncwarp();
+        }
+      } else {
+        const int64_t at = (static_cast<int64_t>(cta) * 2 + x.part) * 256 + w * kTile + r;
+        if (some) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            float o[32];
+            tmem_ld<32>(to + 32 * c, o);
+            tmem_wait_ld();
+            float4* dst = reinterpret_cast<float4*>(ka.ws_acc + at * D + 32 * c);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              dst[j] = make_float4(o[4 * j] * ref, o[4 * j + 1] * ref, o[4 * j + 2] * ref, o[4 * j + 3] * ref);
+          }
+        }
+        ka.ws_ml[at] = make_float2(off, l);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kDEmpty + d % kDescs));
     }
   }
-  for (int r = 0; r < kPer; ++r) {
-    const int row = tile * kRows + warp * kPer + r, i = row / a.group, g = row % a.group;
-    if (row >= n * a.group) continue;
-    uint16_t* out = static_cast<uint16_t*>(a.out) + ((static_cast<int64_t>(t0) + i) * a.Hq + h * a.group + g) * D;
-    for (int e = 0; e < E; ++e)
-      out[lane * E + e] = static_cast<uint16_t>(pack2<BF16>(l[r] > 0.f ? o[r][e] / l[r] : 0.f, 0.f));
+  // ---- every role has left its loop, with nothing in flight
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
   }
+}
+
+// Joins the parts of a cut item: CTA w's item is the one that CTA w of the launch
+// before left open, with a part in each of the next ones up to where it ends.
+constexpr int kMergeRows = 16;             // rows a CTA: two a warp
+template <int D, bool BF16>
+__global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Args ka, int grid) {
+  const PrefillArgs& a = ka.a;
+  const int w = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int* head = ka.ws_head + w * kHeader;
+  if (!head[kHasTail]) return;
+  const int t0 = head[kTailT0], h = head[kTailH], tokens = head[kTailTokens];
+  int parts = 2;                             // (w, 1), (w + 1, 0), ..
+  while (w + parts < grid && !ka.ws_head[(w + parts - 1) * kHeader + kHeadEnds]) ++parts;
+  constexpr int E = D / 32;
+  for (int i = warp; i < kMergeRows; i += 8) {
+    const int row = blockIdx.y * kMergeRows + i, s = row / kTile, r = row % kTile;
+    const int tok = r / a.group, hd = r - tok * a.group;
+    if (tok >= ka.sub || s * ka.sub + tok >= tokens) continue;
+    auto at = [&](int p) { return (p == 0 ? w * 2 + 1 : (w + p) * 2) * INT64_C(256) + row; };
+    float top = -INFINITY;
+    for (int p = lane; p < parts; p += 32) {
+      const float2 ml = ka.ws_ml[at(p)];
+      if (ml.y != 0.f) top = fmaxf(top, ml.x);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    float acc[E] = {}, l = 0.f;
+    for (int p = 0; p < parts; ++p) {
+      const float2 ml = ka.ws_ml[at(p)];
+      if (ml.y == 0.f) continue;           // nothing seen: no O was written
+      const float f = ml.x == top ? 1.f : fast_exp2(ml.x - top);
+      l += ml.y * f;
+      const float* src = ka.ws_acc + at(p) * D + lane * E;
+      float v[E];
+      if constexpr (E == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(src);
+        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(src);
+        v[0] = x.x, v[1] = x.y;
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += v[e] * f;
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint32_t* out = reinterpret_cast<uint32_t*>(
+        static_cast<uint16_t*>(a.out) +
+        ((static_cast<int64_t>(t0) + s * ka.sub + tok) * a.Hq + h * a.group + hd) * D + lane * E);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) out[e / 2] = pack2<BF16>(acc[e] * inv, acc[e + 1] * inv);
+  }
+}
+
+// --------------------------------------------------------------------------- host
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }();
+  return fn;
+}
+
+// The map of a 3-D tensor of 16-bit elements (innermost first; the innermost dense) in
+// boxes of 64 elements x box1 x box2 with the 128-byte swizzle.  Encoding is host work
+// of a few hundred nanoseconds, made for each call: nothing is kept.
+cudaError_t tensor_map(CUtensorMap* m, const void* p, const cuuint64_t (&dims)[3],
+                       const cuuint64_t (&strides)[2], unsigned box1, unsigned box2) {
+  const auto enc = encoder();
+  if (enc == nullptr) return cudaErrorNotSupported;
+  const cuuint32_t box[3] = {64, box1, box2};
+  const cuuint32_t elem[3] = {1, 1, 1};
+  const CUresult r =
+      enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(p), dims, strides, box, elem,
+          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+struct Space {
+  size_t ml, acc, total;
+};
+Space space(int grid, int D) {
+  Space s{};
+  s.ml = (static_cast<size_t>(grid) * kHeader * 4 + 255) / 256 * 256;
+  s.acc = s.ml + static_cast<size_t>(grid) * 2 * 256 * 8;
+  s.total = s.acc + static_cast<size_t>(grid) * 2 * 256 * D * 4;
+  return s;
+}
+
+template <int D, bool BF16, bool FP8>
+cudaError_t launch(const PrefillArgs& args, cudaStream_t s) {
+  using C = Cfg<D, FP8>;
+  Args k{};
+  const int grid = device_sm_count();
+  const size_t smem = 1024 + C::kBig + sizeof(Small);
+  static_assert(1024 + C::kBig + sizeof(Small) <= 232448, "227 KB");
+  static_assert(sizeof(Setup) <= C::kBig, "the setup fits in the operands' place");
+  auto* kern = prefill_kernel<D, BF16, FP8>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  k.sub = kTile / args.group;
+  {
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(args.Hq),
+                                static_cast<cuuint64_t>(args.T)};
+    const cuuint64_t strides[2] = {2 * D, static_cast<cuuint64_t>(args.q_stride) * 2};
+    e = tensor_map(&k.tm_q, args.q, dims, strides, static_cast<unsigned>(args.group),
+                   static_cast<unsigned>(k.sub));
+    if (e != cudaSuccess) return e;
+  }
+  if (!FP8) {
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), 16,
+                                static_cast<cuuint64_t>(args.num_blocks) * args.Hkv};
+    const cuuint64_t strides[2] = {2 * D, 32 * D};
+    e = tensor_map(&k.tm_k, args.k_cache, dims, strides, 16, 1);
+    if (e == cudaSuccess) e = tensor_map(&k.tm_v, args.v_cache, dims, strides, 16, 1);
+    if (e != cudaSuccess) return e;
+  }
+  const Space sp = space(grid, D);
+  uint8_t* ws = static_cast<uint8_t*>(args.workspace);
+  k.ws_head = reinterpret_cast<int*>(ws);
+  k.ws_ml = reinterpret_cast<float2*>(ws + sp.ml);
+  k.ws_acc = reinterpret_cast<float*>(ws + sp.acc);
+  k.negative = args.scale < 0.f;
+  // scale 0: every score counts alike, and a masked one still is -inf
+  const float sl2 = fabsf(args.scale) * 1.4426950408889634f;
+  k.sl2 = sl2 > 1e-30f ? sl2 : 1e-30f;
+  k.wait_limit_ns = kWaitLimitNs;
+  // an item of up to 2 kSnap tiles is never cut: every place in it is that near a border
+  const bool cuts = args.max_context_len > 2 * kSnap * kTile;
+  for (int b0 = 0; b0 < args.B; b0 += kMaxSeqs) {
+    k.a = args;
+    k.a.B = args.B - b0 < kMaxSeqs ? args.B - b0 : kMaxSeqs;
+    k.a.block_tables = args.block_tables + static_cast<int64_t>(b0) * args.mbs;
+    k.a.context_lens = args.context_lens + b0;
+    k.a.starts = args.starts + b0;
+    kern<<<grid, C::kThreads, smem, s>>>(k);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (!cuts) continue;
+    merge_kernel<D, BF16><<<dim3(static_cast<unsigned>(grid), 256 / kMergeRows), 256, 0, s>>>(k, grid);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 template <int D, bool BF16>
 cudaError_t launch(const PrefillArgs& a, bool fp8, cudaStream_t s) {
-  const int64_t rows = static_cast<int64_t>(a.T) * a.group;
-  const dim3 grid(static_cast<unsigned>(rows / kRows + a.B), static_cast<unsigned>(a.Hkv));
-  if (fp8) prefill_kernel<D, BF16, true><<<grid, kWarps * 32, 0, s>>>(a);
-  else prefill_kernel<D, BF16, false><<<grid, kWarps * 32, 0, s>>>(a);
-  return cudaGetLastError();
+  return fp8 ? launch<D, BF16, true>(a, s) : launch<D, BF16, false>(a, s);
 }
 
 }  // namespace
 
-size_t prefill_workspace_bytes(int, int, int, int, int) { return 256; }
+size_t prefill_workspace_bytes(int, int, int, int, int D) { return space(device_sm_count(), D).total; }
 
 cudaError_t launch_prefill(const PrefillArgs& a, bool fp8, bool bf16, cudaStream_t s) {
   if (a.D == 64) return bf16 ? launch<64, true>(a, fp8, s) : launch<64, false>(a, fp8, s);

