@@ -11,9 +11,8 @@
 //   O[128 rows][D]          += P . V         (P in tensor memory, in S's place)
 //
 // Roles of a CTA, one an SM:
-//   warps 0-3, 4-7   the softmax of one subtile each, a thread a row: S is read twice
-//                    from tensor memory (maximum, then weights), so a thread holds 32
-//                    of its values at a time; P goes back as 16-bit pairs;
+//   warps 0-3, 4-7   the softmax of one subtile each, a thread a row, whose 128 scores it
+//                    holds in registers; P goes back to tensor memory as 16-bit pairs;
 //   warp 8           walks the CTA's pieces, copies Q, K and V (TMA);
 //   warp 9           one thread issues the products, each as soon as its operands are
 //                    there.  A subtile's Q.K of the next tile follows its P.V in the
@@ -57,10 +56,17 @@ constexpr int kTile = 128;                 // tokens of a tile, rows of a subtil
 constexpr int kPages = kTile / 16;
 constexpr float kSlack = 8.f;              // log2 units
 constexpr int kSnap = 4;                   // tiles
+// What an item costs besides its tiles (its queries, a pipeline that fills and drains, edges,
+// the result), in tiles: what it adds to the shares.
+constexpr int kItemCost = 4;
 constexpr int kMaxSeqs = 512;              // sequences a launch sorts
 constexpr int kDescs = 4;                  // pieces known ahead
 constexpr int kMetas = 8;                  // tiles whose pages' validity and scales are kept
-constexpr int kCopyWarp = 8, kMmaWarp = 9, kConvWarp = 10, kConvWarps = 4;
+constexpr int kCopyWarp = 8, kMmaWarp = 9, kConvWarp = 11, kConvWarps = 1;
+constexpr int kThreads = 384;
+// Three warpgroups of 168 registers a thread (65536 / 384), re-divided: 216 for a row's
+// 128 scores and their weights, 72 for the rest; 2 x 216 + 72 = 3 x 168.
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 constexpr int kHeader = 16;                // ints a CTA's header in the workspace
 
 struct Args {
@@ -87,7 +93,6 @@ struct Cfg {
   static constexpr int kRaws = FP8 ? 2 : 0;
   // Q of both subtiles, the ring, the codes: 224 KB at head_dim 128, 160 KB at 64
   static constexpr int kSlots = FP8 ? (D == 128 ? 4 : 6) : (D == 128 ? 5 : 8);
-  static constexpr int kThreads = FP8 ? 448 : 320;
   static constexpr int kQ = 2 * kSlot;
   static constexpr int kBig = kQ + kSlots * kSlot + kRaws * kRaw;
 };
@@ -113,12 +118,13 @@ enum : int {                               // mbarriers
   kQConv = kQEmpty + 2,
   kSFull = kQConv + 2,
   kPFull = kSFull + 2,
-  kODone = kPFull + 2,
+  kPHalf = kPFull + 2,                     // the second half of P
+  kODone = kPHalf + 2,
   kVote = kODone + 2,
   kDFull = kVote + 2,
   kDEmpty = kDFull + kDescs,
   kFin = kDEmpty + kDescs,
-  kBars = kFin + 1
+  kBars = kFin + 2
 };
 
 struct Small {                             // shared memory behind the operands
@@ -152,16 +158,11 @@ __device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, vola
   }
 }
 
-// Whether a phase is complete, without waiting.
-__device__ __forceinline__ bool test_wait(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+  return one != 0u;
 }
 
 // A box of a tensor map into shared memory (K and V of a prompt are read by many CTAs:
@@ -212,15 +213,57 @@ __device__ __forceinline__ int2 sub_tiles(const Desc& d, int w, int sub, int win
   return a < e ? make_int2(a, e) : make_int2(0, 0);
 }
 
+// The largest of N values (four chains; NaN is passed over).
 template <int N>
-__device__ __forceinline__ float max_of(const float (&v)[32], int from, float m) {
+__device__ __forceinline__ float max_of(const float* v) {
+  float m[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-  for (int j = 0; j < N; j += 2) m = fmaxf(m, fmaxf(v[from + j], v[from + j + 1]));
-  return m;
+  for (int j = 4; j < N; j += 8)
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      m[k] = j + 4 + k < N ? fmaxf(fmaxf(m[k], v[j + k]), v[j + 4 + k]) : fmaxf(m[k], v[j + k]);
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+// A warpgroup's registers a thread from here on (all its warps).
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair(float2 x) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x.x), "f"(x.y));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pair(a)), "l"(pair(b)), "l"(pair(c)));
+  return unpair(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair(a)), "l"(pair(b)));
+  return unpair(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair(a)), "l"(pair(b)));
+  return unpair(r);
 }
 
 template <int D, bool BF16, bool FP8>
-__global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
 prefill_kernel(const __grid_constant__ Args ka) {
   using C = Cfg<D, FP8>;
   constexpr bool kMmaBf16 = BF16 && !FP8;  // the products' operand type
@@ -246,7 +289,7 @@ prefill_kernel(const __grid_constant__ Args ka) {
   // ---- 1. the items' lengths, and this CTA's share of them
   {
     Setup& su = *reinterpret_cast<Setup*>(smem);
-    for (int b = tid; b < a.B; b += C::kThreads) {
+    for (int b = tid; b < a.B; b += kThreads) {
       const int s0 = a.starts[b], s1 = a.starts[b + 1], L = a.context_lens[b];
       const bool good = s0 >= 0 && s1 >= s0 && s1 <= a.T, fits = L >= 0 && L <= a.max_context_len;
       if (cta == 0 && (!good || (!fits && s1 > s0))) atomicOr(a.status, kStatusBadLen);
@@ -260,10 +303,11 @@ prefill_kernel(const __grid_constant__ Args ka) {
       for (int i = 0; i < kBars; ++i) {
         int n = 1;
         if (FP8 && i >= kFull && i < kFull + 8) n = kConvWarps;
+        if (i >= kEmpty && i < kEmpty + 8) n = 2;
         if (i == kRawEmpty || i == kRawEmpty + 1) n = kConvWarps;
         if (i >= kQConv && i < kQConv + 2) n = 4;
         if (i >= kSFull && i < kSFull + 2) n = 2;
-        if (i >= kPFull && i < kPFull + 2) n = 4;
+        if (i >= kPFull && i < kPHalf + 2) n = 4;
         if (i >= kVote && i < kVote + 2) n = 4;
         if (i >= kDEmpty && i < kDEmpty + kDescs) n = 2 + 8;
         mbar_init(bar(i), n);
@@ -271,11 +315,12 @@ prefill_kernel(const __grid_constant__ Args ka) {
       mbar_init_fence();
     }
     __syncthreads();
-    for (int b = warp; b < a.B; b += C::kThreads / 32) {
+    for (int b = warp; b < a.B; b += kThreads / 32) {
       const int n = su.n[b], L = su.L[b], items = (n + 2 * sub - 1) / (2 * sub);
       int64_t u = 0;
       int lo;
-      for (int j = lane; j < items; j += 32) u += item_units(n, L, j, sub, a.window, &lo);
+      for (int j = lane; j < items; j += 32)
+        u += item_units(n, L, j, sub, a.window, &lo) + kItemCost;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
       if (lane == 0) su.before[b + 1] = u * a.Hkv;
@@ -317,7 +362,7 @@ prefill_kernel(const __grid_constant__ Args ka) {
         int units = 0;
         for (int j0 = 0; j0 < items; j0 += 32) {
           int lo;
-          const int u = j0 + lane < items ? item_units(n, L, j0 + lane, sub, a.window, &lo) : 0;
+          const int u = j0 + lane < items ? item_units(n, L, j0 + lane, sub, a.window, &lo) + kItemCost : 0;
           int64_t inc = u;
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
@@ -335,9 +380,9 @@ prefill_kernel(const __grid_constant__ Args ka) {
           rest -= __shfl_sync(0xffffffffu, inc, 31);
         }
         // a cut near an item's border moves there
-        const int left = units - off;
-        if (off > 0 && k < NW && (off < kSnap || left <= kSnap)) {
-          if (off <= left) {
+        const int tile = off - kItemCost, left = units - off;
+        if (tile < kSnap || left <= kSnap) {
+          if (tile <= left) {
             x -= off;
             off = 0;
           } else {
@@ -353,6 +398,8 @@ prefill_kernel(const __grid_constant__ Args ka) {
               }
             }
           }
+        } else {
+          off = tile;
         }
       }
       if (lane == 0) {
@@ -377,11 +424,13 @@ prefill_kernel(const __grid_constant__ Args ka) {
   const uint32_t tmem_o = tmem + 2 * kTile;
   auto slot_at = [&](int i) { return ring + (i % C::kSlots) * C::kSlot; };   // i: K 2g, V 2g + 1
 
+  if (warp >= 8) {
+  regs_down<kOtherRegs>();
   if (warp == kCopyWarp) {
     // ================================================================ copies
-    const int64_t lo = sm.lo, hi = sm.hi;
-    int64_t pos = lo;
+    const int64_t hi = sm.hi;
     int b = sm.b, h = sm.h, j = sm.j, off = sm.off;
+    int64_t pos = sm.lo - (off > 0 ? off + kItemCost : 0);   // the item's first unit
     int d = 0, g = 0, q_fills[2] = {0, 0}, raws = 0;
     int n = 0, L = 0, t0 = 0, loaded = -1;
     int head[6] = {0, 0, 0, 0, 0, 0};
@@ -418,6 +467,24 @@ prefill_kernel(const __grid_constant__ Args ka) {
       }
       return true;
     };
+    // a piece's query rows
+    auto copy_queries = [&](const Desc& x) {
+      for (int w = 0; w < 2; ++w) {
+        const int2 r = sub_tiles(x, w, sub, a.window);
+        if (r.x == r.y) continue;
+        if (q_fills[w] > 0 && !wait_warp(kQEmpty + w, q_fills[w] - 1)) return false;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar(kQFull + w), static_cast<uint32_t>(C::kHalves * 128 * sub * G));
+#pragma unroll
+          for (int y = 0; y < C::kHalves; ++y)
+            box_g2s(q_at + w * C::kSlot + y * C::kSub, &ka.tm_q, 64 * y, x.h * G, x.t0 + w * sub,
+                    bar(kQFull + w));
+        }
+        ++q_fills[w];
+        __syncwarp();
+      }
+      return true;
+    };
     while (ok && pos < hi) {
       if (b != loaded) {                   // (bad starts and lengths were reported above)
         const int s0 = a.starts[b], s1 = a.starts[b + 1];
@@ -434,7 +501,8 @@ prefill_kernel(const __grid_constant__ Args ka) {
       }
       int k0;
       const int u = item_units(n, L, j, sub, a.window, &k0);
-      const int take = static_cast<int>(min(static_cast<int64_t>(u - off), hi - pos));
+      const int64_t room = hi - pos - kItemCost;   // tiles of it before the share's end
+      const int take = (room < u ? static_cast<int>(room) : u) - off;
       Desc x;
       x.h = h;
       x.b = b;
@@ -467,21 +535,6 @@ prefill_kernel(const __grid_constant__ Args ka) {
       }
       ++d;
       __syncwarp();
-      // ---- its query rows
-      for (int w = 0; w < 2 && ok; ++w) {
-        const int2 r = sub_tiles(x, w, sub, a.window);
-        if (r.x == r.y) continue;
-        if (q_fills[w] > 0 && !wait_warp(kQEmpty + w, q_fills[w] - 1)) ok = false;
-        if (ok && lane == 0) {
-          mbar_arrive_expect_tx(bar(kQFull + w), static_cast<uint32_t>(C::kHalves * 128 * sub * G));
-#pragma unroll
-          for (int y = 0; y < C::kHalves; ++y)
-            box_g2s(q_at + w * C::kSlot + y * C::kSub, &ka.tm_q, 64 * y, h * G, x.t0 + w * sub,
-                    bar(kQFull + w));
-        }
-        ++q_fills[w];
-        __syncwarp();
-      }
       // ---- its tiles: four tiles' page ids at a time, one tile ahead of the copies
       const int32_t* table = a.block_tables + static_cast<int64_t>(b) * a.mbs;
       const int last_page = (L + 15) / 16 - 1;
@@ -505,10 +558,10 @@ prefill_kernel(const __grid_constant__ Args ka) {
           mt.vs[lane] = valid ? a.v_scale[page] : 0.f;
         }
         __syncwarp();
-        ok = copy_tile(0, id, valid, h) && copy_tile(1, id, valid, h);
+        ok = copy_tile(0, id, valid, h) && (t > x.k_lo || copy_queries(x)) && copy_tile(1, id, valid, h);
       }
       // ---- the next item
-      pos += take;
+      pos += u + kItemCost;
       off = 0;
       if (++j == items) {
         j = 0;
@@ -546,123 +599,112 @@ prefill_kernel(const __grid_constant__ Args ka) {
       }
     }
     __syncwarp();
-  } else if (warp == kMmaWarp) {
+  } else if (warp < kConvWarp) {
     // ================================================================ products
-    if (lane == 0) {
-      constexpr uint32_t kIdQK = umma_idesc_f16<kMmaBf16>(kTile, kTile, false);
-      constexpr uint32_t kIdPV = umma_idesc_f16<kMmaBf16>(kTile, D, false) | kBMajorN;
-      struct Cursor {
-        int d = 0, t = 0, e = 0, k_lo = 0, g0 = 0, g_end = 0, q = 0, p = 0;
-        bool open = false, end = false, pv = false, first = true;
-      } cur[2];
-      int k_pos[2] = {0, 0}, v_pos[2] = {0, 0}, k_rel = 0, v_rel = 0;   // tiles passed, slots released
-      bool issued = false;
-      uint64_t idle_since = 0;
-      auto ready = [&](int b, int n) { return test_wait(bar(b), n & 1); };
-      auto full = [&](int i) { return ready(kFull + i % C::kSlots, i / C::kSlots); };
-      while (!(cur[0].end && cur[1].end)) {
-        bool did = false;
+    // One warp a subtile: Q.K of a tile, then, once its weights are there, P.V.
+    constexpr uint32_t kIdQK = umma_idesc_f16<kMmaBf16>(kTile, kTile, false);
+    constexpr uint32_t kIdPV = umma_idesc_f16<kMmaBf16>(kTile, D, false) | kBMajorN;
+    const int w = warp - kMmaWarp;
+    const uint32_t ts = tmem + w * kTile, to = tmem_o + w * D;
+    const uint64_t dq = umma_desc_sw128(q_at + w * C::kSlot, 16, 1024);
+    const uint64_t dk0 = umma_desc_sw128(ring, 16, 1024);
+    const uint64_t dv0 = umma_desc_sw128(ring, C::kSub, 1024);
+    int p_n = 0, q_n = 0;
+    // the next K's and V's place in the ring (K 0, V 1, K 2, ..) and their fills' parity
+    int ks = 0, kp = 0, vs = 1, vp = 0;
+    auto step2 = [&](int& slot, int& parity) {
+      slot += 2;
+      if (slot >= C::kSlots) {
+        slot -= C::kSlots;
+        parity ^= 1;
+      }
+    };
+    auto full = [&](int slot, int parity) { return wait_warp(kFull + slot, parity); };
+    bool issued = false, ok = true;
+    auto scores = [&](bool last) {         // Q.K of the next tile, whose K has landed
+      if (elect_one()) {
+        mbar_arrive(bar(kSFull + w));      // (orders the tile's meta before the softmax's reads)
+        const uint64_t dk = dk0 + static_cast<uint64_t>(ks * (C::kSlot >> 4));
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          Cursor& c = cur[w];
-          if (c.end) continue;
-          if (!c.open) {
-            if (!ready(kDFull + c.d % kDescs, c.d / kDescs)) continue;
-            const Desc& x = sm.desc[c.d % kDescs];
-            did = true;
-            if (x.h < 0) {
-              c.end = true;
-              k_pos[w] = v_pos[w] = INT_MAX;
-              continue;
-            }
-            const int2 r = sub_tiles(x, w, sub, a.window);
-            c.open = true;
-            c.first = true;
-            c.pv = false;
-            c.k_lo = x.k_lo;
-            c.g0 = x.g0;
-            c.g_end = x.g0 + x.k_hi - x.k_lo;
-            c.t = r.x;
-            c.e = r.y;
-            if (r.x < r.y) k_pos[w] = v_pos[w] = c.g0 + c.t - c.k_lo;
-          }
-          const uint32_t ts = tmem + w * kTile, to = tmem_o + w * D;
-          if (c.pv) {
-            const int i = 2 * (c.g0 + c.t - c.k_lo) + 1;
-            if (ready(kPFull + w, c.p) && full(i)) {
-              tc_fence_after();
-              if (!*reinterpret_cast<volatile int*>(&sm.skip[w])) {
-                const uint64_t dv = umma_desc_sw128(slot_at(i), C::kSub, 1024);
-#pragma unroll
-                for (int k = 0; k < kTile / 16; ++k)
-                  umma_f16_ts(to, ts + 8 * k, dv + static_cast<uint64_t>(k * (2048 >> 4)), kIdPV,
-                              !(c.first && k == 0));
-              }
-              issued = true;
-              c.first = false;
-              c.pv = false;
-              ++c.p;
-              v_pos[w] = c.g0 + c.t - c.k_lo + 1;
-              if (++c.t == c.e) umma_commit(bar(kODone + w));
-              did = true;
-            }
-          }
-          if (!c.pv && c.t < c.e) {
-            const int i = 2 * (c.g0 + c.t - c.k_lo);
-            if ((!c.first || ready((FP8 && BF16 ? kQConv : kQFull) + w, c.q)) && full(i)) {
-              mbar_arrive(bar(kSFull + w));   // (orders the tile's meta before the softmax's reads)
-              tc_fence_after();
-              const uint64_t dq = umma_desc_sw128(q_at + w * C::kSlot, 16, 1024);
-              const uint64_t dk = umma_desc_sw128(slot_at(i), 16, 1024);
-#pragma unroll
-              for (int k = 0; k < D / 16; ++k) {
-                const uint64_t o = static_cast<uint64_t>(((k >> 2) * C::kSub + (k & 3) * 32) >> 4);
-                umma_f16(ts, dq + o, dk + o, kIdQK, k > 0);
-              }
-              umma_commit(bar(kSFull + w));
-              issued = true;
-              if (c.t + 1 == c.e) {
-                umma_commit(bar(kQEmpty + w));
-                ++c.q;
-              }
-              k_pos[w] = c.g0 + c.t - c.k_lo + 1;
-              c.pv = true;
-              did = true;
-            }
-          }
-          if (!c.pv && c.t == c.e) {       // the piece is through for this subtile
-            k_pos[w] = v_pos[w] = c.g_end;
-            c.open = false;
-            mbar_arrive(bar(kDEmpty + c.d % kDescs));
-            ++c.d;
-            did = true;
-          }
+        for (int k = 0; k < D / 16; ++k) {
+          const uint64_t o = static_cast<uint64_t>(((k >> 2) * C::kSub + (k & 3) * 32) >> 4);
+          umma_f16(ts, dq + o, dk + o, kIdQK, k > 0);
         }
-        // slots that both subtiles have passed
-        const int k_min = min(min(k_pos[0], k_pos[1]), max(k_pos[0] == INT_MAX ? 0 : k_pos[0], k_pos[1] == INT_MAX ? 0 : k_pos[1]));
-        const int v_min = min(min(v_pos[0], v_pos[1]), max(v_pos[0] == INT_MAX ? 0 : v_pos[0], v_pos[1] == INT_MAX ? 0 : v_pos[1]));
-        for (; k_rel < k_min; ++k_rel) umma_commit(bar(kEmpty + (2 * k_rel) % C::kSlots));
-        for (; v_rel < v_min; ++v_rel) umma_commit(bar(kEmpty + (2 * v_rel + 1) % C::kSlots));
-        if (did) {
-          idle_since = 0;
-          continue;
+        umma_commit(bar(kSFull + w));
+        umma_commit(bar(kEmpty + ks));
+        if (last) umma_commit(bar(kQEmpty + w));
+      }
+      __syncwarp();
+      issued = true;
+      step2(ks, kp);
+    };
+    auto pass = [&](int tiles) {           // tiles that the other subtile alone sees
+      for (int i = 0; i < tiles && ok; ++i) {
+        ok = full(ks, kp) && full(vs, vp);
+        if (ok && lane == 0) {
+          mbar_arrive(bar(kEmpty + ks));
+          mbar_arrive(bar(kEmpty + vs));
         }
-        if (*dead) break;
-        const uint64_t now = global_ns();
-        if (idle_since == 0) {
-          idle_since = now;
-        } else if (now - idle_since > ka.wait_limit_ns) {
-          *dead = 1;
-          atomicOr(a.status, kStatusTimeout);
-          break;
+        step2(ks, kp);
+        step2(vs, vp);
+      }
+    };
+    for (int d = 0; ok; ++d) {
+      if (!wait_warp(kDFull + d % kDescs, d / kDescs)) break;
+      const Desc& x = sm.desc[d % kDescs];
+      if (x.h < 0) break;
+      const int2 r = sub_tiles(x, w, sub, a.window);
+      const bool some = r.x < r.y;
+      const int behind = some ? x.k_hi - r.y : 0;
+      pass(some ? r.x - x.k_lo : x.k_hi - x.k_lo);
+      if (ok && some) {
+        ok = full(ks, kp) && wait_warp((FP8 && BF16 ? kQConv : kQFull) + w, q_n++);
+        if (ok) {
+          tc_fence_after();
+          scores(r.x + 1 == r.y);
         }
       }
-      if (issued) {                        // no product outlives the CTA
-        umma_commit(bar(kFin));
-        const uint64_t since = global_ns();
-        const uint64_t limit = ka.wait_limit_ns > kWaitLimitNs ? ka.wait_limit_ns : kWaitLimitNs;
-        while (!mbar_try_wait(bar(kFin), 0) && global_ns() - since < limit) {
+      for (int t = r.x; ok && t < r.y; ++t, ++p_n) {
+        const bool more = t + 1 < r.y;
+        ok = full(vs, vp) && (!more || full(ks, kp)) && wait_warp(kPFull + w, p_n);
+        if (!ok) break;
+        tc_fence_after();
+        const bool skip = *reinterpret_cast<volatile int*>(&sm.skip[w]) != 0;
+        const uint64_t dv = dv0 + static_cast<uint64_t>(vs * (C::kSlot >> 4));
+        if (!skip && elect_one()) {
+#pragma unroll
+          for (int k = 0; k < kTile / 32; ++k)
+            umma_f16_ts(to, ts + 8 * k, dv + static_cast<uint64_t>(k * (2048 >> 4)), kIdPV,
+                        t > r.x || k > 0);
         }
+        __syncwarp();
+        ok = wait_warp(kPHalf + w, p_n);   // the weights of the second half of the tile
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          if (!skip) {
+#pragma unroll
+            for (int k = kTile / 32; k < kTile / 16; ++k)
+              umma_f16_ts(to, ts + 8 * k, dv + static_cast<uint64_t>(k * (2048 >> 4)), kIdPV, true);
+          }
+          umma_commit(bar(kEmpty + vs));
+          if (!more) umma_commit(bar(kODone + w));
+        }
+        __syncwarp();
+        step2(vs, vp);
+        if (more) scores(t + 2 == r.y);
+      }
+      pass(behind);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kDEmpty + d % kDescs));
+    }
+    // no product outlives the CTA
+    if (issued) {
+      if (elect_one()) umma_commit(bar(kFin + w));
+      __syncwarp();
+      const uint64_t since = global_ns();
+      const uint64_t limit = ka.wait_limit_ns > kWaitLimitNs ? ka.wait_limit_ns : kWaitLimitNs;
+      while (!mbar_try_wait(bar(kFin + w), 0) && global_ns() - since < limit) {
       }
     }
     __syncwarp();
@@ -714,8 +756,10 @@ prefill_kernel(const __grid_constant__ Args ka) {
         mbar_arrive(bar(kRawEmpty + f % 2));
       }
     }
-  } else if (warp < 8) {
+  }
+  } else {
     // ================================================================ softmax
+    regs_up<kSoftmaxRegs>();
     const int w = warp >> 2, wq = warp & 3, r = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t ts = tmem + lanes + w * kTile, to = tmem_o + lanes + w * D;
@@ -778,36 +822,53 @@ prefill_kernel(const __grid_constant__ Args ka) {
         const int p0 = t * kTile;
         const bool edge = valid != 0xffu || p0 + kTile - 1 > first ||
                           (a.window > 0 && p0 < last - a.window + 1);
-        // columns [jl, jh) of the tile are this row's
-        const int jh = pos + 1 - p0, jl = a.window > 0 ? pos - a.window + 1 - p0 : 0;
-        auto sees = [&](int j) { return j >= jl && j < jh && ((valid >> (j >> 4)) & 1u); };
-        auto scores = [&](int c, float (&v)[32]) {   // columns 32c .. 32c + 31
-          tmem_ld<32>(ts + 32 * c, v);
-          tmem_wait_ld();
+        // columns [jl, jh) of the tile are this row's, those of valid pages
+        const int jh = pos + 1 - p0, jl = a.window > 0 ? max(pos - a.window + 1 - p0, 0) : 0;
+        auto below = [](int j) { return j <= 0 ? 0u : j >= 32 ? ~0u : (1u << j) - 1u; };
+        auto word = [&](int c) {           // of columns 32c .. 32c + 31
+          const unsigned pages = ((valid >> (2 * c)) & 1u ? 0xffffu : 0u) |
+                                 ((valid >> (2 * c + 1)) & 1u ? 0xffff0000u : 0u);
+          return below(jh - 32 * c) & ~below(jl - 32 * c) & pages;
+        };
+        // ---- the row's scores, and their maximum
+        float v[kTile];
+        auto load = [&](int c) { tmem_ld<32>(ts + 32 * c, *reinterpret_cast<float (*)[32]>(v + 32 * c)); };
+        auto masked = [&](int c) {
           if (ka.negative) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = -v[j];
+            for (int j = 0; j < 32; ++j) v[32 * c + j] = -v[32 * c + j];
           }
           if (edge) {
+            const unsigned bits = word(c);
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (!sees(32 * c + j)) v[j] = -INFINITY;
+              if (!(bits & (1u << j))) v[32 * c + j] = -INFINITY;
           }
         };
-        // ---- the row's maximum
+        load(0);
+        load(1);
+        tmem_wait_ld();
+        load(2);
+        load(3);
+        masked(0);
+        masked(1);
         float m = -INFINITY, v_big = 0.f;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float v[32];
-          scores(c, v);
+        auto take_max = [&](int c) {       // of columns 64c .. 64c + 63
           if constexpr (FP8) {
-            m = fmaxf(m, max_of<16>(v, 0, -INFINITY) * fmaxf(mt.ks[2 * c], 1e-37f));
-            m = fmaxf(m, max_of<16>(v, 16, -INFINITY) * fmaxf(mt.ks[2 * c + 1], 1e-37f));
-            v_big = fmaxf(v_big, fmaxf(mt.vs[2 * c], mt.vs[2 * c + 1]));
+#pragma unroll
+            for (int k = 4 * c; k < 4 * c + 4; ++k) {
+              m = fmaxf(m, max_of<16>(v + 16 * k) * fmaxf(mt.ks[k], 1e-37f));
+              v_big = fmaxf(v_big, mt.vs[k]);
+            }
           } else {
-            m = max_of<32>(v, 0, m);
+            m = fmaxf(m, max_of<64>(v + 64 * c));
           }
-        }
+        };
+        take_max(0);
+        tmem_wait_ld();
+        masked(2);
+        masked(3);
+        take_max(1);
         m *= sl2;
         // ---- a new offset (and reference of V's scales) where the standing one does not do
         const bool start = t == tiles.x;
@@ -830,14 +891,14 @@ prefill_kernel(const __grid_constant__ Args ka) {
             l *= fl;
           }
           if (!start) {                    // O, whose last product is done (S came after it)
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              float o[32];
-              tmem_ld<32>(to + 32 * c, o);
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+              float o[16];
+              tmem_ld<16>(to + 16 * c, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] *= f;
-              tmem_st<32>(to + 32 * c, o);
+              for (int j = 0; j < 16; ++j) o[j] *= f;
+              tmem_st<16>(to + 16 * c, o);
             }
             tmem_wait_st();
           }
@@ -845,11 +906,10 @@ prefill_kernel(const __grid_constant__ Args ka) {
         // ---- the weights, in S's place
         const float sub_off = (off == -INFINITY ? 0.f : off) - kLift;
         const float inv_ref = FP8 ? 1.f / ref : 1.f;
-        float l0 = 0.f, l1 = 0.f;
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          float v[32], p[16];
-          scores(c, v);
+          float p[16];
 #pragma unroll
           for (int j = 0; j < 32; j += 2) {
             float k = sl2, u = 1.f;
@@ -857,19 +917,25 @@ prefill_kernel(const __grid_constant__ Args ka) {
               k = fmaxf(sl2 * mt.ks[2 * c + j / 16], 1e-37f);
               u = mt.vs[2 * c + j / 16] * inv_ref;
             }
-            float e0 = fast_exp2(fmaf(v[j], k, -sub_off));
-            float e1 = fast_exp2(fmaf(v[j + 1], k, -sub_off));
-            l0 += e0;
-            l1 += e1;
-            if constexpr (FP8) {
-              e0 *= u;
-              e1 *= u;
-            }
-            p[j / 2] = __uint_as_float(pack2<kMmaBf16>(e0, e1));
+            float2 e = fma2(make_float2(v[32 * c + j], v[32 * c + j + 1]), make_float2(k, k),
+                            make_float2(-sub_off, -sub_off));
+            e.x = fast_exp2(e.x);
+            e.y = fast_exp2(e.y);
+            sum[(j / 2) & 1] = add2(sum[(j / 2) & 1], e);
+            if constexpr (FP8) e = mul2(e, make_float2(u, u));
+            p[j / 2] = __uint_as_float(pack2<kMmaBf16>(e.x, e.y));
           }
           tmem_st<16>(ts + 16 * c, p);
+          if (c == 1 && !edge) {           // the product of the first half may begin
+            if (wq == 0 && lane == 0) sm.skip[w] = 0;
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kPFull + w));
+          }
         }
-        l += l0 + l1;
+        const float2 sums = add2(sum[0], sum[1]);
+        l += sums.x + sums.y;
         tmem_wait_st();
         if (edge) {
           // token r of the tile: no data, a row of zeros; else is every value finite?
@@ -906,6 +972,7 @@ prefill_kernel(const __grid_constant__ Args ka) {
           const bool self = fl[0] | fl[1] | fl[2] | fl[3];
           if (self) {
             // this tile's product by the rows' own threads, over the tokens that they see
+#pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 8) {
               float o[8];
               if (start) {
@@ -915,7 +982,9 @@ prefill_kernel(const __grid_constant__ Args ka) {
                 tmem_ld<8>(to + c0, o);
               }
               const uint32_t col = slot_at(i) + (c0 / 64) * C::kSub;
+#pragma unroll 1
               for (int j0 = 0; j0 < kTile; j0 += 8) {
+                const unsigned seen = word(j0 / 32) >> (j0 & 31);
                 float p[4];
                 tmem_ld<4>(ts + j0 / 2, p);
                 tmem_wait_ld();
@@ -927,7 +996,7 @@ prefill_kernel(const __grid_constant__ Args ka) {
                   const float pf = kMmaBf16 ? __uint_as_float(one << 16)
                                             : __half2float(__ushort_as_half(static_cast<unsigned short>(one)));
                   const uint4 v = lds128(col + at * 128 + ((((c0 % 64) / 8) ^ (at & 7)) << 4));
-                  if (!sees(at)) continue;
+                  if (!((seen >> j) & 1u)) continue;
                   const uint32_t us[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                   for (int k = 0; k < 4; ++k) {
@@ -947,12 +1016,13 @@ prefill_kernel(const __grid_constant__ Args ka) {
             tmem_wait_st();
           }
           if (wq == 0 && lane == 0) sm.skip[w] = self;
-        } else if (wq == 0 && lane == 0) {
-          sm.skip[w] = 0;
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kPFull + w));
+        if (lane == 0) {
+          if (edge) mbar_arrive(bar(kPFull + w));
+          mbar_arrive(bar(kPHalf + w));
+        }
       }
       if (!ok) break;
       // ---- the piece's result
@@ -1156,7 +1226,7 @@ cudaError_t launch(const PrefillArgs& args, cudaStream_t s) {
     k.a.block_tables = args.block_tables + static_cast<int64_t>(b0) * args.mbs;
     k.a.context_lens = args.context_lens + b0;
     k.a.starts = args.starts + b0;
-    kern<<<grid, C::kThreads, smem, s>>>(k);
+    kern<<<grid, kThreads, smem, s>>>(k);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (!cuts) continue;
     merge_kernel<D, BF16><<<dim3(static_cast<unsigned>(grid), 256 / kMergeRows), 256, 0, s>>>(k, grid);
