@@ -62,11 +62,7 @@ constexpr int kItemCost = 4;
 constexpr int kMaxSeqs = 512;              // sequences a launch sorts
 constexpr int kDescs = 4;                  // pieces known ahead
 constexpr int kMetas = 8;                  // tiles whose pages' validity and scales are kept
-constexpr int kCopyWarp = 8, kMmaWarp = 9, kConvWarp = 11, kConvWarps = 1;
-constexpr int kThreads = 384;
-// Three warpgroups of 168 registers a thread (65536 / 384), re-divided: 216 for a row's
-// 128 scores and their weights, 72 for the rest; 2 x 216 + 72 = 3 x 168.
-constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
+constexpr int kCopyWarp = 8, kMmaWarp = 9, kConvWarp = 11;
 constexpr int kHeader = 16;                // ints a CTA's header in the workspace
 
 struct Args {
@@ -93,6 +89,12 @@ struct Cfg {
   static constexpr int kRaws = FP8 ? 2 : 0;
   // Q of both subtiles, the ring, the codes: 224 KB at head_dim 128, 160 KB at 64
   static constexpr int kSlots = FP8 ? (D == 128 ? 4 : 6) : (D == 128 ? 5 : 8);
+  // Three warpgroups of 168 registers a thread (65536 / 384), re-divided: 216 for a row's
+  // 128 scores and their weights, 72 for the rest; 2 x 216 + 72 = 3 x 168.  With a fourth,
+  // of converting warps: 128 at first, then 2 x 200 + 2 x 56 = 4 x 128.
+  static constexpr int kThreads = FP8 ? 512 : 384;
+  static constexpr int kSoftmaxRegs = FP8 ? 200 : 216, kOtherRegs = FP8 ? 56 : 72;
+  static constexpr int kConvWarps = FP8 ? 5 : 1;
   static constexpr int kQ = 2 * kSlot;
   static constexpr int kBig = kQ + kSlots * kSlot + kRaws * kRaw;
 };
@@ -263,7 +265,7 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
 }
 
 template <int D, bool BF16, bool FP8>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
 prefill_kernel(const __grid_constant__ Args ka) {
   using C = Cfg<D, FP8>;
   constexpr bool kMmaBf16 = BF16 && !FP8;  // the products' operand type
@@ -289,7 +291,7 @@ prefill_kernel(const __grid_constant__ Args ka) {
   // ---- 1. the items' lengths, and this CTA's share of them
   {
     Setup& su = *reinterpret_cast<Setup*>(smem);
-    for (int b = tid; b < a.B; b += kThreads) {
+    for (int b = tid; b < a.B; b += C::kThreads) {
       const int s0 = a.starts[b], s1 = a.starts[b + 1], L = a.context_lens[b];
       const bool good = s0 >= 0 && s1 >= s0 && s1 <= a.T, fits = L >= 0 && L <= a.max_context_len;
       if (cta == 0 && (!good || (!fits && s1 > s0))) atomicOr(a.status, kStatusBadLen);
@@ -302,9 +304,9 @@ prefill_kernel(const __grid_constant__ Args ka) {
       su.before[0] = 0;
       for (int i = 0; i < kBars; ++i) {
         int n = 1;
-        if (FP8 && i >= kFull && i < kFull + 8) n = kConvWarps;
+        if (FP8 && i >= kFull && i < kFull + 8) n = C::kConvWarps;
         if (i >= kEmpty && i < kEmpty + 8) n = 2;
-        if (i == kRawEmpty || i == kRawEmpty + 1) n = kConvWarps;
+        if (i == kRawEmpty || i == kRawEmpty + 1) n = C::kConvWarps;
         if (i >= kQConv && i < kQConv + 2) n = 4;
         if (i >= kSFull && i < kSFull + 2) n = 2;
         if (i >= kPFull && i < kPHalf + 2) n = 4;
@@ -315,7 +317,7 @@ prefill_kernel(const __grid_constant__ Args ka) {
       mbar_init_fence();
     }
     __syncthreads();
-    for (int b = warp; b < a.B; b += kThreads / 32) {
+    for (int b = warp; b < a.B; b += C::kThreads / 32) {
       const int n = su.n[b], L = su.L[b], items = (n + 2 * sub - 1) / (2 * sub);
       int64_t u = 0;
       int lo;
@@ -425,7 +427,7 @@ prefill_kernel(const __grid_constant__ Args ka) {
   auto slot_at = [&](int i) { return ring + (i % C::kSlots) * C::kSlot; };   // i: K 2g, V 2g + 1
 
   if (warp >= 8) {
-  regs_down<kOtherRegs>();
+  regs_down<C::kOtherRegs>();
   if (warp == kCopyWarp) {
     // ================================================================ copies
     const int64_t hi = sm.hi;
@@ -731,7 +733,7 @@ prefill_kernel(const __grid_constant__ Args ka) {
       const uint32_t src = raw + (f % 2) * C::kRaw, dst = slot_at(f);
       constexpr int kChunks = D / 16;      // 16 codes each, of a row
 #pragma unroll 4
-      for (int i = ct; i < kTile * kChunks; i += kConvWarps * 32) {
+      for (int i = ct; i < kTile * kChunks; i += C::kConvWarps * 32) {
         const uint4 codes = lds128(src + 16 * i);
         const int row = i / kChunks, c = i % kChunks, half = c / 4, p = (c % 4) * 2;
         uint4 lo, hi;
@@ -759,7 +761,7 @@ prefill_kernel(const __grid_constant__ Args ka) {
   }
   } else {
     // ================================================================ softmax
-    regs_up<kSoftmaxRegs>();
+    regs_up<C::kSoftmaxRegs>();
     const int w = warp >> 2, wq = warp & 3, r = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t ts = tmem + lanes + w * kTile, to = tmem_o + lanes + w * D;
@@ -1226,7 +1228,7 @@ cudaError_t launch(const PrefillArgs& args, cudaStream_t s) {
     k.a.block_tables = args.block_tables + static_cast<int64_t>(b0) * args.mbs;
     k.a.context_lens = args.context_lens + b0;
     k.a.starts = args.starts + b0;
-    kern<<<grid, kThreads, smem, s>>>(k);
+    kern<<<grid, C::kThreads, smem, s>>>(k);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (!cuts) continue;
     merge_kernel<D, BF16><<<dim3(static_cast<unsigned>(grid), 256 / kMergeRows), 256, 0, s>>>(k, grid);
