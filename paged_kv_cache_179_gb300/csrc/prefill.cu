@@ -13,16 +13,17 @@
 // Roles of a CTA, one an SM:
 //   warps 0-3, 4-7   the softmax of one subtile each, a thread a row, whose 128 scores it
 //                    holds in registers; P goes back to tensor memory as 16-bit pairs;
-//   warp 8           walks the CTA's pieces, copies Q, K and V (TMA);
+//   warp 8           walks the CTA's pieces, copies Q and K (TMA), of E4M3 pools V too;
 //   warp 9           one thread issues the products, each as soon as its operands are
 //                    there.  A subtile's Q.K of the next tile follows its P.V in the
 //                    same queue, so S needs no second buffer: the tensor cores work on
 //                    one subtile while the other's softmax runs;
 //   warps 10-13      E4M3 pools: codes to f16 (exact) between two shared-memory rings.
 //
-// The softmax offset of a row moves only when a score exceeds it by more than kSlack
-// (log2 units): any standing offset gives the same softmax, weights stay below
-// 2^kSlack, and O is scaled in tensor memory a few times a row instead of every tile.
+// The softmax offset of a row is the maximum of an early tile's scores and moves only
+// when weights grow out of the products' range (kMaxSum): any standing offset gives the
+// same softmax.  So most tiles need no maximum: their weights are made at once, their
+// sum shows whether they may stand, and O is scaled in tensor memory hardly ever.
 // Page scales: K's multiply the scores of their 16 columns, V's the weights (relative
 // to a power of two that follows the largest seen, so that P stays in f16's range).
 //
@@ -55,6 +56,9 @@ namespace {
 constexpr int kTile = 128;                 // tokens of a tile, rows of a subtile
 constexpr int kPages = kTile / 16;
 constexpr float kSlack = 8.f;              // log2 units
+// Weights (and with a page scale up to twice the reference their products) are in f16's
+// range while 64 of them add up to no more than this.
+constexpr float kMaxSum = 32000.f;
 constexpr int kSnap = 4;                   // tiles
 // What an item costs besides its tiles (its queries, a pipeline that fills and drains, edges,
 // the result), in tiles: what it adds to the shares.
@@ -71,8 +75,7 @@ struct Args {
   float* ws_acc;                           // [grid][2 parts][256 rows][D]
   float2* ws_ml;                           // [grid][2][256]: offset (log2 units), sum
   int* ws_head;                            // [grid][kHeader]
-  float sl2;                               // |scale| log2(e), above 0
-  int negative;                            // scale < 0
+  float sl2;                               // scale log2(e), not 0
   int sub;                                 // tokens of a subtile
   uint64_t wait_limit_ns;
 };
@@ -121,7 +124,8 @@ enum : int {                               // mbarriers
   kSFull = kQConv + 2,
   kPFull = kSFull + 2,
   kPHalf = kPFull + 2,                     // the second half of P
-  kODone = kPHalf + 2,
+  kPVHalf = kPHalf + 2,                    // the product of a first half is done
+  kODone = kPVHalf + 2,
   kVote = kODone + 2,
   kDFull = kVote + 2,
   kDEmpty = kDFull + kDescs,
@@ -134,6 +138,7 @@ struct Small {                             // shared memory behind the operands
   Desc desc[kDescs];
   Meta meta[kMetas];
   int tmem, dead, raw_end;
+  int passed[2];                           // tiles that a subtile's products are issued for
   int skip[2];                             // the subtile's threads made this product themselves
   int flag[2][4];                          // by warp: a value of V is not finite
   int64_t lo, hi;                          // the CTA's share
@@ -159,6 +164,11 @@ __device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, vola
     }
   }
 }
+
+// A value that all lanes hold, known to be one: what is computed from it, and loops that it
+// bounds, need no vector registers (a product's descriptors are uniform registers, and
+// bringing each there costs more than issuing the product).
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
@@ -194,6 +204,41 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, ui
       : "memory");
 }
 constexpr uint32_t kBMajorN = 1u << 16;    // B MN-major (V: tokens along K, its rows along N)
+
+// The pages `valid` of a tile (page j's id in lane j) into its slot, page j at rows 16j ..:
+// one lane issues them all from uniform registers.
+template <int HALVES, int SUB>
+__device__ __forceinline__ void copy_pages(const void* tmap, int Hkv, int h, int id, unsigned valid,
+                                           uint32_t slot, uint32_t full) {
+  int page[kPages];
+#pragma unroll
+  for (int j = 0; j < kPages; ++j) page[j] = __shfl_sync(0xffffffffu, id, j) * Hkv + h;
+  if (elect_one()) {
+    mbar_arrive_expect_tx(full, static_cast<uint32_t>(__popc(valid)) * (HALVES * 2048u));
+#pragma unroll
+    for (int j = 0; j < kPages; ++j)
+      if ((valid >> j) & 1u)
+#pragma unroll
+        for (int x = 0; x < HALVES; ++x) box_g2s(slot + x * SUB + j * 2048, tmap, 64 * x, 0, page[j], full);
+  }
+  __syncwarp();
+}
+// The same for pages of codes, dense, page j at byte 16 D j.
+template <int D>
+__device__ __forceinline__ void copy_codes(const uint8_t* pool, int Hkv, int h, int id, unsigned valid,
+                                           uint32_t to, uint32_t full) {
+  int64_t page[kPages];
+#pragma unroll
+  for (int j = 0; j < kPages; ++j)
+    page[j] = static_cast<int64_t>(__shfl_sync(0xffffffffu, id, j)) * Hkv + h;
+  if (elect_one()) {
+    mbar_arrive_expect_tx(full, static_cast<uint32_t>(__popc(valid)) * (16u * D));
+#pragma unroll
+    for (int j = 0; j < kPages; ++j)
+      if ((valid >> j) & 1u) page_g2s(to + j * 16 * D, pool + page[j] * (16 * D), 16 * D, full);
+  }
+  __syncwarp();
+}
 
 // Units of item j (its tiles; 1 when it sees none, for its zeros) of a sequence with n
 // query tokens and L cached ones; *lo: the first tile.
@@ -270,7 +315,7 @@ prefill_kernel(const __grid_constant__ Args ka) {
   using C = Cfg<D, FP8>;
   constexpr bool kMmaBf16 = BF16 && !FP8;  // the products' operand type
   // weights of f16 products are kept 2^6 larger, so that small ones stay in its normal
-  // range (2^(6 + kSlack) times a page scale up to twice the reference: below 2^16)
+  // range (at an edge 2^(6 + kSlack) times a page scale up to twice the reference: below 2^16)
   constexpr float kLift = kMmaBf16 ? 0.f : 6.f;
   const PrefillArgs& a = ka.a;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -281,7 +326,8 @@ prefill_kernel(const __grid_constant__ Args ka) {
   const uint32_t bars = smem_u32(sm.bar);
   auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
   volatile int* dead = &sm.dead;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = uniform(tid >> 5);
   const int G = a.group, sub = ka.sub, cta = blockIdx.x;
   auto wait = [&](int b, int n) {          // the n-th completion (from 0) of barrier b
     return bounded_wait(bar(b), n & 1, dead, ka.wait_limit_ns, a.status);
@@ -301,6 +347,7 @@ prefill_kernel(const __grid_constant__ Args ka) {
     if (tid == 0) {
       sm.dead = 0;
       sm.raw_end = INT_MAX;
+      sm.passed[0] = sm.passed[1] = 0;
       su.before[0] = 0;
       for (int i = 0; i < kBars; ++i) {
         int n = 1;
@@ -311,7 +358,7 @@ prefill_kernel(const __grid_constant__ Args ka) {
         if (i >= kSFull && i < kSFull + 2) n = 2;
         if (i >= kPFull && i < kPHalf + 2) n = 4;
         if (i >= kVote && i < kVote + 2) n = 4;
-        if (i >= kDEmpty && i < kDEmpty + kDescs) n = 2 + 8;
+        if (i >= kDEmpty && i < kDEmpty + kDescs) n = FP8 ? 2 + 8 : 3 + 8;
         mbar_init(bar(i), n);
       }
       mbar_init_fence();
@@ -422,7 +469,7 @@ prefill_kernel(const __grid_constant__ Args ka) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = static_cast<uint32_t>(sm.tmem);
+  const uint32_t tmem = static_cast<uint32_t>(uniform(sm.tmem));
   const uint32_t tmem_o = tmem + 2 * kTile;
   auto slot_at = [&](int i) { return ring + (i % C::kSlots) * C::kSlot; };   // i: K 2g, V 2g + 1
 
@@ -437,35 +484,18 @@ prefill_kernel(const __grid_constant__ Args ka) {
     int n = 0, L = 0, t0 = 0, loaded = -1;
     int head[6] = {0, 0, 0, 0, 0, 0};
     bool ok = true;
-    // K (kv 0) or V of tile g, whose page ids are the first lanes' `id`
-    auto copy_tile = [&](int kv, int id, bool valid, int hh) {
-      const int i = 2 * g + kv;
-      uint32_t full, dst;
+    // K (kv 0) or V (1) of tile g of kv head hh, whose page ids are the first lanes' `id`
+    auto copy_tile = [&](int kv, int id, unsigned valid, int hh) {
       if constexpr (FP8) {
         if (raws >= C::kRaws && !wait_warp(kRawEmpty + raws % 2, raws / 2 - 1)) return false;
-        full = bar(kRawFull + raws % 2);
-        dst = raw + (raws % 2) * C::kRaw;
+        const uint32_t full = bar(kRawFull + raws % 2), to = raw + (raws % 2) * C::kRaw;
         ++raws;
+        copy_codes<D>(static_cast<const uint8_t*>(kv ? a.v_cache : a.k_cache), a.Hkv, hh, id, valid, to, full);
       } else {
+        const int i = 2 * g + kv;
         if (i >= C::kSlots && !wait_warp(kEmpty + i % C::kSlots, i / C::kSlots - 1)) return false;
-        full = bar(kFull + i % C::kSlots);
-        dst = slot_at(i);
-      }
-      const unsigned m = __ballot_sync(0xffffffffu, valid);
-      if (lane == 0)
-        mbar_arrive_expect_tx(full, static_cast<uint32_t>(__popc(m)) * (FP8 ? 16u * D : 32u * D));
-      __syncwarp();
-      if (valid) {
-        const int64_t page = static_cast<int64_t>(id) * a.Hkv + hh;
-        if constexpr (FP8) {
-          const uint8_t* pool = static_cast<const uint8_t*>(kv ? a.v_cache : a.k_cache);
-          page_g2s(dst + lane * 16 * D, pool + page * 16 * D, 16 * D, full);
-        } else {
-#pragma unroll
-          for (int x = 0; x < C::kHalves; ++x)
-            box_g2s(dst + x * C::kSub + lane * 2048, kv ? &ka.tm_v : &ka.tm_k, 64 * x, 0,
-                    static_cast<int>(page), full);
-        }
+        copy_pages<C::kHalves, C::kSub>(kv ? &ka.tm_v : &ka.tm_k, a.Hkv, hh, id, valid, slot_at(i),
+                                        bar(kFull + i % C::kSlots));
       }
       return true;
     };
@@ -560,7 +590,8 @@ prefill_kernel(const __grid_constant__ Args ka) {
           mt.vs[lane] = valid ? a.v_scale[page] : 0.f;
         }
         __syncwarp();
-        ok = copy_tile(0, id, valid, h) && (t > x.k_lo || copy_queries(x)) && copy_tile(1, id, valid, h);
+        ok = copy_tile(0, id, m, h) && (t > x.k_lo || copy_queries(x)) &&
+             (!FP8 || copy_tile(1, id, m, h));
       }
       // ---- the next item
       pos += u + kItemCost;
@@ -597,7 +628,8 @@ prefill_kernel(const __grid_constant__ Args ka) {
       if (FP8) {
         for (int r = 0; r < 2; ++r) settle(kRawFull + r, (raws - r + 1) / 2);
       } else {
-        for (int s = 0; s < C::kSlots; ++s) settle(kFull + s, (2 * g - s + C::kSlots - 1) / C::kSlots);
+        for (int i = (max(2 * g - C::kSlots, 0) + 1) / 2 * 2; i < 2 * g; i += 2)   // each place's last
+          settle(kFull + i % C::kSlots, i / C::kSlots + 1);
       }
     }
     __syncwarp();
@@ -623,6 +655,33 @@ prefill_kernel(const __grid_constant__ Args ka) {
     };
     auto full = [&](int slot, int parity) { return wait_warp(kFull + slot, parity); };
     bool issued = false, ok = true;
+    // The subtiles take turns, tile by tile: left alone they either run in step, and the tensor
+    // cores wait while both softmaxes run, or one runs ahead until the ring has no place
+    // for its keys.
+    int g = 0;                             // the tile in the CTA's stream
+    volatile int* mine = &sm.passed[w];
+    volatile int* other = &sm.passed[w ^ 1];
+    auto my_turn = [&]() {                 // tile g is the first subtile's first
+      uint64_t t0 = 0;
+      for (unsigned i = 1; *other < g + w; ++i) {
+        if (i % 256 != 0) continue;
+        if (*dead) return false;
+        const uint64_t now = global_ns();
+        if (t0 == 0) {
+          t0 = now;
+        } else if (now - t0 > ka.wait_limit_ns) {
+          *dead = 1;
+          atomicOr(a.status, kStatusTimeout);
+          return false;
+        }
+      }
+      return true;
+    };
+    auto passed = [&]() {
+      ++g;
+      __syncwarp();
+      if (lane == 0) *mine = g;
+    };
     auto scores = [&](bool last) {         // Q.K of the next tile, whose K has landed
       if (elect_one()) {
         mbar_arrive(bar(kSFull + w));      // (orders the tile's meta before the softmax's reads)
@@ -649,16 +708,20 @@ prefill_kernel(const __grid_constant__ Args ka) {
         }
         step2(ks, kp);
         step2(vs, vp);
+        passed();
       }
     };
     for (int d = 0; ok; ++d) {
       if (!wait_warp(kDFull + d % kDescs, d / kDescs)) break;
       const Desc& x = sm.desc[d % kDescs];
-      if (x.h < 0) break;
-      const int2 r = sub_tiles(x, w, sub, a.window);
+      if (uniform(x.h) < 0) break;
+      int2 r = sub_tiles(x, w, sub, a.window);
+      r.x = uniform(r.x);
+      r.y = uniform(r.y);
+      const int k_lo = uniform(x.k_lo), k_hi = uniform(x.k_hi);
       const bool some = r.x < r.y;
-      const int behind = some ? x.k_hi - r.y : 0;
-      pass(some ? r.x - x.k_lo : x.k_hi - x.k_lo);
+      const int behind = some ? k_hi - r.y : 0;
+      pass(some ? r.x - k_lo : k_hi - k_lo);
       if (ok && some) {
         ok = full(ks, kp) && wait_warp((FP8 && BF16 ? kQConv : kQFull) + w, q_n++);
         if (ok) {
@@ -668,16 +731,20 @@ prefill_kernel(const __grid_constant__ Args ka) {
       }
       for (int t = r.x; ok && t < r.y; ++t, ++p_n) {
         const bool more = t + 1 < r.y;
-        ok = full(vs, vp) && (!more || full(ks, kp)) && wait_warp(kPFull + w, p_n);
+        ok = full(vs, vp) && (!more || full(ks, kp)) && wait_warp(kPFull + w, p_n) &&
+             __all_sync(0xffffffffu, my_turn());
         if (!ok) break;
         tc_fence_after();
-        const bool skip = *reinterpret_cast<volatile int*>(&sm.skip[w]) != 0;
+        const bool skip = uniform(*reinterpret_cast<volatile int*>(&sm.skip[w])) != 0;
         const uint64_t dv = dv0 + static_cast<uint64_t>(vs * (C::kSlot >> 4));
-        if (!skip && elect_one()) {
+        if (skip) {
+          if (lane == 0) mbar_arrive(bar(kPVHalf + w));
+        } else if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < kTile / 32; ++k)
             umma_f16_ts(to, ts + 8 * k, dv + static_cast<uint64_t>(k * (2048 >> 4)), kIdPV,
                         t > r.x || k > 0);
+          umma_commit(bar(kPVHalf + w));
         }
         __syncwarp();
         ok = wait_warp(kPHalf + w, p_n);   // the weights of the second half of the tile
@@ -695,6 +762,7 @@ prefill_kernel(const __grid_constant__ Args ka) {
         __syncwarp();
         step2(vs, vp);
         if (more) scores(t + 2 == r.y);
+        passed();
       }
       pass(behind);
       __syncwarp();
@@ -710,7 +778,46 @@ prefill_kernel(const __grid_constant__ Args ka) {
       }
     }
     __syncwarp();
-  } else if (FP8 && warp >= kConvWarp) {
+  } else if (!FP8) {
+    // ================================================================ V's copies
+    int g = 0;
+    bool ok = true;
+    for (int d = 0; ok; ++d) {
+      if (!wait_warp(kDFull + d % kDescs, d / kDescs)) break;
+      const Desc& x = sm.desc[d % kDescs];
+      const int h = uniform(x.h);
+      if (h < 0) break;
+      const int k_lo = uniform(x.k_lo), k_hi = uniform(x.k_hi);
+      const int32_t* table = a.block_tables + static_cast<int64_t>(x.b) * a.mbs;
+      const int last_page = (x.L + 15) / 16 - 1;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kDEmpty + d % kDescs));
+      int ids = -1;
+      for (int t = k_lo; ok && t < k_hi; ++t, ++g) {
+        const int in4 = (t - k_lo) & 3;
+        if (in4 == 0) {
+          const int p = t * kPages + lane;
+          ids = p <= last_page && t + (lane >> 3) < k_hi ? table[p] : -1;
+        }
+        const int id = __shfl_sync(0xffffffffu, ids, in4 * 8 + (lane & 7));
+        const unsigned m = __ballot_sync(0xffffffffu, lane < kPages && id >= 0 && id < a.num_blocks);
+        const int i = 2 * g + 1;
+        ok = i < C::kSlots || wait_warp(kEmpty + i % C::kSlots, i / C::kSlots - 1);
+        if (ok)
+          copy_pages<C::kHalves, C::kSub>(&ka.tm_v, a.Hkv, h, id, m, slot_at(i), bar(kFull + i % C::kSlots));
+      }
+    }
+    if (lane == 0) {                       // no copy outlives the CTA
+      const uint64_t since = global_ns();
+      const uint64_t limit = ka.wait_limit_ns > kWaitLimitNs ? ka.wait_limit_ns : kWaitLimitNs;
+      if (!ok) --g;                        // (the last one was not made)
+      for (int i = max(2 * g - C::kSlots, 0) | 1; i < 2 * g; i += 2) {
+        while (!mbar_try_wait(bar(kFull + i % C::kSlots), (i / C::kSlots) & 1) && global_ns() - since < limit) {
+        }
+      }
+    }
+    __syncwarp();
+  } else {
     // ================================================================ codes to f16
     const int ct = tid - kConvWarp * 32;
     for (int f = 0;; ++f) {
@@ -775,8 +882,10 @@ prefill_kernel(const __grid_constant__ Args ka) {
       const int2 tiles = sub_tiles(x, w, sub, a.window);
       const int cnt = min(max(x.tokens - w * sub, 0), sub);
       const int first = x.L - x.n + x.i0 + w * sub, last = first + cnt - 1;
-      const int pos = first + tok;         // this row's (rows behind the subtile's: any)
-      float off = -INFINITY, l = 0.f, ref = 1.f;
+      const int pos = first + tok;         // this row's
+      // rows behind the subtile's hold whatever was there: they ask for nothing
+      const bool row_live = r < cnt * G;
+      float off = -INFINITY, l = 0.f, ref = FP8 ? 0.f : 1.f;
       float sl2 = ka.sl2;
       if (FP8 && BF16 && tiles.x < tiles.y) {
         // bf16 rows to f16, scaled by a power of two so that the row's largest element lies
@@ -805,7 +914,7 @@ prefill_kernel(const __grid_constant__ Args ka) {
               *u = pack2<false>(__uint_as_float(*u << 16) * f0 * f1, __uint_as_float(*u & 0xffff0000u) * f0 * f1);
             sts128(row + y * C::kSub + c * 16, v);
           }
-        sl2 = fmaxf(sl2 / f0 / f1, 1e-37f);
+        sl2 = copysignf(fmaxf(fabsf(sl2) / f0 / f1, 1e-37f), sl2);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kQConv + w));
@@ -832,113 +941,137 @@ prefill_kernel(const __grid_constant__ Args ka) {
                                  ((valid >> (2 * c + 1)) & 1u ? 0xffff0000u : 0u);
           return below(jh - 32 * c) & ~below(jl - 32 * c) & pages;
         };
-        // ---- the row's scores, and their maximum
+        // ---- the row's scores, 64 at a time with the next on their way
+        const bool start = t == tiles.x;
         float v[kTile];
         auto load = [&](int c) { tmem_ld<32>(ts + 32 * c, *reinterpret_cast<float (*)[32]>(v + 32 * c)); };
-        auto masked = [&](int c) {
-          if (ka.negative) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[32 * c + j] = -v[32 * c + j];
-          }
-          if (edge) {
-            const unsigned bits = word(c);
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (!(bits & (1u << j))) v[32 * c + j] = -INFINITY;
-          }
+        // what a score of page c is multiplied with (log2 units), and its weight
+        auto factor = [&](int c) {
+          if constexpr (FP8) return copysignf(fmaxf(fabsf(sl2) * mt.ks[c], 1e-37f), sl2);
+          else return sl2;
         };
+        auto largest = [&](int c) {        // of columns 64c .. 64c + 63, in log2 units
+          float m = -INFINITY;
+#pragma unroll
+          for (int k = 4 * c; k < 4 * c + 4; ++k) {
+            float x[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) x[j] = v[16 * k + j] * factor(k);
+            m = fmaxf(m, max_of<16>(x));
+          }
+          return m;
+        };
+        // ---- a new offset for the rows that `move`, at m; O (when it holds something) and
+        // the sum are scaled down to it, and to a reference of V's scales that does for v_big
+        auto set_offset = [&](bool move, float m, float v_big, bool scale_o) {
+          float f = 1.f;
+          if (move) {
+            const float to_off = fmaxf(off, m);
+            f = off == to_off ? 1.f : fast_exp2(off - to_off);
+            off = to_off;
+            l *= f;
+          }
+          if (FP8 && (v_big > 2.f * ref || !(ref > 0.f))) {
+            // a power of two at or above the largest scale so far
+            const float top = __uint_as_float((__float_as_uint(fmaxf(v_big, 1e-30f)) + 0x7fffffu) & 0x7f800000u);
+            f *= ref > 0.f ? ref / top : 1.f;
+            ref = top;
+          }
+          if (!scale_o) return;
+#pragma unroll 1
+          for (int c = 0; c < D / 16; ++c) {
+            float o[16];
+            tmem_ld<16>(to + 16 * c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[j] *= f;
+            tmem_st<16>(to + 16 * c, o);
+          }
+          tmem_wait_st();
+        };
+        // ---- the weights of columns 64c .. 64c + 63 at the standing offset, as 16-bit
+        // pairs; returns their sum
+        float p[2][16];
+        auto weigh = [&](int c) {
+          const float sub_off = (off == -INFINITY ? 0.f : off) - kLift;
+          const float inv_ref = FP8 ? 1.f / ref : 1.f;
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int j = 0; j < 64; j += 2) {
+            const int at = 64 * c + j;
+            const float k = factor(at / 16);
+            float2 e = fma2(make_float2(v[at], v[at + 1]), make_float2(k, k),
+                            make_float2(-sub_off, -sub_off));
+            e.x = fast_exp2(e.x);
+            e.y = fast_exp2(e.y);
+            sum[(j / 2) & 1] = add2(sum[(j / 2) & 1], e);
+            if constexpr (FP8) {
+              const float u = mt.vs[at / 16] * inv_ref;
+              e = mul2(e, make_float2(u, u));
+            }
+            p[j / 32][(j % 32) / 2] = __uint_as_float(pack2<kMmaBf16>(e.x, e.y));
+          }
+          const float2 both = add2(sum[0], sum[1]);
+          return both.x + both.y;
+        };
+        float v_big = 0.f;
+        if constexpr (FP8) {
+#pragma unroll
+          for (int c = 0; c < kPages; ++c) v_big = fmaxf(v_big, mt.vs[c]);
+        }
         load(0);
         load(1);
         tmem_wait_ld();
         load(2);
         load(3);
-        masked(0);
-        masked(1);
-        float m = -INFINITY, v_big = 0.f;
-        auto take_max = [&](int c) {       // of columns 64c .. 64c + 63
-          if constexpr (FP8) {
+        if (edge || start || (FP8 && v_big > 2.f * ref)) {
+          // The exact maximum first: masks are applied, a row has no offset yet, or the
+          // reference of V's scales moves.
+          tmem_wait_ld();
+          if (edge) {
+            const float out = ka.sl2 < 0.f ? INFINITY : -INFINITY;
 #pragma unroll
-            for (int k = 4 * c; k < 4 * c + 4; ++k) {
-              m = fmaxf(m, max_of<16>(v + 16 * k) * fmaxf(mt.ks[k], 1e-37f));
-              v_big = fmaxf(v_big, mt.vs[k]);
-            }
-          } else {
-            m = fmaxf(m, max_of<64>(v + 64 * c));
-          }
-        };
-        take_max(0);
-        tmem_wait_ld();
-        masked(2);
-        masked(3);
-        take_max(1);
-        m *= sl2;
-        // ---- a new offset (and reference of V's scales) where the standing one does not do
-        const bool start = t == tiles.x;
-        const bool move = m > off + kSlack || (FP8 && v_big > 2.f * ref) || start;
-        if (__any_sync(0xffffffffu, move)) {
-          float f = 1.f;
-          if (move) {
-            const float to_off = fmaxf(off, m);
-            const float fl = off == to_off ? 1.f : fast_exp2(off - to_off);
-            f = fl;
-            if (FP8) {
-              // a power of two at or above the largest scale so far
-              const float top = fmaxf(v_big, 1e-30f);
-              const float new_ref = start ? __uint_as_float((__float_as_uint(top) + 0x7fffffu) & 0x7f800000u)
-                                          : fmaxf(ref, __uint_as_float((__float_as_uint(top) + 0x7fffffu) & 0x7f800000u));
-              f *= ref / new_ref;
-              ref = new_ref;
-            }
-            off = to_off;
-            l *= fl;
-          }
-          if (!start) {                    // O, whose last product is done (S came after it)
-#pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
-              float o[16];
-              tmem_ld<16>(to + 16 * c, o);
-              tmem_wait_ld();
+            for (int c = 0; c < 4; ++c) {
+              const unsigned bits = word(c);
 #pragma unroll
-              for (int j = 0; j < 16; ++j) o[j] *= f;
-              tmem_st<16>(to + 16 * c, o);
+              for (int j = 0; j < 32; ++j)
+                if (!(bits & (1u << j))) v[32 * c + j] = out;
             }
-            tmem_wait_st();
           }
+          const float m = fmaxf(largest(0), largest(1));
+          const bool move = start || (row_live && m > off + kSlack);
+          if (__any_sync(0xffffffffu, move) || (FP8 && v_big > 2.f * ref))
+            set_offset(move, m, v_big, !start);
         }
-        // ---- the weights, in S's place
-        const float sub_off = (off == -INFINITY ? 0.f : off) - kLift;
-        const float inv_ref = FP8 ? 1.f / ref : 1.f;
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float p[16];
-#pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            float k = sl2, u = 1.f;
-            if constexpr (FP8) {
-              k = fmaxf(sl2 * mt.ks[2 * c + j / 16], 1e-37f);
-              u = mt.vs[2 * c + j / 16] * inv_ref;
+        for (int c = 0; c < 2; ++c) {
+          if (c == 1) tmem_wait_ld();
+          float sum = weigh(c);
+          if (!edge) {
+            // The weights at the standing offset do unless they have grown out of the
+            // products' range, which their sum shows (a NaN too: once around, and on).
+            const bool bad = row_live && !(sum <= kMaxSum);
+            if (__any_sync(0xffffffffu, bad)) {
+              load(2 * c);                 // (P has not been stored over these)
+              load(2 * c + 1);
+              tmem_wait_ld();
+              if (c == 1 && !wait_warp(kPVHalf + w, s_n - 1)) ok = false;
+              tc_fence_after();
+              set_offset(bad, largest(c), 0.f, c == 1 || !start);
+              sum = weigh(c);
             }
-            float2 e = fma2(make_float2(v[32 * c + j], v[32 * c + j + 1]), make_float2(k, k),
-                            make_float2(-sub_off, -sub_off));
-            e.x = fast_exp2(e.x);
-            e.y = fast_exp2(e.y);
-            sum[(j / 2) & 1] = add2(sum[(j / 2) & 1], e);
-            if constexpr (FP8) e = mul2(e, make_float2(u, u));
-            p[j / 2] = __uint_as_float(pack2<kMmaBf16>(e.x, e.y));
           }
-          tmem_st<16>(ts + 16 * c, p);
-          if (c == 1 && !edge) {           // the product of the first half may begin
+          l += sum;
+          tmem_st<16>(ts + 32 * c, p[0]);
+          tmem_st<16>(ts + 32 * c + 16, p[1]);
+          tmem_wait_st();
+          if (c == 0 && !edge) {           // the product of the first half may begin
             if (wq == 0 && lane == 0) sm.skip[w] = 0;
-            tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kPFull + w));
           }
         }
-        const float2 sums = add2(sum[0], sum[1]);
-        l += sums.x + sums.y;
-        tmem_wait_st();
         if (edge) {
           // token r of the tile: no data, a row of zeros; else is every value finite?
           const int i = 2 * g + 1;
@@ -1034,7 +1167,6 @@ prefill_kernel(const __grid_constant__ Args ka) {
         ++o_n;
         tc_fence_after();
       }
-      const bool row_live = r < cnt * G;
       if (x.whole) {
         const float inv = l == 0.f ? 0.f : ref / l;   // (a NaN stays one)
         uint16_t* out = static_cast<uint16_t*>(a.out) +
@@ -1215,10 +1347,9 @@ cudaError_t launch(const PrefillArgs& args, cudaStream_t s) {
   k.ws_head = reinterpret_cast<int*>(ws);
   k.ws_ml = reinterpret_cast<float2*>(ws + sp.ml);
   k.ws_acc = reinterpret_cast<float*>(ws + sp.acc);
-  k.negative = args.scale < 0.f;
-  // scale 0: every score counts alike, and a masked one still is -inf
-  const float sl2 = fabsf(args.scale) * 1.4426950408889634f;
-  k.sl2 = sl2 > 1e-30f ? sl2 : 1e-30f;
+  // scale 0: every score counts alike, and a masked one still gets the weight 0
+  const float sl2 = args.scale * 1.4426950408889634f;
+  k.sl2 = fabsf(sl2) > 1e-30f ? sl2 : 1e-30f;
   k.wait_limit_ns = kWaitLimitNs;
   // an item of up to 2 kSnap tiles is never cut: every place in it is that near a border
   const bool cuts = args.max_context_len > 2 * kSnap * kTile;
