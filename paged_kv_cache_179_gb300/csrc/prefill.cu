@@ -41,7 +41,7 @@
 // CTA-wide flag, at which every role leaves; copies and products in flight are waited
 // for and tensor memory is freed first.
 #include <climits>
-#include <mutex>
+#include <type_traits>
 
 #include <cudaTypedefs.h>
 
@@ -62,7 +62,7 @@ constexpr float kMaxSum = 32000.f;
 constexpr int kSnap = 4;                   // tiles
 // What an item costs besides its tiles (its queries, a pipeline that fills and drains, edges,
 // the result), in tiles: what it adds to the shares.
-constexpr int kItemCost = 4;
+constexpr int kItemCost = 8;
 constexpr int kMaxSeqs = 512;              // sequences a launch sorts
 constexpr int kDescs = 4;                  // pieces known ahead
 constexpr int kMetas = 8;                  // tiles whose pages' validity and scales are kept
@@ -72,7 +72,7 @@ constexpr int kHeader = 16;                // ints a CTA's header in the workspa
 struct Args {
   PrefillArgs a;
   CUtensorMap tm_q, tm_k, tm_v;
-  float* ws_acc;                           // [grid][2 parts][256 rows][D]
+  float* ws_acc;                           // [grid][2 parts][2 subtiles][D / 4][128 rows][4]
   float2* ws_ml;                           // [grid][2][256]: offset (log2 units), sum
   int* ws_head;                            // [grid][kHeader]
   float sl2;                               // scale log2(e), not 0
@@ -110,7 +110,7 @@ struct Desc {                              // a piece, or the end (h < 0)
 
 struct Meta {
   unsigned valid;                          // bit j: page j of the tile has a valid id
-  float ks[kPages], vs[kPages];
+  float ks[kPages], vs[kPages], v_big;     // E4M3 pools: the scales, V's largest
 };
 
 enum : int {                               // mbarriers
@@ -258,18 +258,6 @@ __device__ __forceinline__ int2 sub_tiles(const Desc& d, int w, int sub, int win
   const int lo = window > 0 ? max(0, first - window + 1) / kTile : 0;
   const int a = max(lo, d.k_lo), e = min(last / kTile + 1, d.k_hi);
   return a < e ? make_int2(a, e) : make_int2(0, 0);
-}
-
-// The largest of N values (four chains; NaN is passed over).
-template <int N>
-__device__ __forceinline__ float max_of(const float* v) {
-  float m[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-  for (int j = 4; j < N; j += 8)
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      m[k] = j + 4 + k < N ? fmaxf(fmaxf(m[k], v[j + k]), v[j + 4 + k]) : fmaxf(m[k], v[j + k]);
-  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
 // A warpgroup's registers a thread from here on (all its warps).
@@ -584,10 +572,17 @@ prefill_kernel(const __grid_constant__ Args ka) {
         const unsigned m = __ballot_sync(0xffffffffu, valid);
         Meta& mt = sm.meta[g % kMetas];
         if (lane == 0) mt.valid = m;
-        if (FP8 && lane < kPages) {
+        if constexpr (FP8) {
           const int64_t page = static_cast<int64_t>(valid ? id : 0) * a.Hkv + h;
-          mt.ks[lane] = valid ? a.k_scale[page] : 0.f;
-          mt.vs[lane] = valid ? a.v_scale[page] : 0.f;
+          const float sk = valid ? a.k_scale[page] : 0.f, sv = valid ? a.v_scale[page] : 0.f;
+          float top = sv;
+#pragma unroll
+          for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          if (lane < kPages) {
+            mt.ks[lane] = sk;
+            mt.vs[lane] = sv;
+            mt.v_big = top;
+          }
         }
         __syncwarp();
         ok = copy_tile(0, id, m, h) && (t > x.k_lo || copy_queries(x)) &&
@@ -893,184 +888,190 @@ prefill_kernel(const __grid_constant__ Args ka) {
         if (!wait_warp(kQFull + w, q_n)) break;
         const uint32_t row = q_at + w * C::kSlot + r * 128;
         float big = 0.f;
-#pragma unroll
-        for (int y = 0; y < C::kHalves; ++y)
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const uint4 v = lds128(row + y * C::kSub + c * 16);
-            for (const uint32_t u : {v.x, v.y, v.z, v.w})
-              big = fmaxf(big, fmaxf(fabsf(__uint_as_float(u << 16)), fabsf(__uint_as_float(u & 0xffff0000u))));
-          }
+#pragma unroll 4
+        for (int c = 0; c < 8 * C::kHalves; ++c) {
+          const uint4 x4 = lds128(row + (c >> 3) * C::kSub + (((c ^ r) & 7) << 4));
+          for (const uint32_t u : {x4.x, x4.y, x4.z, x4.w})
+            big = fmaxf(big, fmaxf(fabsf(__uint_as_float(u << 16)), fabsf(__uint_as_float(u & 0xffff0000u))));
+        }
         const int e = big > 0.f && big < INFINITY ? 14 - ilogbf(big) : 0;
         // 2^e in two factors: e reaches 147
         const float f0 = __uint_as_float(static_cast<uint32_t>(127 + e / 2) << 23);
         const float f1 = __uint_as_float(static_cast<uint32_t>(127 + e - e / 2) << 23);
-#pragma unroll
-        for (int y = 0; y < C::kHalves; ++y)
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            uint4 v = lds128(row + y * C::kSub + c * 16);
-            for (uint32_t* u : {&v.x, &v.y, &v.z, &v.w})
-              *u = pack2<false>(__uint_as_float(*u << 16) * f0 * f1, __uint_as_float(*u & 0xffff0000u) * f0 * f1);
-            sts128(row + y * C::kSub + c * 16, v);
-          }
+#pragma unroll 4
+        for (int c = 0; c < 8 * C::kHalves; ++c) {
+          const uint32_t chunk = row + (c >> 3) * C::kSub + (((c ^ r) & 7) << 4);
+          uint4 x4 = lds128(chunk);
+          for (uint32_t* u : {&x4.x, &x4.y, &x4.z, &x4.w})
+            *u = pack2<false>(__uint_as_float(*u << 16) * f0 * f1, __uint_as_float(*u & 0xffff0000u) * f0 * f1);
+          sts128(chunk, x4);
+        }
         sl2 = copysignf(fmaxf(fabsf(sl2) / f0 / f1, 1e-37f), sl2);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kQConv + w));
         ++q_n;
       }
-      for (int t = tiles.x; t < tiles.y; ++t) {
-        const int g = x.g0 + t - x.k_lo;
+      // tiles that all rows see whole, while their pages are valid: [full_lo, full_hi)
+      const int full_hi = (first + 1) / kTile;
+      const int full_lo = a.window > 0 ? (max(last - a.window + 1, 0) + kTile - 1) / kTile : 0;
+      // what a score of page c is multiplied with (log2 units)
+      auto factor = [&](const Meta& mt, int c) {
+        if constexpr (FP8) return copysignf(fmaxf(fabsf(sl2) * mt.ks[c], 1e-37f), sl2);
+        else return sl2;
+      };
+      // weights of N scores from page `page` on at the standing offset, as 16-bit pairs; their sum
+      auto weigh = [&](auto n, const Meta& mt, const float* s, float* out, int page, unsigned bits) {
+        constexpr int N = decltype(n)::value;
+        const float sub_off = (off == -INFINITY ? 0.f : off) - kLift;
+        [[maybe_unused]] const float inv_ref = FP8 ? 1.f / ref : 1.f;
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int j = 0; j < N; j += 2) {
+          const float k = factor(mt, page + j / 16);
+          float2 e = fma2(make_float2(s[j], s[j + 1]), make_float2(k, k), make_float2(-sub_off, -sub_off));
+          e.x = fast_exp2(e.x);
+          e.y = fast_exp2(e.y);
+          if (N == 32) {                   // (the exact form: what is masked weighs nothing)
+            e.x = (bits >> j) & 1u ? e.x : 0.f;
+            e.y = (bits >> (j + 1)) & 1u ? e.y : 0.f;
+          }
+          sum[(j / 2) & 1] = add2(sum[(j / 2) & 1], e);
+          if constexpr (FP8) {
+            const float u = mt.vs[page + j / 16] * inv_ref;
+            e = mul2(e, make_float2(u, u));
+          }
+          out[j / 2] = __uint_as_float(pack2<kMmaBf16>(e.x, e.y));
+        }
+        const float2 both = add2(sum[0], sum[1]);
+        return both.x + both.y;
+      };
+      auto announce = [&](int b) {         // this warp's part of P is written
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(b + w));
+      };
+      for (int t = tiles.x; ok && t < tiles.y; ++t) {
+        // ---- a run of whole tiles: a loop of its own, as short as it can be.  The weights at
+        // the standing offset do unless they have grown out of the products' range, which
+        // their sum shows (a NaN too); then the exact form below takes over, from that half on.
+        int from = 0;
+        bool more = t > tiles.x;           // (a row's first tile gives it its offset)
+        while (more) {
+          if (!wait_warp(kSFull + w, s_n)) {
+            ok = false;
+            break;
+          }
+          const Meta& mt = sm.meta[(x.g0 + t - x.k_lo) % kMetas];
+          if (t < full_lo || t >= full_hi || mt.valid != 0xffu || (FP8 && mt.v_big > 2.f * ref)) break;
+          tc_fence_after();
+          float v[kTile], p[32];
+          tmem_ld<32>(ts, *reinterpret_cast<float (*)[32]>(v));
+          tmem_ld<32>(ts + 32, *reinterpret_cast<float (*)[32]>(v + 32));
+          tmem_wait_ld();
+          tmem_ld<32>(ts + 64, *reinterpret_cast<float (*)[32]>(v + 64));
+          tmem_ld<32>(ts + 96, *reinterpret_cast<float (*)[32]>(v + 96));
+          float sum = weigh(std::integral_constant<int, 64>(), mt, v, p, 0, 0u);
+          if (__any_sync(0xffffffffu, row_live && !(sum <= kMaxSum))) {
+            tmem_wait_ld();
+            break;
+          }
+          l += sum;
+          tmem_st<32>(ts, p);
+          if (wq == 0 && lane == 0) sm.skip[w] = 0;
+          announce(kPFull);                // the product of the first half may begin
+          tmem_wait_ld();
+          sum = weigh(std::integral_constant<int, 64>(), mt, v + 64, p, 4, 0u);
+          if (__any_sync(0xffffffffu, row_live && !(sum <= kMaxSum))) {
+            from = 1;
+            break;
+          }
+          l += sum;
+          tmem_st<32>(ts + 32, p);
+          announce(kPHalf);
+          ++s_n;
+          more = ++t < tiles.y;
+        }
+        if (!ok || t == tiles.y) break;
+        // ---- the exact form: the first tile, tiles that some row sees in part, and where the
+        // offset or the reference of V's scales has to move
         if (!wait_warp(kSFull + w, s_n)) {
           ok = false;
           break;
         }
         ++s_n;
         tc_fence_after();
+        const int g = x.g0 + t - x.k_lo, p0 = t * kTile;
         const Meta& mt = sm.meta[g % kMetas];
         const unsigned valid = mt.valid;
-        const int p0 = t * kTile;
-        const bool edge = valid != 0xffu || p0 + kTile - 1 > first ||
-                          (a.window > 0 && p0 < last - a.window + 1);
+        const bool start = t == tiles.x, edge = t < full_lo || t >= full_hi || valid != 0xffu;
+        const float v_big = FP8 ? mt.v_big : 0.f;
         // columns [jl, jh) of the tile are this row's, those of valid pages
         const int jh = pos + 1 - p0, jl = a.window > 0 ? max(pos - a.window + 1 - p0, 0) : 0;
         auto below = [](int j) { return j <= 0 ? 0u : j >= 32 ? ~0u : (1u << j) - 1u; };
         auto word = [&](int c) {           // of columns 32c .. 32c + 31
           const unsigned pages = ((valid >> (2 * c)) & 1u ? 0xffffu : 0u) |
                                  ((valid >> (2 * c + 1)) & 1u ? 0xffff0000u : 0u);
-          return below(jh - 32 * c) & ~below(jl - 32 * c) & pages;
+          return edge ? below(jh - 32 * c) & ~below(jl - 32 * c) & pages : ~0u;
         };
-        // ---- the row's scores, 64 at a time with the next on their way
-        const bool start = t == tiles.x;
-        float v[kTile];
-        auto load = [&](int c) { tmem_ld<32>(ts + 32 * c, *reinterpret_cast<float (*)[32]>(v + 32 * c)); };
-        // what a score of page c is multiplied with (log2 units), and its weight
-        auto factor = [&](int c) {
-          if constexpr (FP8) return copysignf(fmaxf(fabsf(sl2) * mt.ks[c], 1e-37f), sl2);
-          else return sl2;
-        };
-        auto largest = [&](int c) {        // of columns 64c .. 64c + 63, in log2 units
+        if (from == 1 && !wait_warp(kPVHalf + w, s_n - 1)) {   // (O changes below)
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        {
           float m = -INFINITY;
-#pragma unroll
-          for (int k = 4 * c; k < 4 * c + 4; ++k) {
-            float x[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) x[j] = v[16 * k + j] * factor(k);
-            m = fmaxf(m, max_of<16>(x));
-          }
-          return m;
-        };
-        // ---- a new offset for the rows that `move`, at m; O (when it holds something) and
-        // the sum are scaled down to it, and to a reference of V's scales that does for v_big
-        auto set_offset = [&](bool move, float m, float v_big, bool scale_o) {
-          float f = 1.f;
-          if (move) {
-            const float to_off = fmaxf(off, m);
-            f = off == to_off ? 1.f : fast_exp2(off - to_off);
-            off = to_off;
-            l *= f;
-          }
-          if (FP8 && (v_big > 2.f * ref || !(ref > 0.f))) {
-            // a power of two at or above the largest scale so far
-            const float top = __uint_as_float((__float_as_uint(fmaxf(v_big, 1e-30f)) + 0x7fffffu) & 0x7f800000u);
-            f *= ref > 0.f ? ref / top : 1.f;
-            ref = top;
-          }
-          if (!scale_o) return;
 #pragma unroll 1
-          for (int c = 0; c < D / 16; ++c) {
-            float o[16];
-            tmem_ld<16>(to + 16 * c, o);
+          for (int c = 2 * from; c < 4; ++c) {
+            float s[32];
+            tmem_ld<32>(ts + 32 * c, s);
             tmem_wait_ld();
+            const unsigned bits = word(c);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) o[j] *= f;
-            tmem_st<16>(to + 16 * c, o);
-          }
-          tmem_wait_st();
-        };
-        // ---- the weights of columns 64c .. 64c + 63 at the standing offset, as 16-bit
-        // pairs; returns their sum
-        float p[2][16];
-        auto weigh = [&](int c) {
-          const float sub_off = (off == -INFINITY ? 0.f : off) - kLift;
-          const float inv_ref = FP8 ? 1.f / ref : 1.f;
-          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-          for (int j = 0; j < 64; j += 2) {
-            const int at = 64 * c + j;
-            const float k = factor(at / 16);
-            float2 e = fma2(make_float2(v[at], v[at + 1]), make_float2(k, k),
-                            make_float2(-sub_off, -sub_off));
-            e.x = fast_exp2(e.x);
-            e.y = fast_exp2(e.y);
-            sum[(j / 2) & 1] = add2(sum[(j / 2) & 1], e);
-            if constexpr (FP8) {
-              const float u = mt.vs[at / 16] * inv_ref;
-              e = mul2(e, make_float2(u, u));
-            }
-            p[j / 32][(j % 32) / 2] = __uint_as_float(pack2<kMmaBf16>(e.x, e.y));
-          }
-          const float2 both = add2(sum[0], sum[1]);
-          return both.x + both.y;
-        };
-        float v_big = 0.f;
-        if constexpr (FP8) {
-#pragma unroll
-          for (int c = 0; c < kPages; ++c) v_big = fmaxf(v_big, mt.vs[c]);
-        }
-        load(0);
-        load(1);
-        tmem_wait_ld();
-        load(2);
-        load(3);
-        if (edge || start || (FP8 && v_big > 2.f * ref)) {
-          // The exact maximum first: masks are applied, a row has no offset yet, or the
-          // reference of V's scales moves.
-          tmem_wait_ld();
-          if (edge) {
-            const float out = ka.sl2 < 0.f ? INFINITY : -INFINITY;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const unsigned bits = word(c);
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (!(bits & (1u << j))) v[32 * c + j] = out;
+            for (int j = 0; j < 32; ++j) {
+              const float y = s[j] * factor(mt, 2 * c + j / 16);
+              m = fmaxf(m, (bits >> j) & 1u ? y : -INFINITY);
             }
           }
-          const float m = fmaxf(largest(0), largest(1));
+          // A new offset for the rows that move, and a reference of V's scales that does for
+          // this tile's; O (when it holds something) and the sum are scaled down to them.
           const bool move = start || (row_live && m > off + kSlack);
-          if (__any_sync(0xffffffffu, move) || (FP8 && v_big > 2.f * ref))
-            set_offset(move, m, v_big, !start);
-        }
+          const bool refer = FP8 && (v_big > 2.f * ref || !(ref > 0.f));
+          if (refer || __any_sync(0xffffffffu, move)) {
+            float f = 1.f;
+            if (move) {
+              const float to_off = fmaxf(off, m);
+              f = off == to_off ? 1.f : fast_exp2(off - to_off);
+              off = to_off;
+              l *= f;
+            }
+            if (refer) {                   // a power of two at or above the largest scale so far
+              const float top = __uint_as_float((__float_as_uint(fmaxf(v_big, 1e-30f)) + 0x7fffffu) & 0x7f800000u);
+              f *= ref > 0.f ? ref / top : 1.f;
+              ref = top;
+            }
+            if (!start) {
+#pragma unroll 1
+              for (int c = 0; c < D / 16; ++c) {
+                float o[16];
+                tmem_ld<16>(to + 16 * c, o);
+                tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          if (c == 1) tmem_wait_ld();
-          float sum = weigh(c);
-          if (!edge) {
-            // The weights at the standing offset do unless they have grown out of the
-            // products' range, which their sum shows (a NaN too: once around, and on).
-            const bool bad = row_live && !(sum <= kMaxSum);
-            if (__any_sync(0xffffffffu, bad)) {
-              load(2 * c);                 // (P has not been stored over these)
-              load(2 * c + 1);
-              tmem_wait_ld();
-              if (c == 1 && !wait_warp(kPVHalf + w, s_n - 1)) ok = false;
-              tc_fence_after();
-              set_offset(bad, largest(c), 0.f, c == 1 || !start);
-              sum = weigh(c);
+                for (int j = 0; j < 16; ++j) o[j] *= f;
+                tmem_st<16>(to + 16 * c, o);
+              }
             }
           }
-          l += sum;
-          tmem_st<16>(ts + 32 * c, p[0]);
-          tmem_st<16>(ts + 32 * c + 16, p[1]);
-          tmem_wait_st();
-          if (c == 0 && !edge) {           // the product of the first half may begin
-            if (wq == 0 && lane == 0) sm.skip[w] = 0;
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kPFull + w));
+#pragma unroll 1
+          for (int c = 2 * from; c < 4; ++c) {
+            float s[32], y[16];
+            tmem_ld<32>(ts + 32 * c, s);
+            tmem_wait_ld();
+            l += weigh(std::integral_constant<int, 32>(), mt, s, y, 2 * c, word(c));
+            tmem_st<16>(ts + 16 * c, y);   // (over scores that have been read)
           }
+          tmem_wait_st();
         }
         if (edge) {
           // token r of the tile: no data, a row of zeros; else is every value finite?
@@ -1082,17 +1083,19 @@ prefill_kernel(const __grid_constant__ Args ka) {
           const bool data = p0 + r < x.L && ((valid >> (r >> 4)) & 1u);
           const uint32_t vrow = slot_at(i) + r * 128;
           bool odd = false;
-#pragma unroll
-          for (int y = 0; y < C::kHalves; ++y)
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              const uint4 v = lds128(vrow + y * C::kSub + c * 16);
-              constexpr uint32_t kExp = kMmaBf16 ? 0x7f80u : 0x7c00u;
-              for (const uint32_t u : {v.x, v.y, v.z, v.w})
-                odd |= (u & kExp) == kExp || ((u >> 16) & kExp) == kExp;
-              if (!data && (v.x | v.y | v.z | v.w) != 0u)
-                sts128(vrow + y * C::kSub + c * 16, make_uint4(0u, 0u, 0u, 0u));
-            }
+#pragma unroll 4
+          for (int c = 0; c < 8 * C::kHalves; ++c) {
+            // (neighbouring rows begin at different chunks: no bank twice)
+            const uint32_t at = vrow + (c >> 3) * C::kSub + (((c ^ r) & 7) << 4);
+            const uint4 x4 = lds128(at);
+            // a 16-bit value is not finite when its exponent's bits are all set: one more in
+            // the lowest of them carries into the sign
+            constexpr uint32_t kExp = kMmaBf16 ? 0x7f807f80u : 0x7c007c00u;
+            constexpr uint32_t kOne = kMmaBf16 ? 0x00800080u : 0x04000400u;
+            odd |= ((((x4.x & kExp) + kOne) | ((x4.y & kExp) + kOne) | ((x4.z & kExp) + kOne) |
+                     ((x4.w & kExp) + kOne)) & 0x80008000u) != 0u;
+            if (!data && (x4.x | x4.y | x4.z | x4.w) != 0u) sts128(at, make_uint4(0u, 0u, 0u, 0u));
+          }
           fence_proxy_async_smem();
           const bool any = __any_sync(0xffffffffu, odd && data);
           if (lane == 0) {
@@ -1151,13 +1154,11 @@ prefill_kernel(const __grid_constant__ Args ka) {
             tmem_wait_st();
           }
           if (wq == 0 && lane == 0) sm.skip[w] = self;
+        } else if (from == 0 && wq == 0 && lane == 0) {
+          sm.skip[w] = 0;
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if (edge) mbar_arrive(bar(kPFull + w));
-          mbar_arrive(bar(kPHalf + w));
-        }
+        if (from == 0) announce(kPFull);
+        announce(kPHalf);
       }
       if (!ok) break;
       // ---- the piece's result
@@ -1167,44 +1168,37 @@ prefill_kernel(const __grid_constant__ Args ka) {
         ++o_n;
         tc_fence_after();
       }
-      if (x.whole) {
-        const float inv = l == 0.f ? 0.f : ref / l;   // (a NaN stays one)
-        uint16_t* out = static_cast<uint16_t*>(a.out) +
-                        ((static_cast<int64_t>(x.t0) + w * sub + tok) * a.Hq + x.h * G + hd) * D;
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          float o[32];
-          if (some) {
-            tmem_ld<32>(to + 32 * c, o);
-            tmem_wait_ld();
-          }
-          if (row_live) {
-            uint32_t p[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              p[j] = some && l != 0.f ? pack2<BF16>(o[2 * j] * inv, o[2 * j + 1] * inv) : 0u;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              *reinterpret_cast<uint4*>(out + 32 * c + 8 * j) =
-                  make_uint4(p[4 * j], p[4 * j + 1], p[4 * j + 2], p[4 * j + 3]);
-          }
-          __syncwarp();
-        }
-      } else {
-        const int64_t at = (static_cast<int64_t>(cta) * 2 + x.part) * 256 + w * kTile + r;
+      const bool any = some && l != 0.f;   // (a NaN is something)
+      const float f = !any ? 0.f : x.whole ? ref / l : ref;
+      uint16_t* out = static_cast<uint16_t*>(a.out) +
+                      ((static_cast<int64_t>(x.t0) + w * sub + tok) * a.Hq + x.h * G + hd) * D;
+      const int64_t at = (static_cast<int64_t>(cta) * 2 + x.part) * 256 + w * kTile + r;
+      if (!x.whole) ka.ws_ml[at] = make_float2(off, l);
+#pragma unroll 1
+      for (int c = 0; c < D / 16; ++c) {
+        float o[16];
         if (some) {
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            float o[32];
-            tmem_ld<32>(to + 32 * c, o);
-            tmem_wait_ld();
-            float4* dst = reinterpret_cast<float4*>(ka.ws_acc + at * D + 32 * c);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              dst[j] = make_float4(o[4 * j] * ref, o[4 * j + 1] * ref, o[4 * j + 2] * ref, o[4 * j + 3] * ref);
-          }
+          tmem_ld<16>(to + 16 * c, o);
+          tmem_wait_ld();
         }
-        ka.ws_ml[at] = make_float2(off, l);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[j] = any ? o[j] * f : 0.f;
+        if (x.whole) {
+          if (row_live) {
+#pragma unroll
+            for (int j = 0; j < 16; j += 8)
+              *reinterpret_cast<uint4*>(out + 16 * c + j) =
+                  make_uint4(pack2<BF16>(o[j], o[j + 1]), pack2<BF16>(o[j + 2], o[j + 3]),
+                             pack2<BF16>(o[j + 4], o[j + 5]), pack2<BF16>(o[j + 6], o[j + 7]));
+          }
+        } else {                           // four columns of all rows together
+          float4* dst = reinterpret_cast<float4*>(ka.ws_acc) +
+                        ((static_cast<int64_t>(cta) * 2 + x.part) * 2 + w) * (kTile * D / 4) + r;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            dst[(4 * c + j) * kTile] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+        }
+        __syncwarp();
       }
       tc_fence_before();
       __syncwarp();
@@ -1222,7 +1216,7 @@ prefill_kernel(const __grid_constant__ Args ka) {
 
 // Joins the parts of a cut item: CTA w's item is the one that CTA w of the launch
 // before left open, with a part in each of the next ones up to where it ends.
-constexpr int kMergeRows = 16;             // rows a CTA: two a warp
+constexpr int kMergeRows = 32;             // rows a CTA
 template <int D, bool BF16>
 __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Args ka, int grid) {
   const PrefillArgs& a = ka.a;
@@ -1230,45 +1224,50 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Args
   const int* head = ka.ws_head + w * kHeader;
   if (!head[kHasTail]) return;
   const int t0 = head[kTailT0], h = head[kTailH], tokens = head[kTailTokens];
+  const int row = blockIdx.y * kMergeRows + lane, s = row / kTile, r = row % kTile;
+  if (s * ka.sub >= tokens) return;        // (of the whole CTA: 32 rows are of one subtile)
   int parts = 2;                             // (w, 1), (w + 1, 0), ..
   while (w + parts < grid && !ka.ws_head[(w + parts - 1) * kHeader + kHeadEnds]) ++parts;
+  auto at = [&](int p) { return p == 0 ? w * 2 + 1 : (w + p) * 2; };
+  // a lane a row, a warp D / 32 groups of four columns
+  float top = -INFINITY;
+  for (int p = 0; p < parts; ++p) {
+    const float2 ml = ka.ws_ml[at(p) * INT64_C(256) + row];
+    if (ml.y != 0.f) top = fmaxf(top, ml.x);
+  }
   constexpr int E = D / 32;
-  for (int i = warp; i < kMergeRows; i += 8) {
-    const int row = blockIdx.y * kMergeRows + i, s = row / kTile, r = row % kTile;
-    const int tok = r / a.group, hd = r - tok * a.group;
-    if (tok >= ka.sub || s * ka.sub + tok >= tokens) continue;
-    auto at = [&](int p) { return (p == 0 ? w * 2 + 1 : (w + p) * 2) * INT64_C(256) + row; };
-    float top = -INFINITY;
-    for (int p = lane; p < parts; p += 32) {
-      const float2 ml = ka.ws_ml[at(p)];
-      if (ml.y != 0.f) top = fmaxf(top, ml.x);
+  float4 acc[E] = {};
+  float l = 0.f;
+  for (int p = 0; p < parts; ++p) {
+    const float2 ml = ka.ws_ml[at(p) * INT64_C(256) + row];
+    const float f = ml.y == 0.f ? 0.f : ml.x == top ? 1.f : fast_exp2(ml.x - top);
+    l += ml.y * f;
+    const float4* src = reinterpret_cast<const float4*>(ka.ws_acc) +
+                        (at(p) * INT64_C(2) + s) * (kTile * D / 4) + warp * E * kTile + r;
+    float4 v[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = src[e * kTile];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {          // (a part that saw nothing holds zeros)
+      acc[e].x += v[e].x * f;
+      acc[e].y += v[e].y * f;
+      acc[e].z += v[e].z * f;
+      acc[e].w += v[e].w * f;
     }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  __shared__ uint2 tile[kMergeRows][D / 4 + 1];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    float acc[E] = {}, l = 0.f;
-    for (int p = 0; p < parts; ++p) {
-      const float2 ml = ka.ws_ml[at(p)];
-      if (ml.y == 0.f) continue;           // nothing seen: no O was written
-      const float f = ml.x == top ? 1.f : fast_exp2(ml.x - top);
-      l += ml.y * f;
-      const float* src = ka.ws_acc + at(p) * D + lane * E;
-      float v[E];
-      if constexpr (E == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(src);
-        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-      } else {
-        const float2 x = *reinterpret_cast<const float2*>(src);
-        v[0] = x.x, v[1] = x.y;
-      }
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] += v[e] * f;
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    uint32_t* out = reinterpret_cast<uint32_t*>(
-        static_cast<uint16_t*>(a.out) +
-        ((static_cast<int64_t>(t0) + s * ka.sub + tok) * a.Hq + h * a.group + hd) * D + lane * E);
-#pragma unroll
-    for (int e = 0; e < E; e += 2) out[e / 2] = pack2<BF16>(acc[e] * inv, acc[e + 1] * inv);
+  for (int e = 0; e < E; ++e)
+    tile[lane][warp * E + e] = make_uint2(pack2<BF16>(acc[e].x * inv, acc[e].y * inv),
+                                          pack2<BF16>(acc[e].z * inv, acc[e].w * inv));
+  __syncthreads();
+  for (int i = threadIdx.x; i < kMergeRows * (D / 4); i += 256) {
+    const int k = i / (D / 4), c = i % (D / 4), rk = blockIdx.y * kMergeRows % kTile + k, tk = rk / a.group;
+    if (tk >= ka.sub || s * ka.sub + tk >= tokens) continue;
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) +
+                              ((static_cast<int64_t>(t0) + s * ka.sub + tk) * a.Hq + h * a.group + rk - tk * a.group) * D +
+                              4 * c) = tile[k][c];
   }
 }
 
