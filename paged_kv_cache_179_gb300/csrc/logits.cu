@@ -59,7 +59,7 @@ __device__ __forceinline__ int element(int k, int j, int t) {
 }
 
 template <typename T, bool PROBS, bool WIDE, int THREADS>
-__global__ void __launch_bounds__(THREADS)
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS)
 logits_kernel(const LogitsArgs a, int slice, int rows_per_unit) {
   using O = std::conditional_t<PROBS, float, T>;
   constexpr int kSteps = kPer / kVec, kWarps = THREADS / 32;
@@ -165,25 +165,44 @@ logits_kernel(const LogitsArgs a, int slice, int rows_per_unit) {
         x[k * kVec + j] = e < n ? to_f32(in[e]) : -INFINITY;
       }
     }
-#pragma unroll
-    for (int q = 0; q < kPer; ++q) {
-      const int e = element<WIDE, THREADS>(q / kVec, q % kVec, tid);
-      if (e >= n) continue;
-      const unsigned w = seen[e];
-      if (w != 0u) {
-        const unsigned count = w & kCount;
-        if (count != 0u || (w & kInPrompt)) x[q] = x[q] > 0.f ? x[q] / rep : x[q] * rep;
-        if (count != 0u) x[q] -= fmaf(freq, static_cast<float>(count), pres);
-        if (w & kHasBias) {
-          float s = 0.f;
-          for (int j = 0; j < n_bias; ++j)
-            if (bias_t[j] == e) s += bias_v[j];
-          x[q] += s;
-        }
+    auto adjust = [&](int e, unsigned w, float v) {   // a token that something is known of
+      const unsigned count = w & kCount;
+      if (count != 0u || (w & kInPrompt)) v = v > 0.f ? v / rep : v * rep;
+      if (count != 0u) v -= fmaf(freq, static_cast<float>(count), pres);
+      if (w & kHasBias) {
+        float s = 0.f;
+        for (int j = 0; j < n_bias; ++j)
+          if (bias_t[j] == e) s += bias_v[j];
+        v += s;
       }
-      if (allowed != nullptr) {
-        const int t = lo + e;
-        if (!((allowed[t >> 5] >> (t & 31)) & 1u)) x[q] = -INFINITY;
+      return v;
+    };
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+      if constexpr (WIDE) {
+        const int e = element<WIDE, THREADS>(k, 0, tid);
+        if (e >= n) continue;
+        // (slices are multiples of 32 tokens: four tokens share a word of the mask)
+        const uint4 w = *reinterpret_cast<const uint4*>(seen + e);
+        const unsigned ok = allowed != nullptr ? allowed[(lo + e) >> 5] >> (e & 31) : ~0u;
+        if ((w.x | w.y | w.z | w.w) != 0u) {
+          if (w.x != 0u) x[k * kVec] = adjust(e, w.x, x[k * kVec]);
+          if (w.y != 0u) x[k * kVec + 1] = adjust(e + 1, w.y, x[k * kVec + 1]);
+          if (w.z != 0u) x[k * kVec + 2] = adjust(e + 2, w.z, x[k * kVec + 2]);
+          if (w.w != 0u) x[k * kVec + 3] = adjust(e + 3, w.w, x[k * kVec + 3]);
+        }
+#pragma unroll
+        for (int j = 0; j < kVec; ++j)
+          if (!((ok >> j) & 1u)) x[k * kVec + j] = -INFINITY;
+      } else {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+          const int e = element<WIDE, THREADS>(k, j, tid), q = k * kVec + j;
+          if (e >= n) continue;
+          const unsigned w = seen[e];
+          if (w != 0u) x[q] = adjust(e, w, x[q]);
+          if (allowed != nullptr && !((allowed[(lo + e) >> 5] >> (e & 31)) & 1u)) x[q] = -INFINITY;
+        }
       }
     }
     if constexpr (PROBS) {

@@ -23,7 +23,11 @@ namespace {
 
 constexpr int kScanThreads = 1024;
 constexpr int kScanWarps = kScanThreads / 32;
-constexpr int kScanCtas = 8;                       // a portable cluster
+constexpr int kScanCtas = 8;                       // a portable cluster, for larger pools
+// Up to this many pages one CTA ranks by itself: 4 pages a lane, two barriers less.
+constexpr int kOneCtaPages = 4096;
+// Where items' pages go is kept in shared memory for up to this many items.
+constexpr int kKeptItems = 8192;
 constexpr unsigned kMany = (1u << 30) + 1u;        // sums of needs saturate above any pool
 
 __device__ __forceinline__ void st_cluster_u32(void* p, uint32_t rank, uint32_t v) {
@@ -48,13 +52,31 @@ __device__ __forceinline__ unsigned live_bits(int4 c) {
   return (c.x > 0) | (c.y > 0) << 1 | (c.z > 0) << 2 | (c.w > 0) << 3;
 }
 
+// Pages of this warp's part whose bits_of(counts) are set.
+template <typename F>
+__device__ __forceinline__ unsigned count_part(const int32_t* ref, int num_blocks, int behind, int g0,
+                                               int g1, int lane, F bits_of) {
+  unsigned n = 0;
+  for (int g = g0; g < g1; g += 128) {             // four loads in flight
+    int4 c[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      c[u] = g + 32 * u + lane < g1 ? counts_at(ref, g + 32 * u + lane, num_blocks, behind)
+                                    : make_int4(behind, behind, behind, behind);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) n += __popc(bits_of(c[u]));
+  }
+  return __reduce_add_sync(0xffffffffu, n);
+}
+
 // This warp's part of the groups of four pages: an equal contiguous share.
 struct Part {
   int g0, g1;
 };
+template <int CTAS>
 __device__ __forceinline__ Part my_part(int num_blocks, uint32_t rank, int warp) {
   const int groups = (num_blocks + 3) / 4;
-  const int parts = kScanCtas * kScanWarps;
+  const int parts = CTAS * kScanWarps;
   const int per = (groups + parts - 1) / parts;
   const int64_t w = static_cast<int64_t>(rank) * kScanWarps + warp;
   const int g0 = static_cast<int>(min(w * per, static_cast<int64_t>(groups)));
@@ -68,6 +90,7 @@ __device__ __forceinline__ Part my_part(int num_blocks, uint32_t rank, int warp)
 struct Before {
   unsigned before, total;
 };
+template <int CTAS>
 __device__ __forceinline__ Before cluster_prefix(unsigned n, unsigned* mine, unsigned* box, int warp,
                                                  int lane, uint32_t rank) {
   if (lane == 0) mine[warp] = n;
@@ -81,11 +104,12 @@ __device__ __forceinline__ Before cluster_prefix(unsigned n, unsigned* mine, uns
   }
   const unsigned all = __shfl_sync(0xffffffffu, inc, 31);
   const unsigned in_cta = __shfl_sync(0xffffffffu, inc - sum, warp);
-  if (warp == 0 && lane < kScanCtas) st_cluster_u32(box + rank, lane, all);
+  if (CTAS == 1) return Before{in_cta, all};
+  if (warp == 0 && lane < CTAS) st_cluster_u32(box + rank, lane, all);
   cluster_sync();
   Before b{in_cta, 0u};
 #pragma unroll
-  for (int r = 0; r < kScanCtas; ++r) {
+  for (int r = 0; r < CTAS; ++r) {
     const unsigned v = box[r];
     b.before += static_cast<uint32_t>(r) < rank ? v : 0u;
     b.total += v;
@@ -147,27 +171,30 @@ __device__ __forceinline__ Need need_of(const TakeArgs& a, int i, bool report) {
   return n;
 }
 
-template <bool FORK>
+template <bool FORK, int CTAS>
 __global__ void __launch_bounds__(kScanThreads, 1) take_kernel(const TakeArgs a) {
-  extern __shared__ __align__(16) int first[];     // [items + 1]: needs before each item
+  // [items + 1]: needs before each item; then, of up to kKeptItems, the place in the tables
+  // of the page of rank 0 of each item (-1: passed over)
+  extern __shared__ __align__(16) int first[];
   __shared__ unsigned mine[kScanWarps], box[kScanCtas], sums[kScanWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t rank = cluster_rank();
-  cluster_arrive();                                // (this CTA has started)
+  const uint32_t rank = CTAS > 1 ? cluster_rank() : 0u;
+  if (CTAS > 1) cluster_arrive();                  // (this CTA has started)
+  const bool kept = a.items <= kKeptItems;
+  int64_t* place = reinterpret_cast<int64_t*>(first + (a.items + 4) / 4 * 4);
   // ---- the free pages of this warp's part
-  const Part part = my_part(a.num_blocks, rank, warp);
-  unsigned n_free = 0;
-  for (int g = part.g0 + lane; g < part.g1; g += 32)
-    n_free += __popc(free_bits(counts_at(a.ref_counts, g, a.num_blocks, 1)));
-  n_free = warp_sum(n_free);
+  const Part part = my_part<CTAS>(a.num_blocks, rank, warp);
+  const unsigned n_free = count_part(a.ref_counts, a.num_blocks, 1, part.g0, part.g1, lane, free_bits);
   // ---- the needs and their prefix sums, by every CTA for itself
   const int per = (a.items + kScanThreads - 1) / kScanThreads;
   const int i0 = min(a.items, tid * per), i1 = min(a.items, i0 + per);
+  auto place_of = [&](const Need& n) { return static_cast<int64_t>(n.row) * a.mbs + n.entry; };
   unsigned sum = 0;
   for (int i = i0; i < i1; ++i) {
-    const int pages = max(need_of<FORK>(a, i, rank == 0).pages, 0);
-    first[i] = pages;
-    sum = min(sum + pages, kMany);
+    const Need n = need_of<FORK>(a, i, rank == 0);
+    first[i] = max(n.pages, 0);
+    if (kept) place[i] = n.pages < 0 ? -1 : place_of(n);
+    sum = min(sum + first[i], kMany);
   }
   unsigned inc = sum;
 #pragma unroll
@@ -177,8 +204,8 @@ __global__ void __launch_bounds__(kScanThreads, 1) take_kernel(const TakeArgs a)
   }
   if (lane == 31) sums[warp] = inc;
   const unsigned up = __shfl_up_sync(0xffffffffu, inc, 1);
-  cluster_wait();
-  const Before at = cluster_prefix(n_free, mine, box, warp, lane, rank);   // (syncs: sums are there)
+  if (CTAS > 1) cluster_wait();
+  const Before at = cluster_prefix<CTAS>(n_free, mine, box, warp, lane, rank);   // (syncs: sums are there)
   unsigned ex = lane > 0 ? up : 0u;
   for (int w = 0; w < warp; ++w) ex = min(ex + sums[w], kMany);
   for (int i = i0; i < i1; ++i) {
@@ -200,56 +227,72 @@ __global__ void __launch_bounds__(kScanThreads, 1) take_kernel(const TakeArgs a)
   };
   const unsigned limit = first[last_at_most(static_cast<int>(at.total))];
   unsigned k0 = at.before;
+  auto counts = [&](int g) {
+    return g + lane < part.g1 ? counts_at(a.ref_counts, g + lane, a.num_blocks, 1) : make_int4(1, 1, 1, 1);
+  };
+  int4 c = part.g0 < part.g1 ? counts(part.g0) : make_int4(1, 1, 1, 1);
   for (int g = part.g0; g < part.g1 && k0 < limit; g += 32) {
-    const int4 c = counts_at(a.ref_counts, min(g + lane, part.g1 - 1), a.num_blocks, 1);
-    unsigned bits = g + lane < part.g1 ? free_bits(c) : 0u;
+    unsigned bits = free_bits(c);
+    if (g + 32 < part.g1) c = counts(g + 32);      // on their way
     const unsigned mine_n = __popc(bits);
     unsigned k = k0 + warp_prefix(mine_n, lane);
-    for (; bits != 0u && k < limit; bits &= bits - 1, ++k) {
-      const int page = 4 * (g + lane) + __ffs(bits) - 1;
-      const int i = last_at_most(static_cast<int>(k));
-      const Need n = need_of<FORK>(a, i, false);
-      a.block_tables[static_cast<int64_t>(n.row) * a.mbs + n.entry + (k - first[i])] = page;
-      a.ref_counts[page] = 1;
+    if (bits != 0u && k < limit) {
+      int i = last_at_most(static_cast<int>(k));   // this lane's pages have ranks k, k + 1, ..
+      for (; bits != 0u && k < limit; bits &= bits - 1, ++k) {
+        while (first[i + 1] <= static_cast<int>(k)) ++i;
+        const int page = 4 * (g + lane) + __ffs(bits) - 1;
+        const int64_t to = kept ? place[i] : place_of(need_of<FORK>(a, i, false));
+        a.block_tables[to + (k - first[i])] = page;
+        a.ref_counts[page] = 1;
+      }
     }
     k0 += warp_sum(mine_n);
   }
   // ---- what the items hold now, once no CTA reads num_pages any more
-  cluster_sync();
+  if (CTAS > 1) cluster_sync();
+  else __syncthreads();
   if (rank != 0) return;
   for (int i = tid; i < a.items; i += kScanThreads) {
-    const Need n = need_of<FORK>(a, i, false);
-    const bool ok = n.pages >= 0 && static_cast<unsigned>(first[i] + n.pages) <= at.total;
+    // (a kept item's need is the difference of the prefix sums, unless those have saturated,
+    // and then it is not granted)
+    const bool passed_over = kept ? place[i] < 0 : need_of<FORK>(a, i, false).pages < 0;
+    const bool ok = !passed_over && static_cast<unsigned>(first[i + 1]) <= at.total;
+    if (!FORK && ok) a.num_pages[a.rows[i]] = need_of<FORK>(a, i, false).holds;
     a.granted[i] = ok;
-    if (!FORK && ok) a.num_pages[n.row] = n.holds;
   }
 }
 
-template <bool FORK>
+template <bool FORK, int CTAS>
 cudaError_t launch_take(const TakeArgs& a, cudaStream_t s) {
-  auto* kern = take_kernel<FORK>;
-  const size_t smem = (static_cast<size_t>(a.items) + 1) * 4;
+  auto* kern = take_kernel<FORK, CTAS>;
+  const size_t smem = (static_cast<size_t>(a.items) + 4) / 4 * 16 +
+                      (a.items <= kKeptItems ? static_cast<size_t>(a.items) * 8 : 0);
   if (smem > 47 * 1024) {                          // (the default limit is 48 KB with the static arrays)
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (kPagesMaxItems + 1) * 4);
+                                               (kPagesMaxItems + 4) * 4);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kScanCtas);
+  cfg.gridDim = dim3(CTAS);
   cfg.blockDim = dim3(kScanThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kScanCtas;
+  attr[0].val.clusterDim.x = CTAS;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = CTAS > 1 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kern, a);
+}
+template <bool FORK>
+cudaError_t launch_take(const TakeArgs& a, cudaStream_t s) {
+  static_assert(kKeptItems * 12 + 16 <= (kPagesMaxItems + 4) * 4, "one limit serves both layouts");
+  return a.num_blocks <= kOneCtaPages ? launch_take<FORK, 1>(a, s) : launch_take<FORK, kScanCtas>(a, s);
 }
 
 // -------------------------------------------------------------------- giving back
-constexpr int kFreeThreads = 256;
+constexpr int kFreeThreads = 1024;
 __global__ void __launch_bounds__(kFreeThreads)
 free_kernel(int32_t* tables, int mbs, int32_t* num_pages, int num_rows, const int32_t* rows,
             int32_t* ref, int num_blocks, unsigned* status) {
@@ -357,19 +400,17 @@ __host__ __device__ inline CompactSpace compact_space(void* ws, int num_blocks) 
 }
 
 // Ranks the live pages; writes num_live, moved_to, ref_counts_out and the lists.
+template <int CTAS>
 __global__ void __launch_bounds__(kScanThreads, 1) compact_plan_kernel(const CompactArgs a) {
   __shared__ unsigned mine[kScanWarps], box[2][kScanCtas];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_rank();
-  cluster_arrive();                                // (this CTA has started)
+  const uint32_t rank = CTAS > 1 ? cluster_rank() : 0u;
+  if (CTAS > 1) cluster_arrive();                  // (this CTA has started)
   const CompactSpace ws = compact_space(a.workspace, a.num_blocks);
-  const Part part = my_part(a.num_blocks, rank, warp);
-  unsigned n = 0;
-  for (int g = part.g0 + lane; g < part.g1; g += 32)
-    n += __popc(live_bits(counts_at(a.ref_counts, g, a.num_blocks, 0)));
-  n = warp_sum(n);
-  cluster_wait();
-  const Before at = cluster_prefix(n, mine, box[0], warp, lane, rank);
+  const Part part = my_part<CTAS>(a.num_blocks, rank, warp);
+  const unsigned n = count_part(a.ref_counts, a.num_blocks, 0, part.g0, part.g1, lane, live_bits);
+  if (CTAS > 1) cluster_wait();
+  const Before at = cluster_prefix<CTAS>(n, mine, box[0], warp, lane, rank);
   const int live = static_cast<int>(at.total);
   // ---- pages that stay, holes (rank: free pages below) and movers (live ones below)
   unsigned k0 = at.before, holes = 0;
@@ -401,10 +442,11 @@ __global__ void __launch_bounds__(kScanThreads, 1) compact_plan_kernel(const Com
   }
   holes = warp_sum(holes);
   __syncthreads();                                 // `mine` has been read by all
-  const int moves = static_cast<int>(cluster_prefix(holes, mine, box[1], warp, lane, rank).total);
+  const int moves = static_cast<int>(cluster_prefix<CTAS>(holes, mine, box[1], warp, lane, rank).total);
+  if (CTAS == 1) __syncthreads();
   // (the barrier inside: the lists are whole) movers take the holes, in order
   for (int m = static_cast<int>(rank) * kScanThreads + threadIdx.x; m < moves;
-       m += kScanCtas * kScanThreads) {
+       m += CTAS * kScanThreads) {
     const int src = ws.movers[live - moves + m], dst = ws.holes[m];
     const int count = a.ref_counts[src];
     a.moved_to[src] = dst;
@@ -476,8 +518,9 @@ size_t compact_workspace_bytes(int num_blocks) {
 }
 
 cudaError_t launch_compact_pages(const CompactArgs& a, const PagePools& p, cudaStream_t s) {
+  const bool one = a.num_blocks <= kOneCtaPages;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kScanCtas);
+  cfg.gridDim = dim3(one ? 1 : kScanCtas);
   cfg.blockDim = dim3(kScanThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -485,8 +528,9 @@ cudaError_t launch_compact_pages(const CompactArgs& a, const PagePools& p, cudaS
   attr[0].val.clusterDim.x = kScanCtas;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (const cudaError_t e = cudaLaunchKernelEx(&cfg, compact_plan_kernel, a)) return e;
+  cfg.numAttrs = one ? 0 : 1;
+  auto* plan = one ? compact_plan_kernel<1> : compact_plan_kernel<kScanCtas>;
+  if (const cudaError_t e = cudaLaunchKernelEx(&cfg, plan, a)) return e;
   compact_move_kernel<<<device_sm_count() * 8, kMoveThreads, 0, s>>>(a, p);
   return cudaGetLastError();
 }
