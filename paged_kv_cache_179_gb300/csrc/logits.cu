@@ -4,10 +4,12 @@
 //   x = logit; seen: x > 0 ? x / r : x r; x -= f c + p (c > 0); x += bias; masked: -inf
 //   out = x, or exp((x - max) / T) / sum
 //
-// One cluster of CTAs holds the rows of a sequence (or one row), each CTA an equal
-// slice of the vocabulary: its counts of the sequence's history in shared memory
-// (one word a token: the output's count, and whether the prompt or a bias has it),
-// a row's logits in registers, 32 a thread.  So a row is read once and written
+// One cluster of CTAs holds the rows of a sequence (or one row), its CTAs taking the
+// vocabulary's blocks of 128 tokens in turn (the tokens that text repeats are low ones: a
+// contiguous share of them would be one CTA's, and the others would wait): their
+// counts of the sequence's history in shared memory (one word a token: the output's
+// count, and whether the prompt or a bias has it), a row's logits in registers, 32 a
+// thread.  So a row is read once and written
 // once; only two words a CTA cross the cluster, each CTA's maximum and the sum of
 // its exponentials relative to it.  The row after the first of a sequence adds one
 // draft to the counts.
@@ -79,10 +81,16 @@ logits_kernel(const LogitsArgs a, int slice, int rows_per_unit) {
   const int unit = blockIdx.x / C;
   const int b = unit / units, i0 = (unit - b * units) * rows_per_unit;
   const int i1 = min(i0 + rows_per_unit, a.rows);
-  const int lo = min(rank * slice, a.V), n = min(slice, a.V - lo);   // this CTA's tokens
+  // this CTA's element e is token ((e / 128) C + rank) 128 + e % 128 (C a power of two)
+  const int shift = __ffs(C) - 1;
+  auto token = [&](int e) { return ((((e >> 7) << shift) + rank) << 7) + (e & 127); };
+  // the element of a token, or -1: another CTA's (or padding)
+  auto element_of = [&](int t) {
+    return t >= 0 && ((t >> 7) & (C - 1)) == rank ? ((t >> (7 + shift)) << 7) + (t & 127) : -1;
+  };
   if (PROBS) cluster_arrive();                     // (this CTA has started)
   // ---- the history's counts in this slice
-  for (int j = tid; j < (n + 3) / 4; j += THREADS)
+  for (int j = tid; j < slice / 4; j += THREADS)
     reinterpret_cast<uint4*>(seen)[j] = make_uint4(0u, 0u, 0u, 0u);
   if (tid == 0) n_bias = 0;
   __syncthreads();
@@ -91,8 +99,8 @@ logits_kernel(const LogitsArgs a, int slice, int rows_per_unit) {
       if (rank == 0) atomicOr(a.status, kStatusBadToken);
       return;
     }
-    const int e = t - lo;
-    if (e < 0 || e >= n) return;                   // (padding is below lo too)
+    const int e = element_of(t);
+    if (e < 0) return;
     if (prompt) atomicOr(seen + e, kInPrompt);
     else atomicAdd(seen + e, 1u);
   };
@@ -115,19 +123,20 @@ logits_kernel(const LogitsArgs a, int slice, int rows_per_unit) {
       const bool in = j < sp.num_bias;
       const int t = in ? sp.bias_tokens[static_cast<int64_t>(b) * sp.num_bias + j] : -1;
       if (t >= a.V && rank == 0) atomicOr(a.status, kStatusBadToken);
-      const bool ours = t >= lo && t < lo + n;
+      const int e = t < a.V ? element_of(t) : -1;
+      const bool ours = e >= 0;
       const unsigned m = __ballot_sync(0xffffffffu, ours);
       if (ours) {
         const int at = kept + __popc(m & ((1u << lane) - 1u));
-        bias_t[at] = t - lo;
+        bias_t[at] = e;
         bias_v[at] = sp.bias_values[static_cast<int64_t>(b) * sp.num_bias + j];
-        atomicOr(seen + (t - lo), kHasBias);
+        atomicOr(seen + e, kHasBias);
       }
       kept += __popc(m);
     }
     if (lane == 0) n_bias = kept;
   }
-  const float rep = sp.repetition != nullptr ? sp.repetition[b] : 1.f;
+  const float rep = sp.repetition != nullptr ? sp.repetition[b] : 1.f, inv_rep = 1.f / rep;
   const float freq = sp.frequency != nullptr ? sp.frequency[b] : 0.f;
   const float pres = sp.presence != nullptr ? sp.presence[b] : 0.f;
   const float temp = sp.temperature != nullptr ? sp.temperature[b] : 1.f;
@@ -144,16 +153,16 @@ logits_kernel(const LogitsArgs a, int slice, int rows_per_unit) {
       __syncthreads();
     }
     const int64_t row = static_cast<int64_t>(b) * a.rows + i;
-    const T* in = static_cast<const T*>(a.logits) + row * a.in_stride + lo;
-    O* out = static_cast<O*>(a.out) + row * a.out_stride + lo;
+    const T* in = static_cast<const T*>(a.logits) + row * a.in_stride;
+    O* out = static_cast<O*>(a.out) + row * a.out_stride;
     const uint32_t* allowed = sp.allowed != nullptr ? sp.allowed + row * sp.allowed_stride : nullptr;
     float x[kPer];
 #pragma unroll
     for (int k = 0; k < kSteps; ++k) {
       if constexpr (WIDE) {
-        const int e = element<WIDE, THREADS>(k, 0, tid);
-        if (e + kVec <= n) {
-          const Pack<T> p = *reinterpret_cast<const Pack<T>*>(in + e);
+        const int t = token(element<WIDE, THREADS>(k, 0, tid));
+        if (t + kVec <= a.V) {
+          const Pack<T> p = *reinterpret_cast<const Pack<T>*>(in + t);
 #pragma unroll
           for (int j = 0; j < kVec; ++j) x[k * kVec + j] = to_f32(p.v[j]);
           continue;
@@ -161,13 +170,17 @@ logits_kernel(const LogitsArgs a, int slice, int rows_per_unit) {
       }
 #pragma unroll
       for (int j = 0; j < kVec; ++j) {
-        const int e = element<WIDE, THREADS>(k, j, tid);
-        x[k * kVec + j] = e < n ? to_f32(in[e]) : -INFINITY;
+        const int t = token(element<WIDE, THREADS>(k, j, tid));
+        x[k * kVec + j] = t < a.V ? to_f32(in[t]) : -INFINITY;
       }
     }
     auto adjust = [&](int e, unsigned w, float v) {   // a token that something is known of
       const unsigned count = w & kCount;
-      if (count != 0u || (w & kInPrompt)) v = v > 0.f ? v / rep : v * rep;
+      if (count != 0u || (w & kInPrompt)) {
+        // the quotient by the reciprocal, corrected by its remainder
+        const float q = v * inv_rep;
+        v = v > 0.f ? (v < INFINITY ? fmaf(fmaf(-q, rep, v), inv_rep, q) : v / rep) : v * rep;
+      }
       if (count != 0u) v -= fmaf(freq, static_cast<float>(count), pres);
       if (w & kHasBias) {
         float s = 0.f;
@@ -181,10 +194,10 @@ logits_kernel(const LogitsArgs a, int slice, int rows_per_unit) {
     for (int k = 0; k < kSteps; ++k) {
       if constexpr (WIDE) {
         const int e = element<WIDE, THREADS>(k, 0, tid);
-        if (e >= n) continue;
-        // (slices are multiples of 32 tokens: four tokens share a word of the mask)
+        const int t = token(e);
+        if (t >= a.V) continue;
         const uint4 w = *reinterpret_cast<const uint4*>(seen + e);
-        const unsigned ok = allowed != nullptr ? allowed[(lo + e) >> 5] >> (e & 31) : ~0u;
+        const unsigned ok = allowed != nullptr ? allowed[t >> 5] >> (t & 31) : ~0u;
         if ((w.x | w.y | w.z | w.w) != 0u) {
           if (w.x != 0u) x[k * kVec] = adjust(e, w.x, x[k * kVec]);
           if (w.y != 0u) x[k * kVec + 1] = adjust(e + 1, w.y, x[k * kVec + 1]);
@@ -198,10 +211,11 @@ logits_kernel(const LogitsArgs a, int slice, int rows_per_unit) {
 #pragma unroll
         for (int j = 0; j < kVec; ++j) {
           const int e = element<WIDE, THREADS>(k, j, tid), q = k * kVec + j;
-          if (e >= n) continue;
+          const int t = token(e);
+          if (t >= a.V) continue;
           const unsigned w = seen[e];
           if (w != 0u) x[q] = adjust(e, w, x[q]);
-          if (allowed != nullptr && !((allowed[(lo + e) >> 5] >> (e & 31)) & 1u)) x[q] = -INFINITY;
+          if (allowed != nullptr && !((allowed[t >> 5] >> (t & 31)) & 1u)) x[q] = -INFINITY;
         }
       }
     }
@@ -223,7 +237,7 @@ logits_kernel(const LogitsArgs a, int slice, int rows_per_unit) {
 #pragma unroll
         for (int q = 0; q < kPer; ++q)
           if (x[q] == m && m > -INFINITY)
-            best = min(best, static_cast<unsigned>(lo + element<WIDE, THREADS>(q / kVec, q % kVec, tid)));
+            best = min(best, static_cast<unsigned>(token(element<WIDE, THREADS>(q / kVec, q % kVec, tid))));
         best = __reduce_min_sync(0xffffffffu, best);
       } else {
 #pragma unroll
@@ -264,7 +278,7 @@ logits_kernel(const LogitsArgs a, int slice, int rows_per_unit) {
           if (box_m[set][r] == M) best = min(best, box_i[set][r]);
 #pragma unroll
         for (int q = 0; q < kPer; ++q)
-          x[q] = static_cast<unsigned>(lo + element<WIDE, THREADS>(q / kVec, q % kVec, tid)) == best ? 1.f : 0.f;
+          x[q] = static_cast<unsigned>(token(element<WIDE, THREADS>(q / kVec, q % kVec, tid))) == best ? 1.f : 0.f;
       } else {
         auto factor = [&](float mr) {              // 2^(c (mr - M)); all of them -inf: 0
           return mr == M ? (M > -INFINITY ? 1.f : 0.f) : fast_exp2((mr - M) * c);
@@ -278,19 +292,19 @@ logits_kernel(const LogitsArgs a, int slice, int rows_per_unit) {
 #pragma unroll
     for (int k = 0; k < kSteps; ++k) {
       if constexpr (WIDE) {
-        const int e = element<WIDE, THREADS>(k, 0, tid);
-        if (e + kVec <= n) {
+        const int t = token(element<WIDE, THREADS>(k, 0, tid));
+        if (t + kVec <= a.V) {
           Pack<O> p;
 #pragma unroll
           for (int j = 0; j < kVec; ++j) from_f32(x[k * kVec + j], &p.v[j]);
-          *reinterpret_cast<Pack<O>*>(out + e) = p;
+          *reinterpret_cast<Pack<O>*>(out + t) = p;
           continue;
         }
       }
 #pragma unroll
       for (int j = 0; j < kVec; ++j) {
-        const int e = element<WIDE, THREADS>(k, j, tid);
-        if (e < n) from_f32(x[k * kVec + j], out + e);
+        const int t = token(element<WIDE, THREADS>(k, j, tid));
+        if (t < a.V) from_f32(x[k * kVec + j], out + t);
       }
     }
   }
@@ -325,8 +339,11 @@ cudaError_t launch_type(const LogitsArgs& a, bool probs, cudaStream_t s) {
   const bool wide = (a.in_stride % kVec) == 0 && (a.out_stride % kVec) == 0 &&
                     reinterpret_cast<uintptr_t>(a.out) % (out_size * kVec) == 0;
   int C = 1;
-  while (C < kMaxCluster && (a.V > C * 512 * kPer || static_cast<int64_t>(a.B) * a.rows * C < 152)) C *= 2;
-  const int slice = ((a.V + C - 1) / C + 31) / 32 * 32;
+  const int blocks = (a.V + 127) / 128;
+  while (C < kMaxCluster &&
+         (blocks > C * (512 * kPer / 128) || (C < blocks && static_cast<int64_t>(a.B) * a.rows * C < 152)))
+    C *= 2;
+  const int slice = (blocks + C - 1) / C * 128;
   const bool big = slice > 512 * kPer;
   const int per_unit = static_cast<int64_t>(a.B) * C >= 608 ? a.rows : 1;
   if (big) {

@@ -21,6 +21,26 @@
 namespace pa {
 namespace {
 
+// These calls are short and follow one another: each kernel is launched while the one before
+// it on the stream still runs, and waits for its end before it touches memory.
+cudaLaunchAttribute after_previous() {
+  cudaLaunchAttribute a{};
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  return a;
+}
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kern)(P...), unsigned grid, unsigned threads, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1] = {after_previous()};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 constexpr int kScanThreads = 1024;
 constexpr int kScanWarps = kScanThreads / 32;
 constexpr int kScanCtas = 8;                       // a portable cluster, for larger pools
@@ -131,6 +151,10 @@ __device__ __forceinline__ unsigned warp_prefix(unsigned v, int lane) {   // exc
 }
 
 // ---------------------------------------------------------------------- taking
+// The free pages that a call takes are the lowest ones, a small part of the pool: the
+// warps take chunks of the pages in turn, so that all of them have some of it.
+constexpr int kMaxChunks = 4096;
+constexpr int kChunkGroups = 128;                  // groups of four pages: 512 pages, or more in large pools
 // What item i needs: pages (-1: it is passed over), in which row, from which
 // entry of its table on, and how many the row holds with them.
 struct Need {
@@ -176,15 +200,30 @@ __global__ void __launch_bounds__(kScanThreads, 1) take_kernel(const TakeArgs a)
   // [items + 1]: needs before each item; then, of up to kKeptItems, the place in the tables
   // of the page of rank 0 of each item (-1: passed over)
   extern __shared__ __align__(16) int first[];
-  __shared__ unsigned mine[kScanWarps], box[kScanCtas], sums[kScanWarps];
+  __shared__ unsigned before[kMaxChunks + 1];      // free pages in, then before, each chunk
+  __shared__ unsigned sums[2][kScanWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = CTAS > 1 ? cluster_rank() : 0u;
-  if (CTAS > 1) cluster_arrive();                  // (this CTA has started)
+  griddep_launch_dependents();
+  griddep_wait();
+  if (CTAS > 1) cluster_sync();                    // all CTAs have started
   const bool kept = a.items <= kKeptItems;
   int64_t* place = reinterpret_cast<int64_t*>(first + (a.items + 4) / 4 * 4);
-  // ---- the free pages of this warp's part
-  const Part part = my_part<CTAS>(a.num_blocks, rank, warp);
-  const unsigned n_free = count_part(a.ref_counts, a.num_blocks, 1, part.g0, part.g1, lane, free_bits);
+  // ---- the free pages of each chunk
+  const int groups = (a.num_blocks + 3) / 4;
+  const int per_chunk = max(kChunkGroups, ((groups + kMaxChunks - 1) / kMaxChunks + 31) / 32 * 32);
+  const int chunks = (groups + per_chunk - 1) / per_chunk;
+  constexpr int kWarpsInAll = CTAS * kScanWarps;
+  const int me = warp * CTAS + static_cast<int>(rank);
+  for (int k = me; k < chunks; k += kWarpsInAll) {
+    const int g0 = k * per_chunk;
+    const unsigned n = count_part(a.ref_counts, a.num_blocks, 1, g0, min(g0 + per_chunk, groups), lane, free_bits);
+    if (CTAS == 1) {
+      if (lane == 0) before[k] = n;
+    } else if (lane < CTAS) {
+      st_cluster_u32(before + k, lane, n);
+    }
+  }
   // ---- the needs and their prefix sums, by every CTA for itself
   const int per = (a.items + kScanThreads - 1) / kScanThreads;
   const int i0 = min(a.items, tid * per), i1 = min(a.items, i0 + per);
@@ -196,24 +235,49 @@ __global__ void __launch_bounds__(kScanThreads, 1) take_kernel(const TakeArgs a)
     if (kept) place[i] = n.pages < 0 ? -1 : place_of(n);
     sum = min(sum + first[i], kMany);
   }
-  unsigned inc = sum;
+  if (CTAS > 1) cluster_sync();
+  else __syncthreads();
+  // ---- both prefix sums: a thread's share first
+  constexpr int kMine = kMaxChunks / kScanThreads;
+  unsigned free_n = 0;
+#pragma unroll
+  for (int j = 0; j < kMine; ++j) free_n += tid * kMine + j < chunks ? before[tid * kMine + j] : 0u;
+  unsigned inc = sum, inc_free = free_n;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const unsigned t = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc = min(inc + t, kMany);
+    const unsigned t = __shfl_up_sync(0xffffffffu, inc, o), u = __shfl_up_sync(0xffffffffu, inc_free, o);
+    if (lane >= o) {
+      inc = min(inc + t, kMany);
+      inc_free += u;
+    }
   }
-  if (lane == 31) sums[warp] = inc;
+  if (lane == 31) {
+    sums[0][warp] = inc;
+    sums[1][warp] = inc_free;
+  }
   const unsigned up = __shfl_up_sync(0xffffffffu, inc, 1);
-  if (CTAS > 1) cluster_wait();
-  const Before at = cluster_prefix<CTAS>(n_free, mine, box, warp, lane, rank);   // (syncs: sums are there)
-  unsigned ex = lane > 0 ? up : 0u;
-  for (int w = 0; w < warp; ++w) ex = min(ex + sums[w], kMany);
+  __syncthreads();
+  unsigned ex = lane > 0 ? up : 0u, ex_free = inc_free - free_n, total = 0;
+  for (int w = 0; w < kScanWarps; ++w) {
+    if (w < warp) {
+      ex = min(ex + sums[0][w], kMany);
+      ex_free += sums[1][w];
+    }
+    total += sums[1][w];
+  }
   for (int i = i0; i < i1; ++i) {
     const unsigned pages = first[i];
     first[i] = ex;
     ex = min(ex + pages, kMany);
   }
   if (tid == kScanThreads - 1) first[a.items] = ex;
+#pragma unroll
+  for (int j = 0; j < kMine; ++j)
+    if (tid * kMine + j < chunks) {
+      const unsigned n = before[tid * kMine + j];
+      before[tid * kMine + j] = ex_free;
+      ex_free += n;
+    }
   __syncthreads();
   // ---- items are granted while their last page's rank is there
   auto last_at_most = [&](int v) {                 // the last j with first[j] <= v
@@ -225,28 +289,32 @@ __global__ void __launch_bounds__(kScanThreads, 1) take_kernel(const TakeArgs a)
     }
     return l;
   };
-  const unsigned limit = first[last_at_most(static_cast<int>(at.total))];
-  unsigned k0 = at.before;
-  auto counts = [&](int g) {
-    return g + lane < part.g1 ? counts_at(a.ref_counts, g + lane, a.num_blocks, 1) : make_int4(1, 1, 1, 1);
-  };
-  int4 c = part.g0 < part.g1 ? counts(part.g0) : make_int4(1, 1, 1, 1);
-  for (int g = part.g0; g < part.g1 && k0 < limit; g += 32) {
-    unsigned bits = free_bits(c);
-    if (g + 32 < part.g1) c = counts(g + 32);      // on their way
-    const unsigned mine_n = __popc(bits);
-    unsigned k = k0 + warp_prefix(mine_n, lane);
-    if (bits != 0u && k < limit) {
-      int i = last_at_most(static_cast<int>(k));   // this lane's pages have ranks k, k + 1, ..
-      for (; bits != 0u && k < limit; bits &= bits - 1, ++k) {
-        while (first[i + 1] <= static_cast<int>(k)) ++i;
-        const int page = 4 * (g + lane) + __ffs(bits) - 1;
-        const int64_t to = kept ? place[i] : place_of(need_of<FORK>(a, i, false));
-        a.block_tables[to + (k - first[i])] = page;
-        a.ref_counts[page] = 1;
+  const unsigned limit = first[last_at_most(static_cast<int>(total))];
+  for (int chunk = me; chunk < chunks; chunk += kWarpsInAll) {
+    unsigned k0 = before[chunk];
+    const int g1 = min((chunk + 1) * per_chunk, groups);
+    auto counts = [&](int g) {
+      return g + lane < g1 ? counts_at(a.ref_counts, g + lane, a.num_blocks, 1) : make_int4(1, 1, 1, 1);
+    };
+    if (k0 >= limit) break;                        // (so do those behind)
+    int4 c = counts(chunk * per_chunk);
+    for (int g = chunk * per_chunk; g < g1 && k0 < limit; g += 32) {
+      unsigned bits = free_bits(c);
+      if (g + 32 < g1) c = counts(g + 32);         // on their way
+      const unsigned mine_n = __popc(bits);
+      unsigned k = k0 + warp_prefix(mine_n, lane);
+      if (bits != 0u && k < limit) {
+        int i = last_at_most(static_cast<int>(k));   // this lane's pages have ranks k, k + 1, ..
+        for (; bits != 0u && k < limit; bits &= bits - 1, ++k) {
+          while (first[i + 1] <= static_cast<int>(k)) ++i;
+          const int page = 4 * (g + lane) + __ffs(bits) - 1;
+          const int64_t to = kept ? place[i] : place_of(need_of<FORK>(a, i, false));
+          a.block_tables[to + (k - first[i])] = page;
+          a.ref_counts[page] = 1;
+        }
       }
+      k0 += warp_sum(mine_n);
     }
-    k0 += warp_sum(mine_n);
   }
   // ---- what the items hold now, once no CTA reads num_pages any more
   if (CTAS > 1) cluster_sync();
@@ -256,7 +324,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) take_kernel(const TakeArgs a)
     // (a kept item's need is the difference of the prefix sums, unless those have saturated,
     // and then it is not granted)
     const bool passed_over = kept ? place[i] < 0 : need_of<FORK>(a, i, false).pages < 0;
-    const bool ok = !passed_over && static_cast<unsigned>(first[i + 1]) <= at.total;
+    const bool ok = !passed_over && static_cast<unsigned>(first[i + 1]) <= total;
     if (!FORK && ok) a.num_pages[a.rows[i]] = need_of<FORK>(a, i, false).holds;
     a.granted[i] = ok;
   }
@@ -267,7 +335,7 @@ cudaError_t launch_take(const TakeArgs& a, cudaStream_t s) {
   auto* kern = take_kernel<FORK, CTAS>;
   const size_t smem = (static_cast<size_t>(a.items) + 4) / 4 * 16 +
                       (a.items <= kKeptItems ? static_cast<size_t>(a.items) * 8 : 0);
-  if (smem > 47 * 1024) {                          // (the default limit is 48 KB with the static arrays)
+  if (smem > 30 * 1024) {                          // (the default limit is 48 KB with the static arrays)
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (kPagesMaxItems + 4) * 4);
     if (e != cudaSuccess) return e;
@@ -277,12 +345,13 @@ cudaError_t launch_take(const TakeArgs& a, cudaStream_t s) {
   cfg.blockDim = dim3(kScanThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = CTAS;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0] = after_previous();
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CTAS;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = CTAS > 1 ? 1 : 0;
+  cfg.numAttrs = CTAS > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, a);
 }
 template <bool FORK>
@@ -297,6 +366,8 @@ __global__ void __launch_bounds__(kFreeThreads)
 free_kernel(int32_t* tables, int mbs, int32_t* num_pages, int num_rows, const int32_t* rows,
             int32_t* ref, int num_blocks, unsigned* status) {
   __shared__ int held;
+  griddep_launch_dependents();
+  griddep_wait();
   const int row = rows[blockIdx.x];
   if (row < 0 || row >= num_rows) {
     if (threadIdx.x == 0) atomicOr(status, kStatusBadRow);
@@ -352,6 +423,8 @@ constexpr int kForkThreads = 256;
 // counts, then the copy.
 __global__ void __launch_bounds__(kForkThreads)
 fork_kernel(const TakeArgs a, int32_t* context_lens, const PagePools p) {
+  griddep_launch_dependents();
+  griddep_wait();
   const int i = blockIdx.x;
   if (!a.granted[i]) return;
   const int src = a.src_rows[i], dst = a.rows[i], L = context_lens[src];
@@ -403,6 +476,8 @@ __host__ __device__ inline CompactSpace compact_space(void* ws, int num_blocks) 
 template <int CTAS>
 __global__ void __launch_bounds__(kScanThreads, 1) compact_plan_kernel(const CompactArgs a) {
   __shared__ unsigned mine[kScanWarps], box[2][kScanCtas];
+  griddep_launch_dependents();
+  griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CTAS > 1 ? cluster_rank() : 0u;
   if (CTAS > 1) cluster_arrive();                  // (this CTA has started)
@@ -462,6 +537,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) compact_plan_kernel(const Com
 constexpr int kMoveThreads = 256;
 __global__ void __launch_bounds__(kMoveThreads)
 compact_move_kernel(const CompactArgs a, const PagePools p) {
+  griddep_wait();
   const CompactSpace ws = compact_space(a.workspace, a.num_blocks);
   const int moves = *ws.moves, live = *a.num_live;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -501,16 +577,14 @@ cudaError_t launch_alloc_pages(const TakeArgs& a, cudaStream_t s) { return launc
 cudaError_t launch_free_pages(int32_t* tables, int mbs, int32_t* num_pages, int num_rows,
                               const int32_t* rows, int items, int32_t* ref_counts, int num_blocks,
                               unsigned* status, cudaStream_t s) {
-  free_kernel<<<items, kFreeThreads, 0, s>>>(tables, mbs, num_pages, num_rows, rows, ref_counts,
-                                             num_blocks, status);
-  return cudaGetLastError();
+  return launch_after(free_kernel, static_cast<unsigned>(items), kFreeThreads, s, tables, mbs, num_pages,
+                      num_rows, rows, ref_counts, num_blocks, status);
 }
 
 cudaError_t launch_fork_pages(const TakeArgs& a, int32_t* context_lens, const PagePools& p,
                               cudaStream_t s) {
   if (const cudaError_t e = launch_take<true>(a, s)) return e;
-  fork_kernel<<<a.items, kForkThreads, 0, s>>>(a, context_lens, p);
-  return cudaGetLastError();
+  return launch_after(fork_kernel, static_cast<unsigned>(a.items), kForkThreads, s, a, context_lens, p);
 }
 
 size_t compact_workspace_bytes(int num_blocks) {
@@ -523,16 +597,16 @@ cudaError_t launch_compact_pages(const CompactArgs& a, const PagePools& p, cudaS
   cfg.gridDim = dim3(one ? 1 : kScanCtas);
   cfg.blockDim = dim3(kScanThreads);
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kScanCtas;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0] = after_previous();
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kScanCtas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = one ? 0 : 1;
+  cfg.numAttrs = one ? 1 : 2;
   auto* plan = one ? compact_plan_kernel<1> : compact_plan_kernel<kScanCtas>;
   if (const cudaError_t e = cudaLaunchKernelEx(&cfg, plan, a)) return e;
-  compact_move_kernel<<<device_sm_count() * 8, kMoveThreads, 0, s>>>(a, p);
-  return cudaGetLastError();
+  return launch_after(compact_move_kernel, static_cast<unsigned>(device_sm_count()) * 8, kMoveThreads, s, a, p);
 }
 
 }  // namespace pa
