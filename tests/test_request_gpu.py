@@ -123,6 +123,12 @@ PROMPTS = [  # lens, news, Hq, Hkv, D, dtype, fp8, window
     ([130, 513], [130, 200], 5, 5, 128, F16, True, 0),
     ([900, 1200], [128, 300], 7, 1, 128, BF16, True, 300),
     ([2100, 1], [6, 1], 8, 2, 64, BF16, True, 0),
+    ([1500], [1500], 7, 1, 128, BF16, False, 0),        # whole tiles, cut items
+    ([1400, 1300], [1, 1300], 3, 1, 64, F16, False, 0),
+    ([1700], [900], 10, 2, 128, F16, True, 0),
+    ([1600], [700], 4, 1, 64, BF16, True, 1000),        # a window over whole tiles
+    ([1999], [1300], 5, 1, 128, F16, False, 777),
+    ([129] * 40, [2] * 40, 12, 12, 64, F16, False, 0),
 ]
 
 
@@ -210,6 +216,49 @@ def test_prefill_large_logits_and_scales():
         out = p.run()
         ok()
         p.check(out)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_prefill_weights_that_outgrow_their_offset(fp8, dtype):
+    """Scores that rise by hundreds in the middle of a long context, in the first half of a
+    tile and in the second, after the offset has stood for many tiles; and one key that
+    outweighs all others by more than the products' range."""
+    for at in (700, 780, 1155):
+        p = Prompts([1300], [100], 4, 2, 128, dtype, fp8)
+        for page in range(at // 16, 81):
+            k = p.kc[int(p.tables[0, page])]
+            if fp8:
+                p.ks[int(p.tables[0, page])] *= 40
+            else:
+                k *= 40
+        out = p.run()
+        ok()
+        p.check(out)
+    p = Prompts([1300], [100], 2, 1, 64, dtype, fp8)
+    if fp8:
+        p.ks[int(p.tables[0, 50])] *= 300
+    else:
+        p.kc[int(p.tables[0, 50]), 0, 5] *= 300
+    out = p.run()
+    ok()
+    p.check(out)
+
+
+def test_prefill_not_finite_in_long_contexts():
+    """A key or value that is not a number, far from any edge: the queries get what the
+    definition says, nothing hangs and other sequences do not notice."""
+    for where, value in (("k", float("nan")), ("k", float("inf")), ("v", float("inf"))):
+        p = Prompts([1300, 200], [60, 50], 4, 2, 128, F16)
+        clean = Prompts([1300, 200], [60, 50], 4, 2, 128, F16)
+        (p.kc if where == "k" else p.vc)[int(p.tables[0, 30]), 1, 3, 7] = value
+        got, want = R.f64(p.run()), R.f64(clean.run())
+        ok()
+        assert np.array_equal(got[60:], want[60:]) and np.array_equal(got[:60, :2], want[:60, :2])
+        if where == "v":
+            assert not np.isfinite(got[:60, 2:, 7]).any()
+        elif value != value:
+            assert np.isnan(got[:60, 2:]).all()
 
 
 def test_prefill_page_scales_far_apart():
@@ -719,6 +768,10 @@ LOGITS = [  # B, n, V, H, bias, mask, dtype
     (1, 1, 300001, 50, 20, True, BF16),
     (1, 0, 1 << 19, 400, 0, False, F16),
     (700, 2, 1000, 30, 2, False, F16),
+    (160, 0, 4, 9, 3, True, F32),             # rows for all SMs, the shortest that is read by fours
+    (155, 0, 12344, 900, 40, True, BF16),
+    (40, 3, 33000, 5000, 1024, True, F32),    # nearly as many known tokens as the table takes
+    (152, 0, 2000, 6000, 200, False, F16),    # more than it takes
 ]
 
 
@@ -767,6 +820,46 @@ def test_logits_in_place_padded_rows_and_two_dims():
         assert bool((out[:, V:] == 7).all())
 
 
+def test_logits_of_many_rows_padded_and_in_place():
+    """Rows for all SMs, of a length that is no multiple of four, apart from one another."""
+    g = gen(16)
+    V, B = 1003, 200
+    base = (torch.randn(B, V + 5, generator=g) * 2).to(BF16)
+    spec = logits_case(g, B, 0, V, 60, 9, True)
+    out = torch.full((B, V + 1), 7., device="cuda")
+    run_logits(base.cuda()[:, :V], spec, True, out=out[:, :V])
+    check_logits(base[:, :V], spec, True, out[:, :V])
+    assert bool((out[:, V:] == 7).all())
+    dev = base.cuda()
+    run_logits(dev[:, :V], spec, False, out=dev[:, :V])
+    ok()
+    check_logits(base[:, :V], spec, False, dev[:, :V])
+    assert torch.equal(dev[:, V:].cpu(), base[:, V:])
+    x = torch.randn(B, V + 1, generator=g)                        # fp32 logits to their own place
+    dev = x.cuda()
+    run_logits(dev, logits_case(g, B, 0, V + 1, parts=()), True, out=dev)
+    ok()
+    assert float((dev.cpu() - x.softmax(-1)).abs().max()) <= 1e-6
+
+
+@pytest.mark.parametrize("rows", [6, 160])
+def test_logits_bad_tokens_and_lengths_of_few_and_many_rows(rows):
+    g = gen(17)
+    x = torch.randn(rows, 2, 400, generator=g)
+    spec = logits_case(g, rows, 1, 400, 30, 6)
+    spec["history_lens"][:] = 30
+    spec["history"][3, 7], spec["bias_tokens"][5, 2] = 400, 2 ** 31 - 1
+    spec["draft_tokens"][2, 0] = 4000
+    out = run_logits(x, spec, True)
+    status(_abi.PA_STATUS_BAD_TOKEN)
+    check_logits(x, spec, True, out)
+    spec = logits_case(g, rows, 1, 400, 30, 6)
+    spec["history_lens"][1], spec["history_lens"][4] = -1, 31
+    out = run_logits(x, spec, False)
+    status(_abi.PA_STATUS_BAD_LEN)
+    check_logits(x, spec, False, out)
+
+
 def test_logits_padding_and_bad_tokens():
     g = gen(7)
     x = torch.randn(2, 3, 100, generator=g)
@@ -796,7 +889,9 @@ def test_logits_padding_and_bad_tokens():
     check_logits(x, spec, False, out)
 
 
-def test_logits_not_finite():
+@pytest.mark.parametrize("copies", [1, 40])
+def test_logits_not_finite(copies):
+    """Few rows, and enough that each is a CTA's."""
     x = torch.randn(6, 300, generator=gen(1))
     inf, nan = float("inf"), float("nan")
     x[0, 5] = x[0, 270] = inf                        # they share the row
@@ -805,12 +900,14 @@ def test_logits_not_finite():
     x[3, :] = nan
     x[4, 7] = -inf
     x[5, 9] = inf
-    spec = logits_case(gen(2), 6, 0, 300, parts=())
+    spec = logits_case(gen(2), 6 * copies, 0, 300, parts=())
+    many = x.repeat(copies, 1)
     for temp in (None, .5, 0., 1e-38, inf, 1e38, nan):
-        spec["temperature"] = None if temp is None else torch.full((6,), temp)
-        out = run_logits(x, spec, True).cpu()
+        spec["temperature"] = None if temp is None else torch.full((6 * copies,), temp)
+        out = run_logits(many, spec, True).cpu()
         ok()
         assert not torch.isnan(out).any()
+        assert torch.equal(out, out[:6].repeat(copies, 1))
         if temp in (0., 1e-38) or temp != temp:
             best = torch.nan_to_num(x, nan=-inf, posinf=inf, neginf=-inf).argmax(-1)
             for r in (2, 4, 5):
@@ -820,18 +917,23 @@ def test_logits_not_finite():
             assert out[0, 5] == out[0, 270] == .5 and out[0].sum() == 1
             check_logits(x[2:3], {k: None if v is None else v[2:3] for k, v in spec.items()}, True, out[2:3])
         assert out[1].sum() == 0 and out[3].sum() == 0 and out[2, 3] == 0 and out[4, 7] == 0
-    assert torch.equal(torch.nan_to_num(run_logits(x, spec, False).cpu(), nan=3.25), torch.nan_to_num(x, nan=3.25))
+    got = run_logits(many, spec, False).cpu()
+    assert torch.equal(torch.nan_to_num(got, nan=3.25), torch.nan_to_num(many, nan=3.25))
 
 
-def test_logits_ties_go_to_the_lowest_token():
+@pytest.mark.parametrize("copies", [1, 60])
+def test_logits_ties_go_to_the_lowest_token(copies):
     x = torch.zeros(3, 1, 70000, dtype=BF16)
     x[1, 0, 60001:] = 2
     x[2, 0, [69999, 17, 30000]] = 5
-    spec = logits_case(gen(2), 3, 0, 70000, parts=())
-    spec["temperature"] = torch.zeros(3)
-    out = run_logits(x, spec, True)
+    spec = logits_case(gen(2), 3 * copies, 0, 70000, parts=())
+    spec["temperature"] = torch.zeros(3 * copies)
+    spec["bias_tokens"] = torch.full((3 * copies, 1), 60001, dtype=torch.int32)   # a known token among them
+    spec["bias_values"] = torch.zeros(3 * copies, 1)
+    out = run_logits(x.repeat(copies, 1, 1), spec, True)
     ok()
-    assert out.argmax(-1).flatten().tolist() == [0, 60001, 17] and out.sum(-1).flatten().tolist() == [1, 1, 1]
+    assert out.argmax(-1).flatten().tolist() == [0, 60001, 17] * copies
+    assert out.sum(-1).flatten().tolist() == [1, 1, 1] * copies
 
 
 def test_logits_captured_and_on_another_stream():
