@@ -20,6 +20,14 @@
 // row streams past them, twice for probabilities (the second time from L2).  Nothing
 // waits for other CTAs then.
 //
+// Bound by memory where there are many rows, by latency where there are few.  Measured on a
+// GB300, rows of 128000 bf16 logits to fp32 probabilities: 512 rows with histories of 300
+// tokens 146 us (2.7 TB/s of the logits read once and the probabilities written), of 4096
+// tokens 184 us: the histories' insertion, and two rounds of two CTAs an SM, are what
+// separates them from the 58 us of a copy of those bytes.  The cluster form takes 212 and
+// 248 us there.  At 152 rows: 60 against 81 us, 78 against 95 with the long histories.
+// One row of 32000 fp32 logits: 6 us.
+//
 // Counts are integers, and a token's biases are added in their order, so results
 // do not depend on the order of execution.
 #include <type_traits>
@@ -36,9 +44,7 @@
 namespace pa {
 namespace {
 
-// Logits a thread holds: 16, in CTAs of 512 threads of which two are on an SM, or, where
-// a cluster of those does not hold the vocabulary, 32 in CTAs of 1024.
-constexpr int kPerSmall = 32, kPerLarge = 32;
+constexpr int kPer = 32;                           // logits a thread holds
 constexpr int kVec = 4;                            // consecutive ones, where rows are aligned
 constexpr int kMaxCluster = 16;
 constexpr unsigned kInPrompt = 1u << 31, kHasBias = 1u << 30, kCount = kHasBias - 1u;
@@ -71,9 +77,9 @@ struct Penalties {
                           int n_bias) const {
     const unsigned count = w & kCount;
     if (count != 0u || (w & kInPrompt)) {
-      // the quotient by the reciprocal, corrected by its remainder
+      // the quotient by the reciprocal, corrected by its remainder (where both are finite)
       const float q = v * inv_rep;
-      v = v > 0.f ? (v < INFINITY ? fmaf(fmaf(-q, rep, v), inv_rep, q) : v / rep) : v * rep;
+      v = v > 0.f ? (q < 1e37f ? fmaf(fmaf(-q, rep, v), inv_rep, q) : v / rep) : v * rep;
     }
     if (count != 0u) v -= fmaf(freq, static_cast<float>(count), pres);
     if (w & kHasBias) {
@@ -95,7 +101,7 @@ struct alignas(sizeof(T) * kVec) Pack {
   T v[kVec];
 };
 
-template <typename T, bool PROBS, bool WIDE, int THREADS, int kPer>
+template <typename T, bool PROBS, bool WIDE, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
 logits_kernel(const LogitsArgs a, int slice, int rows_per_unit) {
   using O = std::conditional_t<PROBS, float, T>;
@@ -452,6 +458,7 @@ stream_kernel(const LogitsArgs a, int log_slots) {
     vals[j] = __float_as_uint(x);
     if (PROBS) take(x, t);
   }
+  __syncthreads();                                 // (in place, the rest is written over them)
   // ---- the rest: kStreamSteps loads in flight, none of them behind a branch
   const int last = (a.V - kVec) & ~(kVec - 1);
   auto load = [&](int t0, Pack<T> (&raw)[kStreamSteps], unsigned (&bits)[kStreamSteps]) {
@@ -571,9 +578,9 @@ cudaError_t launch_stream(const LogitsArgs& a, int64_t known, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-template <typename T, bool PROBS, bool WIDE, int THREADS, int kPer>
+template <typename T, bool PROBS, bool WIDE, int THREADS>
 cudaError_t launch(const LogitsArgs& a, int C, int slice, int rows_per_unit, cudaStream_t s) {
-  auto* kern = logits_kernel<T, PROBS, WIDE, THREADS, kPer>;
+  auto* kern = logits_kernel<T, PROBS, WIDE, THREADS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        THREADS * kPer * 4);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
@@ -599,14 +606,15 @@ cudaError_t launch_type(const LogitsArgs& a, bool probs, cudaStream_t s) {
   // rows that begin at a multiple of kVec elements are read kVec at a time
   const bool wide = a.V >= kVec && (a.in_stride % kVec) == 0 && (a.out_stride % kVec) == 0 &&
                     reinterpret_cast<uintptr_t>(a.out) % (out_size * kVec) == 0;
-  // tokens that something may be known of in a row
+  // tokens that something may be known of in a row; from a row an SM on a CTA makes a row
+  // by itself (152 rows to logits: 31 us, by clusters 51)
   const int64_t known = (a.spec.history != nullptr ? a.spec.history_stride : 0) + a.spec.num_bias + a.rows;
   if (wide && static_cast<int64_t>(a.B) * a.rows >= 152 && known <= kStreamKnown)
     return probs ? launch_stream<T, true>(a, known, s) : launch_stream<T, false>(a, known, s);
   // as few CTAs a row as hold it, more where there are not enough rows for the SMs
   const int blocks = (a.V + 127) / 128;
-  const bool large = blocks > kMaxCluster * (512 * kPerSmall / 128);
-  const int most = (large ? 1024 * kPerLarge : 512 * kPerSmall) / 128;   // blocks a CTA
+  const bool large = blocks > kMaxCluster * (512 * kPer / 128);
+  const int most = (large ? 1024 : 512) * kPer / 128;   // blocks a CTA
   int C = 1;
   while (C < kMaxCluster &&
          (blocks > C * most || (C < blocks && static_cast<int64_t>(a.B) * a.rows * C < 152)))
@@ -615,15 +623,15 @@ cudaError_t launch_type(const LogitsArgs& a, bool probs, cudaStream_t s) {
   // a unit is a sequence's rows, whose counts differ by a draft each, or one row
   const int per_unit = static_cast<int64_t>(a.B) * C >= 608 ? a.rows : 1;
   if (large) {
-    if (probs) return wide ? launch<T, true, true, 1024, kPerLarge>(a, C, slice, per_unit, s)
-                           : launch<T, true, false, 1024, kPerLarge>(a, C, slice, per_unit, s);
-    return wide ? launch<T, false, true, 1024, kPerLarge>(a, C, slice, per_unit, s)
-                : launch<T, false, false, 1024, kPerLarge>(a, C, slice, per_unit, s);
+    if (probs) return wide ? launch<T, true, true, 1024>(a, C, slice, per_unit, s)
+                           : launch<T, true, false, 1024>(a, C, slice, per_unit, s);
+    return wide ? launch<T, false, true, 1024>(a, C, slice, per_unit, s)
+                : launch<T, false, false, 1024>(a, C, slice, per_unit, s);
   }
-  if (probs) return wide ? launch<T, true, true, 512, kPerSmall>(a, C, slice, per_unit, s)
-                         : launch<T, true, false, 512, kPerSmall>(a, C, slice, per_unit, s);
-  return wide ? launch<T, false, true, 512, kPerSmall>(a, C, slice, per_unit, s)
-              : launch<T, false, false, 512, kPerSmall>(a, C, slice, per_unit, s);
+  if (probs) return wide ? launch<T, true, true, 512>(a, C, slice, per_unit, s)
+                         : launch<T, true, false, 512>(a, C, slice, per_unit, s);
+  return wide ? launch<T, false, true, 512>(a, C, slice, per_unit, s)
+              : launch<T, false, false, 512>(a, C, slice, per_unit, s);
 }
 
 }  // namespace

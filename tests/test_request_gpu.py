@@ -936,6 +936,28 @@ def test_logits_ties_go_to_the_lowest_token(copies):
     assert out.sum(-1).flatten().tolist() == [1, 1, 1] * copies
 
 
+@pytest.mark.parametrize("B", [2, 200])
+def test_penalised_logits_of_any_magnitude(B):
+    """x / r for logits and penalties whose quotient leaves fp32's range, or whose
+    reciprocal does: within a step of the 64-bit quotient, inf where that is."""
+    x = torch.tensor([1e38, 3e38, 1e-38, 1., 7., float("inf"), 1e-30, 5e37], dtype=torch.float32)
+    logits = x.repeat(B, 1).cuda()
+    rep = torch.tensor([.1, 1e38, 3e-39, 1.3, 3e38, 1e-20, 2., .9], dtype=torch.float32).repeat((B + 7) // 8)[:B].cuda()
+    hist = torch.arange(8, dtype=torch.int32).repeat(B, 1).cuda()
+    lens = torch.full((B,), 8, dtype=torch.int32, device="cuda")
+    out = torch.empty_like(logits)
+    _abi.pa_process_logits(out, logits, _abi.LogitsSpec(history=hist, history_lens=lens, repetition=rep))
+    assert _abi.pa_get_status() == (0, 0)
+    want = logits.double().cpu() / rep.double().cpu()[:, None]
+    got = out.double().cpu()
+    top = torch.finfo(torch.float32).max
+    big = want > top
+    # a rounding of the quotient and one of its correction, each half a step (2^-24), and below the
+    # normal range a step of 2^-149 each
+    near = (got - want).abs() <= want * 2. ** -23 + 2. ** -148
+    assert bool(torch.where(big, torch.isinf(got) | (got >= top), near).all())
+
+
 def test_logits_captured_and_on_another_stream():
     g = gen(11)
     x = torch.randn(4, 2, 5000, generator=g)
