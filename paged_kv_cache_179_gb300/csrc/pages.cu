@@ -10,6 +10,14 @@
 // The page of rank k goes to the item whose needs' prefix sum holds k, found by
 // bisection: the lowest free pages, in the items' order, whatever order the
 // warps run in.
+//
+// Latency bounds them, the pages' copies excepted: the counts of a pool of 577k pages are
+// 2.3 MB, read once from memory and, where pages are taken, again from L2.  Measured on
+// a GB300: 64 rows given back and 256 served from that pool 26 us (two launches; 85 with
+// contiguous parts of the pool for the warps and one load in flight); the same in a pool
+// of 64 pages 8 us; 96 forks with their copies, after 96 rows are given back, 16 us;
+// compaction of 16384 pages, half of them live (132 MB of copies and tables), 28 us,
+// 4.7 TB/s; of 49001 E4M3 pages (341 MB) 65 us, 5.3 TB/s, 78 % of a plain copy's rate.
 #include <algorithm>
 #include <climits>
 
@@ -44,7 +52,9 @@ cudaError_t launch_after(void (*kern)(P...), unsigned grid, unsigned threads, cu
 constexpr int kScanThreads = 1024;
 constexpr int kScanWarps = kScanThreads / 32;
 constexpr int kScanCtas = 8;                       // a portable cluster, for larger pools
-// Up to this many pages one CTA ranks by itself: 4 pages a lane, two barriers less.
+// Up to this many pages one CTA ranks by itself: 4 pages a lane, and no cluster's barriers
+// (a fork of four beams in a small pool: 10 us for the call and the free before it, 14 with
+// the cluster; beyond, the cluster reads the counts in an eighth of the rounds).
 constexpr int kOneCtaPages = 4096;
 // Where items' pages go is kept in shared memory for up to this many items.
 constexpr int kKeptItems = 8192;
@@ -433,7 +443,8 @@ fork_kernel(const TakeArgs a, int32_t* context_lens, const PagePools p) {
   int32_t* to = a.block_tables + static_cast<int64_t>(dst) * a.mbs;
   if (L & 15) {
     const int old = from[full], mine = to[full];
-    if (old < 0 || old >= a.num_blocks) {
+    // (`mine` is what the launch before took, unless another pair changed src meanwhile)
+    if (old < 0 || old >= a.num_blocks || mine < 0 || mine >= a.num_blocks) {
       if (threadIdx.x == 0) atomicOr(a.status, kStatusBadBlock);
     } else {
       const int64_t chunks = p.page_bytes / 16;
