@@ -50,9 +50,13 @@ extern "C" {
  *   out: [num_tokens][num_q_heads][head_dim]; query_starts: int32
  *   [num_seqs + 1]; num_q_heads / num_kv_heads 1..32; head_dim 64 or 128;
  *   block_size 16; num_tokens * num_q_heads at most 2^30; max_context_len at most
- *   2^30; num_seqs at most 65535; scale finite.
+ *   2^30; num_seqs at most 65535; num_blocks * num_kv_heads of a 16-bit pool below
+ *   2^31; scale finite; out must not overlap q.
  *   workspace: pa_prefill_workspace_size bytes, 256-byte aligned, of any
- *   contents; calls that share one must not overlap on the device.
+ *   contents (its size goes by the current device's SMs and head_dim: one serves all
+ *   calls); calls that share one must not overlap on the device.
+ * Every wait of the kernel is bounded by 2 s: one that runs out sets
+ * PA_STATUS_TIMEOUT, and the outputs are not to be used.
  * Results do not depend on the order of execution.
  */
 size_t pa_prefill_workspace_size(int num_seqs, int num_tokens, int num_q_heads, int num_kv_heads,
@@ -88,7 +92,9 @@ int pa_prefill_fp8(void *out, const void *q, int64_t q_stride, const uint8_t *k_
  * PA_STATUS_BAD_ROW and the item is passed over; a num_pages outside [0,
  * max_blocks_per_seq] sets PA_STATUS_BAD_LEN, likewise.  num_blocks at most 2^30;
  * num_items at most 32768 where granted is written, else 2^24; ref_counts
- * 16-byte aligned.
+ * 16-byte aligned.  These calls write tables, lengths and pages: a decode that
+ * follows one of them with nothing else between on the stream must not be one with
+ * PA_DECODE_EARLY_PROLOGUE or PA_DECODE_EARLY_COPIES.
  *
  * pa_alloc_pages: rows[i] gets pages until it holds ceil(new_lens[i] / 16)
  * (one that holds as many keeps what it has), from the lowest free ones on, with
@@ -147,8 +153,7 @@ int pa_fork_pages(void *k_cache, void *v_cache, float *k_scale, float *v_scale,
  *   pool or free sets PA_STATUS_BAD_BLOCK; it is kept, or becomes -1.
  * ref_counts_out may be ref_counts and tables_out block_tables (in place); no
  * other overlap.  workspace: pa_compact_workspace_size bytes, 256-byte aligned,
- * of any contents.  The next decode must not be one with
- * PA_DECODE_EARLY_PROLOGUE or PA_DECODE_EARLY_COPIES.
+ * of any contents.
  */
 size_t pa_compact_workspace_size(int num_blocks);
 int pa_compact_pages(void *k_cache, void *v_cache, float *k_scale, float *v_scale,

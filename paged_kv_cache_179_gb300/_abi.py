@@ -112,6 +112,11 @@ REQUEST_SIGNATURES = {
                           _vp, _vp, _vp, _vp, _vp, _sz, _vp], _i32),
     "pa_process_logits": ([_vp, _i64, _vp, _i64, _vp, _i32, _i32, _i32, _i32, _i32, _vp], _i32),
 }
+# the failure-path test of include/pa_request_test.h
+REQUEST_TEST_SIGNATURES = {
+    "pa_test_prefill_timeout": ([_vp, _vp, _i64, _vp, _vp, _vp, _i32, _vp, _i32, _vp, _i32, _i32, _i32,
+                                 _i32, _i32, _i32, _f32, _i32, _i32, ctypes.c_uint64, _vp, _sz, _vp], _i32),
+}
 # the failure-path test of include/pa_serving_test.h
 SERVING_TEST_SIGNATURES = {
     "pa_test_weights_timeout": ([_vp, _i64, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32,
@@ -145,6 +150,7 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
             L = ctypes.CDLL(_build.LIB)
             for name, (args, res) in (*SIGNATURES.items(), *SERVING_SIGNATURES.items(),
                                       *REQUEST_SIGNATURES.items(),
+                                      *REQUEST_TEST_SIGNATURES.items(),
                                       *SERVING_TEST_SIGNATURES.items()):
                 fn = getattr(L, name)
                 fn.argtypes = args
@@ -1009,6 +1015,20 @@ def pa_prefill_fp8(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, con
     a, b = _prefill_args(out, q, k_cache, v_cache, block_tables, context_lens, max_context_len,
                          query_starts, scale, workspace, window, torch.uint8, (k_scale, v_scale))
     _call(load().pa_prefill_fp8, "pa_prefill_fp8", *a, *b)
+
+
+def pa_test_prefill_timeout(out, q, k_cache, v_cache, block_tables, context_lens,
+                            max_context_len: int, query_starts, scale: float, workspace, *,
+                            drop_tile: int, limit_ns: int) -> None:
+    """Failure-path test: pa_prefill whose CTAs wait for keys that are never copied (tile
+    ``drop_tile`` of each), give up after ``limit_ns`` and set PA_STATUS_TIMEOUT."""
+    a, b = _prefill_args(out, q, k_cache, v_cache, block_tables, context_lens, max_context_len,
+                         query_starts, scale, workspace, 0, None, ())
+    tables, mbs, lens, mx, starts, T, B, Hq, Hkv, D, bs, NB, sc, _, dtype, ws, n, stream = b
+    if bs != 16:
+        raise ValueError("blocks of 16 tokens")
+    _call(load().pa_test_prefill_timeout, "pa_test_prefill_timeout", *a, tables, mbs, lens, mx, starts,
+          T, B, Hq, Hkv, D, NB, sc, dtype, int(drop_tile), int(limit_ns), ws, n, stream)
 
 
 def _page_state(block_tables, num_pages, ref_counts):

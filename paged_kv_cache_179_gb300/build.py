@@ -42,7 +42,7 @@ def nvcc() -> str:
 def _inputs():
     return ([os.path.join(CSRC, s) for s in SOURCES] + [os.path.join(CSRC, h) for h in HEADERS]
             + [os.path.join(INCLUDE, h) for h in ("pa.h", "pa_serving.h", "pa_serving_test.h",
-                                                    "pa_request.h")] + [os.path.abspath(__file__)])
+                                                    "pa_request.h", "pa_request_test.h")] + [os.path.abspath(__file__)])
 
 
 def up_to_date() -> bool:

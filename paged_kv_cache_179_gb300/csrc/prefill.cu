@@ -14,16 +14,27 @@
 //   warps 0-3, 4-7   the softmax of one subtile each, a thread a row, whose 128 scores it
 //                    holds in registers; P goes back to tensor memory as 16-bit pairs;
 //   warp 8           walks the CTA's pieces, copies Q and K (TMA), of E4M3 pools V too;
-//   warp 9           one thread issues the products, each as soon as its operands are
-//                    there.  A subtile's Q.K of the next tile follows its P.V in the
-//                    same queue, so S needs no second buffer: the tensor cores work on
-//                    one subtile while the other's softmax runs;
-//   warps 10-13      E4M3 pools: codes to f16 (exact) between two shared-memory rings.
+//   warps 9, 10      the products of one subtile each.  Its Q.K of the next tile follows its
+//                    P.V in the same queue, so S needs no second buffer.  The subtiles
+//                    take turns, tile by tile: the tensor cores work on one while the
+//                    other's softmax runs;
+//   warp 11          copies V; or, warps 11-15, of E4M3 pools: codes to f16 (exact)
+//                    between two shared-memory rings.
 //
 // The softmax offset of a row is the maximum of an early tile's scores and moves only
 // when weights grow out of the products' range (kMaxSum): any standing offset gives the
 // same softmax.  So most tiles need no maximum: their weights are made at once, their
-// sum shows whether they may stand, and O is scaled in tensor memory hardly ever.
+// sum shows whether they may stand, and O is scaled in tensor memory hardly ever.  The
+// weights of a tile's first half are announced alone, and its product begins.
+//
+// What bounds it: a product of 128 x 128 x 16 takes 64 cycles (measured, alone; 65 to 80
+// with the softmax beside it), so a tile of both subtiles takes 2048 of the tensor
+// cores, and 1200 of each exponential unit.  Measured on a GB300 (28/4 heads of 128,
+// bf16): one prompt of 16384 tokens 1.19 ms, 1.62 PFLOP/s, 85 % of the measured bf16
+// rate; with one loop for whole tiles and edges together it took 1.31 ms, with both
+// subtiles' products in one queue unordered 1.95 (either in step, or one ahead until the
+// ring had no place for its keys), with one thread issuing both subtiles' 3.8.
+//
 // Page scales: K's multiply the scores of their 16 columns, V's the weights (relative
 // to a power of two that follows the largest seen, so that P stays in f16's range).
 //
@@ -462,405 +473,406 @@ prefill_kernel(const __grid_constant__ Args ka) {
   auto slot_at = [&](int i) { return ring + (i % C::kSlots) * C::kSlot; };   // i: K 2g, V 2g + 1
 
   if (warp >= 8) {
-  regs_down<C::kOtherRegs>();
-  if (warp == kCopyWarp) {
-    // ================================================================ copies
-    const int64_t hi = sm.hi;
-    int b = sm.b, h = sm.h, j = sm.j, off = sm.off;
-    int64_t pos = sm.lo - (off > 0 ? off + kItemCost : 0);   // the item's first unit
-    int d = 0, g = 0, q_fills[2] = {0, 0}, raws = 0;
-    int n = 0, L = 0, t0 = 0, loaded = -1;
-    int head[6] = {0, 0, 0, 0, 0, 0};
-    bool ok = true;
-    // K (kv 0) or V (1) of tile g of kv head hh, whose page ids are the first lanes' `id`
-    auto copy_tile = [&](int kv, int id, unsigned valid, int hh) {
-      if constexpr (FP8) {
-        if (raws >= C::kRaws && !wait_warp(kRawEmpty + raws % 2, raws / 2 - 1)) return false;
-        const uint32_t full = bar(kRawFull + raws % 2), to = raw + (raws % 2) * C::kRaw;
-        ++raws;
-        copy_codes<D>(static_cast<const uint8_t*>(kv ? a.v_cache : a.k_cache), a.Hkv, hh, id, valid, to, full);
-      } else {
-        const int i = 2 * g + kv;
-        if (i >= C::kSlots && !wait_warp(kEmpty + i % C::kSlots, i / C::kSlots - 1)) return false;
-        copy_pages<C::kHalves, C::kSub>(kv ? &ka.tm_v : &ka.tm_k, a.Hkv, hh, id, valid, slot_at(i),
-                                        bar(kFull + i % C::kSlots));
-      }
-      return true;
-    };
-    // a piece's query rows
-    auto copy_queries = [&](const Desc& x) {
-      for (int w = 0; w < 2; ++w) {
-        const int2 r = sub_tiles(x, w, sub, a.window);
-        if (r.x == r.y) continue;
-        if (q_fills[w] > 0 && !wait_warp(kQEmpty + w, q_fills[w] - 1)) return false;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(bar(kQFull + w), static_cast<uint32_t>(C::kHalves * 128 * sub * G));
-#pragma unroll
-          for (int y = 0; y < C::kHalves; ++y)
-            box_g2s(q_at + w * C::kSlot + y * C::kSub, &ka.tm_q, 64 * y, x.h * G, x.t0 + w * sub,
-                    bar(kQFull + w));
-        }
-        ++q_fills[w];
-        __syncwarp();
-      }
-      return true;
-    };
-    while (ok && pos < hi) {
-      if (b != loaded) {                   // (bad starts and lengths were reported above)
-        const int s0 = a.starts[b], s1 = a.starts[b + 1];
-        n = s0 >= 0 && s1 >= s0 && s1 <= a.T ? s1 - s0 : 0;
-        L = a.context_lens[b];
-        L = L >= 0 && L <= a.max_context_len ? L : 0;
-        t0 = s0;
-        loaded = b;
-      }
-      const int items = (n + 2 * sub - 1) / (2 * sub);
-      if (items == 0) {
-        ++b;
-        continue;
-      }
-      int k0;
-      const int u = item_units(n, L, j, sub, a.window, &k0);
-      const int64_t room = hi - pos - kItemCost;   // tiles of it before the share's end
-      const int take = (room < u ? static_cast<int>(room) : u) - off;
-      Desc x;
-      x.h = h;
-      x.b = b;
-      x.n = n;
-      x.L = L;
-      x.i0 = j * 2 * sub;
-      x.tokens = min(n - x.i0, 2 * sub);
-      x.t0 = t0 + x.i0;
-      const bool sees = L - n + x.i0 + x.tokens - 1 >= 0;
-      x.k_lo = sees ? k0 + off : 0;
-      x.k_hi = sees ? k0 + off + take : 0;
-      x.g0 = g;
-      x.whole = take == u;
-      x.part = off > 0 ? 0 : 1;
-      if (!x.whole) {
-        if (off > 0) {
-          head[kHasHead] = 1;
-          head[kHeadEnds] = off + take == u;
-        } else {
-          head[kHasTail] = 1;
-          head[kTailT0] = x.t0;
-          head[kTailH] = h;
-          head[kTailTokens] = x.tokens;
-        }
-      }
-      if (d >= kDescs && !wait_warp(kDEmpty + d % kDescs, d / kDescs - 1)) break;
-      if (lane == 0) {
-        sm.desc[d % kDescs] = x;
-        mbar_arrive(bar(kDFull + d % kDescs));
-      }
-      ++d;
-      __syncwarp();
-      // ---- its tiles: four tiles' page ids at a time, one tile ahead of the copies
-      const int32_t* table = a.block_tables + static_cast<int64_t>(b) * a.mbs;
-      const int last_page = (L + 15) / 16 - 1;
-      int ids = -1;
-      for (int t = x.k_lo; ok && t < x.k_hi; ++t, ++g) {
-        const int in4 = (t - x.k_lo) & 3;
-        if (in4 == 0) {
-          const int p = t * kPages + lane;
-          ids = p <= last_page && t + (lane >> 3) < x.k_hi ? table[p] : -1;
-        }
-        const int id = __shfl_sync(0xffffffffu, ids, in4 * 8 + (lane & 7));
-        const bool mine = lane < kPages && t * kPages + lane <= last_page;
-        const bool valid = mine && id >= 0 && id < a.num_blocks;
-        if (mine && !valid) atomicOr(a.status, kStatusBadBlock);
-        const unsigned m = __ballot_sync(0xffffffffu, valid);
-        Meta& mt = sm.meta[g % kMetas];
-        if (lane == 0) mt.valid = m;
+    regs_down<C::kOtherRegs>();
+    if (warp == kCopyWarp) {
+      // ================================================================ copies
+      const int64_t hi = sm.hi;
+      int b = sm.b, h = sm.h, j = sm.j, off = sm.off;
+      int64_t pos = sm.lo - (off > 0 ? off + kItemCost : 0);   // the item's first unit
+      int d = 0, g = 0, q_fills[2] = {0, 0}, raws = 0;
+      int n = 0, L = 0, t0 = 0, loaded = -1;
+      int head[6] = {0, 0, 0, 0, 0, 0};
+      bool ok = true;
+      // K (kv 0) or V (1) of tile g of kv head hh, whose page ids are the first lanes' `id`
+      auto copy_tile = [&](int kv, int id, unsigned valid, int hh) {
         if constexpr (FP8) {
-          const int64_t page = static_cast<int64_t>(valid ? id : 0) * a.Hkv + h;
-          const float sk = valid ? a.k_scale[page] : 0.f, sv = valid ? a.v_scale[page] : 0.f;
-          float top = sv;
+          if (raws >= C::kRaws && !wait_warp(kRawEmpty + raws % 2, raws / 2 - 1)) return false;
+          const uint32_t full = bar(kRawFull + raws % 2), to = raw + (raws % 2) * C::kRaw;
+          ++raws;
+          copy_codes<D>(static_cast<const uint8_t*>(kv ? a.v_cache : a.k_cache), a.Hkv, hh, id, valid, to, full);
+        } else {
+          const int i = 2 * g + kv;
+          if (i >= C::kSlots && !wait_warp(kEmpty + i % C::kSlots, i / C::kSlots - 1)) return false;
+          if (g != a.drop_tile)
+            copy_pages<C::kHalves, C::kSub>(&ka.tm_k, a.Hkv, hh, id, valid, slot_at(i),
+                                            bar(kFull + i % C::kSlots));
+        }
+        return true;
+      };
+      // a piece's query rows
+      auto copy_queries = [&](const Desc& x) {
+        for (int w = 0; w < 2; ++w) {
+          const int2 r = sub_tiles(x, w, sub, a.window);
+          if (r.x == r.y) continue;
+          if (q_fills[w] > 0 && !wait_warp(kQEmpty + w, q_fills[w] - 1)) return false;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar(kQFull + w), static_cast<uint32_t>(C::kHalves * 128 * sub * G));
 #pragma unroll
-          for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          if (lane < kPages) {
-            mt.ks[lane] = sk;
-            mt.vs[lane] = sv;
-            mt.v_big = top;
+            for (int y = 0; y < C::kHalves; ++y)
+              box_g2s(q_at + w * C::kSlot + y * C::kSub, &ka.tm_q, 64 * y, x.h * G, x.t0 + w * sub,
+                      bar(kQFull + w));
+          }
+          ++q_fills[w];
+          __syncwarp();
+        }
+        return true;
+      };
+      while (ok && pos < hi) {
+        if (b != loaded) {                   // (bad starts and lengths were reported above)
+          const int s0 = a.starts[b], s1 = a.starts[b + 1];
+          n = s0 >= 0 && s1 >= s0 && s1 <= a.T ? s1 - s0 : 0;
+          L = a.context_lens[b];
+          L = L >= 0 && L <= a.max_context_len ? L : 0;
+          t0 = s0;
+          loaded = b;
+        }
+        const int items = (n + 2 * sub - 1) / (2 * sub);
+        if (items == 0) {
+          ++b;
+          continue;
+        }
+        int k0;
+        const int u = item_units(n, L, j, sub, a.window, &k0);
+        const int64_t room = hi - pos - kItemCost;   // tiles of it before the share's end
+        const int take = (room < u ? static_cast<int>(room) : u) - off;
+        Desc x;
+        x.h = h;
+        x.b = b;
+        x.n = n;
+        x.L = L;
+        x.i0 = j * 2 * sub;
+        x.tokens = min(n - x.i0, 2 * sub);
+        x.t0 = t0 + x.i0;
+        const bool sees = L - n + x.i0 + x.tokens - 1 >= 0;
+        x.k_lo = sees ? k0 + off : 0;
+        x.k_hi = sees ? k0 + off + take : 0;
+        x.g0 = g;
+        x.whole = take == u;
+        x.part = off > 0 ? 0 : 1;
+        if (!x.whole) {
+          if (off > 0) {
+            head[kHasHead] = 1;
+            head[kHeadEnds] = off + take == u;
+          } else {
+            head[kHasTail] = 1;
+            head[kTailT0] = x.t0;
+            head[kTailH] = h;
+            head[kTailTokens] = x.tokens;
           }
         }
+        if (d >= kDescs && !wait_warp(kDEmpty + d % kDescs, d / kDescs - 1)) break;
+        if (lane == 0) {
+          sm.desc[d % kDescs] = x;
+          mbar_arrive(bar(kDFull + d % kDescs));
+        }
+        ++d;
         __syncwarp();
-        ok = copy_tile(0, id, m, h) && (t > x.k_lo || copy_queries(x)) &&
-             (!FP8 || copy_tile(1, id, m, h));
-      }
-      // ---- the next item
-      pos += u + kItemCost;
-      off = 0;
-      if (++j == items) {
-        j = 0;
-        if (++h == a.Hkv) {
-          h = 0;
-          ++b;
+        // ---- its tiles: four tiles' page ids at a time, one tile ahead of the copies
+        const int32_t* table = a.block_tables + static_cast<int64_t>(b) * a.mbs;
+        const int last_page = (L + 15) / 16 - 1;
+        int ids = -1;
+        for (int t = x.k_lo; ok && t < x.k_hi; ++t, ++g) {
+          const int in4 = (t - x.k_lo) & 3;
+          if (in4 == 0) {
+            const int p = t * kPages + lane;
+            ids = p <= last_page && t + (lane >> 3) < x.k_hi ? table[p] : -1;
+          }
+          const int id = __shfl_sync(0xffffffffu, ids, in4 * 8 + (lane & 7));
+          const bool mine = lane < kPages && t * kPages + lane <= last_page;
+          const bool valid = mine && id >= 0 && id < a.num_blocks;
+          if (mine && !valid) atomicOr(a.status, kStatusBadBlock);
+          const unsigned m = __ballot_sync(0xffffffffu, valid);
+          Meta& mt = sm.meta[g % kMetas];
+          if (lane == 0) mt.valid = m;
+          if constexpr (FP8) {
+            const int64_t page = static_cast<int64_t>(valid ? id : 0) * a.Hkv + h;
+            const float sk = valid ? a.k_scale[page] : 0.f, sv = valid ? a.v_scale[page] : 0.f;
+            float top = sv;
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            if (lane < kPages) {
+              mt.ks[lane] = sk;
+              mt.vs[lane] = sv;
+              mt.v_big = top;
+            }
+          }
+          __syncwarp();
+          ok = copy_tile(0, id, m, h) && (t > x.k_lo || copy_queries(x)) &&
+               (!FP8 || copy_tile(1, id, m, h));
+        }
+        // ---- the next item
+        pos += u + kItemCost;
+        off = 0;
+        if (++j == items) {
+          j = 0;
+          if (++h == a.Hkv) {
+            h = 0;
+            ++b;
+          }
         }
       }
-    }
-    if (ok && (d < kDescs || wait_warp(kDEmpty + d % kDescs, d / kDescs - 1))) {
-      if (lane == 0) {
-        sm.desc[d % kDescs].h = -1;
-        mbar_arrive(bar(kDFull + d % kDescs));
+      if (ok && (d < kDescs || wait_warp(kDEmpty + d % kDescs, d / kDescs - 1))) {
+        if (lane == 0) {
+          sm.desc[d % kDescs].h = -1;
+          mbar_arrive(bar(kDFull + d % kDescs));
+        }
       }
-    }
-    if (FP8 && lane == 0) {                // the converting warps' end
-      *reinterpret_cast<volatile int*>(&sm.raw_end) = raws;
-      __threadfence_block();
-    }
-    if (lane == 0)
-      for (int i = 0; i < 6; ++i) ka.ws_head[cta * kHeader + i] = head[i];
-    // no copy outlives the CTA
-    if (lane == 0) {
-      const uint64_t since = global_ns();
-      const uint64_t limit = ka.wait_limit_ns > kWaitLimitNs ? ka.wait_limit_ns : kWaitLimitNs;
-      auto settle = [&](int bb, int fills) {
-        while (fills > 0 && !mbar_try_wait(bar(bb), (fills - 1) & 1) && global_ns() - since < limit) {
+      if (FP8 && lane == 0) {                // the converting warps' end
+        *reinterpret_cast<volatile int*>(&sm.raw_end) = raws;
+        __threadfence_block();
+      }
+      if (lane == 0)
+        for (int i = 0; i < 6; ++i) ka.ws_head[cta * kHeader + i] = head[i];
+      // no copy outlives the CTA
+      if (lane == 0) {
+        const uint64_t since = global_ns();
+        const uint64_t limit = ka.wait_limit_ns > kWaitLimitNs ? ka.wait_limit_ns : kWaitLimitNs;
+        auto settle = [&](int bb, int fills) {
+          while (fills > 0 && !mbar_try_wait(bar(bb), (fills - 1) & 1) && global_ns() - since < limit) {
+          }
+        };
+        for (int w = 0; w < 2; ++w) settle(kQFull + w, q_fills[w]);
+        if (FP8) {
+          for (int r = 0; r < 2; ++r) settle(kRawFull + r, (raws - r + 1) / 2);
+        } else {
+          for (int i = (max(2 * g - C::kSlots, 0) + 1) / 2 * 2; i < 2 * g; i += 2)   // each place's last
+            settle(kFull + i % C::kSlots, i / C::kSlots + 1);
+        }
+      }
+      __syncwarp();
+    } else if (warp < kConvWarp) {
+      // ================================================================ products
+      // One warp a subtile: Q.K of a tile, then, once its weights are there, P.V.
+      constexpr uint32_t kIdQK = umma_idesc_f16<kMmaBf16>(kTile, kTile, false);
+      constexpr uint32_t kIdPV = umma_idesc_f16<kMmaBf16>(kTile, D, false) | kBMajorN;
+      const int w = warp - kMmaWarp;
+      const uint32_t ts = tmem + w * kTile, to = tmem_o + w * D;
+      const uint64_t dq = umma_desc_sw128(q_at + w * C::kSlot, 16, 1024);
+      const uint64_t dk0 = umma_desc_sw128(ring, 16, 1024);
+      const uint64_t dv0 = umma_desc_sw128(ring, C::kSub, 1024);
+      int p_n = 0, q_n = 0;
+      // the next K's and V's place in the ring (K 0, V 1, K 2, ..) and their fills' parity
+      int ks = 0, kp = 0, vs = 1, vp = 0;
+      auto step2 = [&](int& slot, int& parity) {
+        slot += 2;
+        if (slot >= C::kSlots) {
+          slot -= C::kSlots;
+          parity ^= 1;
         }
       };
-      for (int w = 0; w < 2; ++w) settle(kQFull + w, q_fills[w]);
-      if (FP8) {
-        for (int r = 0; r < 2; ++r) settle(kRawFull + r, (raws - r + 1) / 2);
-      } else {
-        for (int i = (max(2 * g - C::kSlots, 0) + 1) / 2 * 2; i < 2 * g; i += 2)   // each place's last
-          settle(kFull + i % C::kSlots, i / C::kSlots + 1);
-      }
-    }
-    __syncwarp();
-  } else if (warp < kConvWarp) {
-    // ================================================================ products
-    // One warp a subtile: Q.K of a tile, then, once its weights are there, P.V.
-    constexpr uint32_t kIdQK = umma_idesc_f16<kMmaBf16>(kTile, kTile, false);
-    constexpr uint32_t kIdPV = umma_idesc_f16<kMmaBf16>(kTile, D, false) | kBMajorN;
-    const int w = warp - kMmaWarp;
-    const uint32_t ts = tmem + w * kTile, to = tmem_o + w * D;
-    const uint64_t dq = umma_desc_sw128(q_at + w * C::kSlot, 16, 1024);
-    const uint64_t dk0 = umma_desc_sw128(ring, 16, 1024);
-    const uint64_t dv0 = umma_desc_sw128(ring, C::kSub, 1024);
-    int p_n = 0, q_n = 0;
-    // the next K's and V's place in the ring (K 0, V 1, K 2, ..) and their fills' parity
-    int ks = 0, kp = 0, vs = 1, vp = 0;
-    auto step2 = [&](int& slot, int& parity) {
-      slot += 2;
-      if (slot >= C::kSlots) {
-        slot -= C::kSlots;
-        parity ^= 1;
-      }
-    };
-    auto full = [&](int slot, int parity) { return wait_warp(kFull + slot, parity); };
-    bool issued = false, ok = true;
-    // The subtiles take turns, tile by tile: left alone they either run in step, and the tensor
-    // cores wait while both softmaxes run, or one runs ahead until the ring has no place
-    // for its keys.
-    int g = 0;                             // the tile in the CTA's stream
-    volatile int* mine = &sm.passed[w];
-    volatile int* other = &sm.passed[w ^ 1];
-    auto my_turn = [&]() {                 // tile g is the first subtile's first
-      uint64_t t0 = 0;
-      for (unsigned i = 1; *other < g + w; ++i) {
-        if (i % 256 != 0) continue;
-        if (*dead) return false;
-        const uint64_t now = global_ns();
-        if (t0 == 0) {
-          t0 = now;
-        } else if (now - t0 > ka.wait_limit_ns) {
-          *dead = 1;
-          atomicOr(a.status, kStatusTimeout);
-          return false;
-        }
-      }
-      return true;
-    };
-    auto passed = [&]() {
-      ++g;
-      __syncwarp();
-      if (lane == 0) *mine = g;
-    };
-    auto scores = [&](bool last) {         // Q.K of the next tile, whose K has landed
-      if (elect_one()) {
-        mbar_arrive(bar(kSFull + w));      // (orders the tile's meta before the softmax's reads)
-        const uint64_t dk = dk0 + static_cast<uint64_t>(ks * (C::kSlot >> 4));
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint64_t o = static_cast<uint64_t>(((k >> 2) * C::kSub + (k & 3) * 32) >> 4);
-          umma_f16(ts, dq + o, dk + o, kIdQK, k > 0);
-        }
-        umma_commit(bar(kSFull + w));
-        umma_commit(bar(kEmpty + ks));
-        if (last) umma_commit(bar(kQEmpty + w));
-      }
-      __syncwarp();
-      issued = true;
-      step2(ks, kp);
-    };
-    auto pass = [&](int tiles) {           // tiles that the other subtile alone sees
-      for (int i = 0; i < tiles && ok; ++i) {
-        ok = full(ks, kp) && full(vs, vp);
-        if (ok && lane == 0) {
-          mbar_arrive(bar(kEmpty + ks));
-          mbar_arrive(bar(kEmpty + vs));
-        }
-        step2(ks, kp);
-        step2(vs, vp);
-        passed();
-      }
-    };
-    for (int d = 0; ok; ++d) {
-      if (!wait_warp(kDFull + d % kDescs, d / kDescs)) break;
-      const Desc& x = sm.desc[d % kDescs];
-      if (uniform(x.h) < 0) break;
-      int2 r = sub_tiles(x, w, sub, a.window);
-      r.x = uniform(r.x);
-      r.y = uniform(r.y);
-      const int k_lo = uniform(x.k_lo), k_hi = uniform(x.k_hi);
-      const bool some = r.x < r.y;
-      const int behind = some ? k_hi - r.y : 0;
-      pass(some ? r.x - k_lo : k_hi - k_lo);
-      if (ok && some) {
-        ok = full(ks, kp) && wait_warp((FP8 && BF16 ? kQConv : kQFull) + w, q_n++);
-        if (ok) {
-          tc_fence_after();
-          scores(r.x + 1 == r.y);
-        }
-      }
-      for (int t = r.x; ok && t < r.y; ++t, ++p_n) {
-        const bool more = t + 1 < r.y;
-        ok = full(vs, vp) && (!more || full(ks, kp)) && wait_warp(kPFull + w, p_n) &&
-             __all_sync(0xffffffffu, my_turn());
-        if (!ok) break;
-        tc_fence_after();
-        const bool skip = uniform(*reinterpret_cast<volatile int*>(&sm.skip[w])) != 0;
-        const uint64_t dv = dv0 + static_cast<uint64_t>(vs * (C::kSlot >> 4));
-        if (skip) {
-          if (lane == 0) mbar_arrive(bar(kPVHalf + w));
-        } else if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < kTile / 32; ++k)
-            umma_f16_ts(to, ts + 8 * k, dv + static_cast<uint64_t>(k * (2048 >> 4)), kIdPV,
-                        t > r.x || k > 0);
-          umma_commit(bar(kPVHalf + w));
-        }
-        __syncwarp();
-        ok = wait_warp(kPHalf + w, p_n);   // the weights of the second half of the tile
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) {
-          if (!skip) {
-#pragma unroll
-            for (int k = kTile / 32; k < kTile / 16; ++k)
-              umma_f16_ts(to, ts + 8 * k, dv + static_cast<uint64_t>(k * (2048 >> 4)), kIdPV, true);
-          }
-          umma_commit(bar(kEmpty + vs));
-          if (!more) umma_commit(bar(kODone + w));
-        }
-        __syncwarp();
-        step2(vs, vp);
-        if (more) scores(t + 2 == r.y);
-        passed();
-      }
-      pass(behind);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kDEmpty + d % kDescs));
-    }
-    // no product outlives the CTA
-    if (issued) {
-      if (elect_one()) umma_commit(bar(kFin + w));
-      __syncwarp();
-      const uint64_t since = global_ns();
-      const uint64_t limit = ka.wait_limit_ns > kWaitLimitNs ? ka.wait_limit_ns : kWaitLimitNs;
-      while (!mbar_try_wait(bar(kFin + w), 0) && global_ns() - since < limit) {
-      }
-    }
-    __syncwarp();
-  } else if (!FP8) {
-    // ================================================================ V's copies
-    int g = 0;
-    bool ok = true;
-    for (int d = 0; ok; ++d) {
-      if (!wait_warp(kDFull + d % kDescs, d / kDescs)) break;
-      const Desc& x = sm.desc[d % kDescs];
-      const int h = uniform(x.h);
-      if (h < 0) break;
-      const int k_lo = uniform(x.k_lo), k_hi = uniform(x.k_hi);
-      const int32_t* table = a.block_tables + static_cast<int64_t>(x.b) * a.mbs;
-      const int last_page = (x.L + 15) / 16 - 1;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kDEmpty + d % kDescs));
-      int ids = -1;
-      for (int t = k_lo; ok && t < k_hi; ++t, ++g) {
-        const int in4 = (t - k_lo) & 3;
-        if (in4 == 0) {
-          const int p = t * kPages + lane;
-          ids = p <= last_page && t + (lane >> 3) < k_hi ? table[p] : -1;
-        }
-        const int id = __shfl_sync(0xffffffffu, ids, in4 * 8 + (lane & 7));
-        const unsigned m = __ballot_sync(0xffffffffu, lane < kPages && id >= 0 && id < a.num_blocks);
-        const int i = 2 * g + 1;
-        ok = i < C::kSlots || wait_warp(kEmpty + i % C::kSlots, i / C::kSlots - 1);
-        if (ok)
-          copy_pages<C::kHalves, C::kSub>(&ka.tm_v, a.Hkv, h, id, m, slot_at(i), bar(kFull + i % C::kSlots));
-      }
-    }
-    if (lane == 0) {                       // no copy outlives the CTA
-      const uint64_t since = global_ns();
-      const uint64_t limit = ka.wait_limit_ns > kWaitLimitNs ? ka.wait_limit_ns : kWaitLimitNs;
-      if (!ok) --g;                        // (the last one was not made)
-      for (int i = max(2 * g - C::kSlots, 0) | 1; i < 2 * g; i += 2) {
-        while (!mbar_try_wait(bar(kFull + i % C::kSlots), (i / C::kSlots) & 1) && global_ns() - since < limit) {
-        }
-      }
-    }
-    __syncwarp();
-  } else {
-    // ================================================================ codes to f16
-    const int ct = tid - kConvWarp * 32;
-    for (int f = 0;; ++f) {
-      // the next fill, or the end
-      const uint64_t since = global_ns();
-      bool got = false, end = false;
-      while (!got && !end) {
-        got = mbar_try_wait(bar(kRawFull + f % 2), (f / 2) & 1);
-        if (!got) {
-          end = f >= *reinterpret_cast<volatile int*>(&sm.raw_end) || *dead;
-          if (!end && global_ns() - since > ka.wait_limit_ns) {
+      auto full = [&](int slot, int parity) { return wait_warp(kFull + slot, parity); };
+      bool issued = false, ok = true;
+      // The subtiles take turns, tile by tile: left alone they either run in step, and the tensor
+      // cores wait while both softmaxes run, or one runs ahead until the ring has no place
+      // for its keys.
+      int g = 0;                             // the tile in the CTA's stream
+      volatile int* mine = &sm.passed[w];
+      volatile int* other = &sm.passed[w ^ 1];
+      auto my_turn = [&]() {                 // tile g is the first subtile's first
+        uint64_t t0 = 0;
+        for (unsigned i = 1; *other < g + w; ++i) {
+          if (i % 256 != 0) continue;
+          if (*dead) return false;
+          const uint64_t now = global_ns();
+          if (t0 == 0) {
+            t0 = now;
+          } else if (now - t0 > ka.wait_limit_ns) {
             *dead = 1;
             atomicOr(a.status, kStatusTimeout);
-            end = true;
+            return false;
+          }
+        }
+        return true;
+      };
+      auto passed = [&]() {
+        ++g;
+        __syncwarp();
+        if (lane == 0) *mine = g;
+      };
+      auto scores = [&](bool last) {         // Q.K of the next tile, whose K has landed
+        if (elect_one()) {
+          mbar_arrive(bar(kSFull + w));      // (orders the tile's meta before the softmax's reads)
+          const uint64_t dk = dk0 + static_cast<uint64_t>(ks * (C::kSlot >> 4));
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint64_t o = static_cast<uint64_t>(((k >> 2) * C::kSub + (k & 3) * 32) >> 4);
+            umma_f16(ts, dq + o, dk + o, kIdQK, k > 0);
+          }
+          umma_commit(bar(kSFull + w));
+          umma_commit(bar(kEmpty + ks));
+          if (last) umma_commit(bar(kQEmpty + w));
+        }
+        __syncwarp();
+        issued = true;
+        step2(ks, kp);
+      };
+      auto pass = [&](int tiles) {           // tiles that the other subtile alone sees
+        for (int i = 0; i < tiles && ok; ++i) {
+          ok = full(ks, kp) && full(vs, vp);
+          if (ok && lane == 0) {
+            mbar_arrive(bar(kEmpty + ks));
+            mbar_arrive(bar(kEmpty + vs));
+          }
+          step2(ks, kp);
+          step2(vs, vp);
+          passed();
+        }
+      };
+      for (int d = 0; ok; ++d) {
+        if (!wait_warp(kDFull + d % kDescs, d / kDescs)) break;
+        const Desc& x = sm.desc[d % kDescs];
+        if (uniform(x.h) < 0) break;
+        int2 r = sub_tiles(x, w, sub, a.window);
+        r.x = uniform(r.x);
+        r.y = uniform(r.y);
+        const int k_lo = uniform(x.k_lo), k_hi = uniform(x.k_hi);
+        const bool some = r.x < r.y;
+        const int behind = some ? k_hi - r.y : 0;
+        pass(some ? r.x - k_lo : k_hi - k_lo);
+        if (ok && some) {
+          ok = full(ks, kp) && wait_warp((FP8 && BF16 ? kQConv : kQFull) + w, q_n++);
+          if (ok) {
+            tc_fence_after();
+            scores(r.x + 1 == r.y);
+          }
+        }
+        for (int t = r.x; ok && t < r.y; ++t, ++p_n) {
+          const bool more = t + 1 < r.y;
+          ok = full(vs, vp) && (!more || full(ks, kp)) && wait_warp(kPFull + w, p_n) &&
+               __all_sync(0xffffffffu, my_turn());
+          if (!ok) break;
+          tc_fence_after();
+          const bool skip = uniform(*reinterpret_cast<volatile int*>(&sm.skip[w])) != 0;
+          const uint64_t dv = dv0 + static_cast<uint64_t>(vs * (C::kSlot >> 4));
+          if (skip) {
+            if (lane == 0) mbar_arrive(bar(kPVHalf + w));
+          } else if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < kTile / 32; ++k)
+              umma_f16_ts(to, ts + 8 * k, dv + static_cast<uint64_t>(k * (2048 >> 4)), kIdPV,
+                          t > r.x || k > 0);
+            umma_commit(bar(kPVHalf + w));
+          }
+          __syncwarp();
+          ok = wait_warp(kPHalf + w, p_n);   // the weights of the second half of the tile
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            if (!skip) {
+#pragma unroll
+              for (int k = kTile / 32; k < kTile / 16; ++k)
+                umma_f16_ts(to, ts + 8 * k, dv + static_cast<uint64_t>(k * (2048 >> 4)), kIdPV, true);
+            }
+            umma_commit(bar(kEmpty + vs));
+            if (!more) umma_commit(bar(kODone + w));
+          }
+          __syncwarp();
+          step2(vs, vp);
+          if (more) scores(t + 2 == r.y);
+          passed();
+        }
+        pass(behind);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kDEmpty + d % kDescs));
+      }
+      // no product outlives the CTA
+      if (issued) {
+        if (elect_one()) umma_commit(bar(kFin + w));
+        __syncwarp();
+        const uint64_t since = global_ns();
+        const uint64_t limit = ka.wait_limit_ns > kWaitLimitNs ? ka.wait_limit_ns : kWaitLimitNs;
+        while (!mbar_try_wait(bar(kFin + w), 0) && global_ns() - since < limit) {
+        }
+      }
+      __syncwarp();
+    } else if (!FP8) {
+      // ================================================================ V's copies
+      int g = 0;
+      bool ok = true;
+      for (int d = 0; ok; ++d) {
+        if (!wait_warp(kDFull + d % kDescs, d / kDescs)) break;
+        const Desc& x = sm.desc[d % kDescs];
+        const int h = uniform(x.h);
+        if (h < 0) break;
+        const int k_lo = uniform(x.k_lo), k_hi = uniform(x.k_hi);
+        const int32_t* table = a.block_tables + static_cast<int64_t>(x.b) * a.mbs;
+        const int last_page = (x.L + 15) / 16 - 1;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kDEmpty + d % kDescs));
+        int ids = -1;
+        for (int t = k_lo; ok && t < k_hi; ++t, ++g) {
+          const int in4 = (t - k_lo) & 3;
+          if (in4 == 0) {
+            const int p = t * kPages + lane;
+            ids = p <= last_page && t + (lane >> 3) < k_hi ? table[p] : -1;
+          }
+          const int id = __shfl_sync(0xffffffffu, ids, in4 * 8 + (lane & 7));
+          const unsigned m = __ballot_sync(0xffffffffu, lane < kPages && id >= 0 && id < a.num_blocks);
+          const int i = 2 * g + 1;
+          ok = i < C::kSlots || wait_warp(kEmpty + i % C::kSlots, i / C::kSlots - 1);
+          if (ok)
+            copy_pages<C::kHalves, C::kSub>(&ka.tm_v, a.Hkv, h, id, m, slot_at(i), bar(kFull + i % C::kSlots));
+        }
+      }
+      if (lane == 0) {                       // no copy outlives the CTA
+        const uint64_t since = global_ns();
+        const uint64_t limit = ka.wait_limit_ns > kWaitLimitNs ? ka.wait_limit_ns : kWaitLimitNs;
+        if (!ok) --g;                        // (the last one was not made)
+        for (int i = max(2 * g - C::kSlots, 0) | 1; i < 2 * g; i += 2) {
+          while (!mbar_try_wait(bar(kFull + i % C::kSlots), (i / C::kSlots) & 1) && global_ns() - since < limit) {
           }
         }
       }
-      if (!__all_sync(0xffffffffu, got)) break;
-      if (f >= C::kSlots && !wait_warp(kEmpty + f % C::kSlots, f / C::kSlots - 1)) break;
-      const uint32_t src = raw + (f % 2) * C::kRaw, dst = slot_at(f);
-      constexpr int kChunks = D / 16;      // 16 codes each, of a row
-#pragma unroll 4
-      for (int i = ct; i < kTile * kChunks; i += C::kConvWarps * 32) {
-        const uint4 codes = lds128(src + 16 * i);
-        const int row = i / kChunks, c = i % kChunks, half = c / 4, p = (c % 4) * 2;
-        uint4 lo, hi;
-        lo.x = e4m3x2_to_f16x2(codes.x & 0xffffu);
-        lo.y = e4m3x2_to_f16x2(codes.x >> 16);
-        lo.z = e4m3x2_to_f16x2(codes.y & 0xffffu);
-        lo.w = e4m3x2_to_f16x2(codes.y >> 16);
-        hi.x = e4m3x2_to_f16x2(codes.z & 0xffffu);
-        hi.y = e4m3x2_to_f16x2(codes.z >> 16);
-        hi.z = e4m3x2_to_f16x2(codes.w & 0xffffu);
-        hi.w = e4m3x2_to_f16x2(codes.w >> 16);
-        const uint32_t at = dst + half * C::kSub + row * 128;
-        // (the other half's lanes store their two chunks in the other order: no bank twice)
-        const int p0 = half ? p + 1 : p, p1 = half ? p : p + 1;
-        sts128(at + ((p0 ^ (row & 7)) << 4), half ? hi : lo);
-        sts128(at + ((p1 ^ (row & 7)) << 4), half ? lo : hi);
-      }
-      fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bar(kFull + f % C::kSlots));
-        mbar_arrive(bar(kRawEmpty + f % 2));
+    } else {
+      // ================================================================ codes to f16
+      const int ct = tid - kConvWarp * 32;
+      for (int f = 0;; ++f) {
+        // the next fill, or the end
+        const uint64_t since = global_ns();
+        bool got = false, end = false;
+        while (!got && !end) {
+          got = mbar_try_wait(bar(kRawFull + f % 2), (f / 2) & 1);
+          if (!got) {
+            end = f >= *reinterpret_cast<volatile int*>(&sm.raw_end) || *dead;
+            if (!end && global_ns() - since > ka.wait_limit_ns) {
+              *dead = 1;
+              atomicOr(a.status, kStatusTimeout);
+              end = true;
+            }
+          }
+        }
+        if (!__all_sync(0xffffffffu, got)) break;
+        if (f >= C::kSlots && !wait_warp(kEmpty + f % C::kSlots, f / C::kSlots - 1)) break;
+        const uint32_t src = raw + (f % 2) * C::kRaw, dst = slot_at(f);
+        constexpr int kChunks = D / 16;      // 16 codes each, of a row
+#pragma unroll 4
+        for (int i = ct; i < kTile * kChunks; i += C::kConvWarps * 32) {
+          const uint4 codes = lds128(src + 16 * i);
+          const int row = i / kChunks, c = i % kChunks, half = c / 4, p = (c % 4) * 2;
+          uint4 lo, hi;
+          lo.x = e4m3x2_to_f16x2(codes.x & 0xffffu);
+          lo.y = e4m3x2_to_f16x2(codes.x >> 16);
+          lo.z = e4m3x2_to_f16x2(codes.y & 0xffffu);
+          lo.w = e4m3x2_to_f16x2(codes.y >> 16);
+          hi.x = e4m3x2_to_f16x2(codes.z & 0xffffu);
+          hi.y = e4m3x2_to_f16x2(codes.z >> 16);
+          hi.z = e4m3x2_to_f16x2(codes.w & 0xffffu);
+          hi.w = e4m3x2_to_f16x2(codes.w >> 16);
+          const uint32_t at = dst + half * C::kSub + row * 128;
+          // (the other half's lanes store their two chunks in the other order: no bank twice)
+          const int p0 = half ? p + 1 : p, p1 = half ? p : p + 1;
+          sts128(at + ((p0 ^ (row & 7)) << 4), half ? hi : lo);
+          sts128(at + ((p1 ^ (row & 7)) << 4), half ? lo : hi);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(kFull + f % C::kSlots));
+          mbar_arrive(bar(kRawEmpty + f % 2));
+        }
       }
     }
-  }
   } else {
     // ================================================================ softmax
     regs_up<C::kSoftmaxRegs>();
@@ -1008,7 +1020,7 @@ prefill_kernel(const __grid_constant__ Args ka) {
         const bool start = t == tiles.x, edge = t < full_lo || t >= full_hi || valid != 0xffu;
         const float v_big = FP8 ? mt.v_big : 0.f;
         // columns [jl, jh) of the tile are this row's, those of valid pages
-        const int jh = pos + 1 - p0, jl = a.window > 0 ? max(pos - a.window + 1 - p0, 0) : 0;
+        const int jh = pos + 1 - p0, jl = a.window > 0 ? max(max(pos, 0) - a.window + 1 - p0, 0) : 0;
         auto below = [](int j) { return j <= 0 ? 0u : j >= 32 ? ~0u : (1u << j) - 1u; };
         auto word = [&](int c) {           // of columns 32c .. 32c + 31
           const unsigned pages = ((valid >> (2 * c)) & 1u ? 0xffffu : 0u) |
@@ -1349,7 +1361,7 @@ cudaError_t launch(const PrefillArgs& args, cudaStream_t s) {
   // scale 0: every score counts alike, and a masked one still gets the weight 0
   const float sl2 = args.scale * 1.4426950408889634f;
   k.sl2 = fabsf(sl2) > 1e-30f ? sl2 : 1e-30f;
-  k.wait_limit_ns = kWaitLimitNs;
+  k.wait_limit_ns = args.wait_limit_ns;
   // an item of up to 2 kSnap tiles is never cut: every place in it is that near a border
   const bool cuts = args.max_context_len > 2 * kSnap * kTile;
   for (int b0 = 0; b0 < args.B; b0 += kMaxSeqs) {

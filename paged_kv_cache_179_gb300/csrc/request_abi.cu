@@ -5,6 +5,7 @@
 
 #include "pa_launch.h"
 #include "pa_request.h"
+#include "pa_request_test.h"
 #include "request_launch.h"
 
 using namespace pa;
@@ -30,6 +31,9 @@ int prefill(PrefillArgs a, int block_size, int dtype, size_t workspace_bytes, bo
   if (a.group > 32) return PA_ERR_UNSUPPORTED;
   if (a.B > 65535 || a.Hkv > 65535 || a.max_context_len > kMaxContext) return PA_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(a.T) * a.Hq > (1 << 30)) return PA_ERR_UNSUPPORTED;
+  // a 16-bit pool's (block, kv head) tiles are coordinates of its tensor map
+  if (!fp8 && static_cast<int64_t>(a.num_blocks) * a.Hkv > INT_MAX) return PA_ERR_UNSUPPORTED;
+  if (a.window >= a.max_context_len) a.window = 0;   // the whole context
   if (!a.out || !a.q || !a.k_cache || !a.v_cache || !a.block_tables || !a.context_lens || !a.starts)
     return PA_ERR_INVALID_ARG;
   for (const void* p : {static_cast<const void*>(a.out), a.q, a.k_cache, a.v_cache})
@@ -116,6 +120,8 @@ int pa_prefill(void* out, const void* q, int64_t q_stride, const void* k_cache,
   a.max_context_len = max_context_len;
   a.window = window_size;
   a.scale = scale;
+  a.wait_limit_ns = kWaitLimitNs;
+  a.drop_tile = -1;
   return prefill(a, block_size, dtype, workspace_bytes, false, stream);
 }
 
@@ -149,7 +155,42 @@ int pa_prefill_fp8(void* out, const void* q, int64_t q_stride, const uint8_t* k_
   a.max_context_len = max_context_len;
   a.window = window_size;
   a.scale = scale;
+  a.wait_limit_ns = kWaitLimitNs;
+  a.drop_tile = -1;
   return prefill(a, block_size, dtype, workspace_bytes, true, stream);
+}
+
+int pa_test_prefill_timeout(void* out, const void* q, int64_t q_stride, const void* k_cache,
+                            const void* v_cache, const int32_t* block_tables,
+                            int max_blocks_per_seq, const int32_t* context_lens,
+                            int max_context_len, const int32_t* query_starts, int num_tokens,
+                            int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                            int num_blocks, float scale, int dtype, int drop_tile,
+                            uint64_t limit_ns, void* workspace, size_t workspace_bytes, void* stream) {
+  if (limit_ns == 0 || limit_ns > kWaitLimitNs) return PA_ERR_INVALID_ARG;
+  if (num_seqs <= 0 || num_tokens <= 0 || drop_tile < 0) return PA_ERR_INVALID_ARG;
+  PrefillArgs a{};
+  a.out = out;
+  a.q = q;
+  a.q_stride = q_stride;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.starts = query_starts;
+  a.workspace = workspace;
+  a.mbs = max_blocks_per_seq;
+  a.T = num_tokens;
+  a.B = num_seqs;
+  a.Hq = num_q_heads;
+  a.Hkv = num_kv_heads;
+  a.D = head_dim;
+  a.num_blocks = num_blocks;
+  a.max_context_len = max_context_len;
+  a.scale = scale;
+  a.wait_limit_ns = limit_ns;
+  a.drop_tile = drop_tile;
+  return prefill(a, 16, dtype, workspace_bytes, false, stream);
 }
 
 int pa_alloc_pages(int32_t* block_tables, int max_blocks_per_seq, int32_t* num_pages,

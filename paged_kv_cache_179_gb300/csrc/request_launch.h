@@ -28,6 +28,8 @@ struct PrefillArgs {
   unsigned* status;
   int mbs, T, B, Hq, Hkv, group, D, num_blocks, max_context_len, window;
   float scale;
+  uint64_t wait_limit_ns;      // time limit of every wait
+  int drop_tile;               // a test's: this tile of each CTA's is not copied (-1: none)
 };
 size_t prefill_workspace_bytes(int B, int T, int Hq, int Hkv, int D);
 cudaError_t launch_prefill(const PrefillArgs& a, bool fp8, bool bf16, cudaStream_t s);

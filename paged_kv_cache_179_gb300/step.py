@@ -64,6 +64,7 @@ class DecodeStep:
                                                   k_cache.device, query_rows=rows)
         self._bound = {}     # run_from_staging's bound steps
         self._weights_ws = {}   # accumulate's workspaces
+        self._prefill_ws = None   # prefill's
 
     def append(self, k_new, v_new, slot_mapping):
         if self.kv == "fp8":
@@ -83,6 +84,26 @@ class DecodeStep:
                            self.context_lens, self.max_context_len, self.scale,
                            self.split_ctas, self.workspace, window=self.window,
                            early_prologue=self.early_prologue, early_copies=self.early_copies)
+
+    def prefill(self, q, out, query_starts):
+        """The attention of each sequence's last query tokens, q[query_starts[b]:
+        query_starts[b + 1]] (int32 [B + 1]; q and out [T][Hq][D]), over its cached
+        context: a prompt or a chunk of one, any number of tokens for each sequence,
+        whose keys and values have been appended (``append``, ``rope_append``).  The first
+        call allocates the workspace, so it cannot be one that is captured; calls share
+        it and must not overlap on the device."""
+        if self._prefill_ws is None:
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("prefill: make a call before the capture, it allocates the workspace")
+            self._prefill_ws = _abi.alloc_prefill_workspace(self.B, q.shape[0], self.Hq, self.Hkv,
+                                                            self.D, self.k_cache.device)
+        args = (self.block_tables, self.context_lens, self.max_context_len, query_starts,
+                self.scale, self._prefill_ws)
+        if self.kv == "fp8":
+            _abi.pa_prefill_fp8(out, q, self.k_cache, self.v_cache, self.k_scale, self.v_scale, *args,
+                                window=self.window)
+        else:
+            _abi.pa_prefill(out, q, self.k_cache, self.v_cache, *args, window=self.window)
 
     def rope_append(self, q_out, q, k_new, v_new, slot_mapping, positions, spec):
         """``append`` with rotary positions, in one launch: q rotated into q_out, k

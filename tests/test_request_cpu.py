@@ -58,9 +58,26 @@ def test_prefill_refusals(lib):
         for bad in (dict(ws=None), dict(ws=FAKE + 16)):
             assert call(fp8, **bad) == WSP, bad
     assert call(True, ks=None) == INV and call(True, vs=FAKE + 2) == INV
+    assert call(NB=2 ** 30) == UNS                                # 2^31 tiles
     f = lib.pa_prefill_workspace_size
     assert f(2, 10, 7, 2, 64) == 0 and f(-1, 10, 8, 2, 64) == 0 and f(2, 10, 8, 2, 80) == 0
     assert f(2, 10, 66, 2, 64) == 0
+
+
+def test_failure_path_header_and_refusals(lib):
+    text = open(os.path.join(ROOT, "include", "pa_request_test.h")).read()
+    text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
+    names = sorted(set(re.findall(r"\b(pa_test_[a-z0-9_]+)\s*\(", text)))
+    assert sorted(_abi.REQUEST_TEST_SIGNATURES) == names and len(names) == 1
+    decl = re.search(names[0] + r"\s*\((.*?)\);", text, flags=re.S).group(1)
+    assert len(_abi.REQUEST_TEST_SIGNATURES[names[0]][0]) == len(decl.split(","))
+
+    def call(limit, T=10, B=2, drop=0):
+        return lib.pa_test_prefill_timeout(FAKE, 2 * FAKE, 512, FAKE, FAKE, FAKE, 8, FAKE, 128, FAKE, T, B, 8, 2,
+                                           64, 32, .125, 0, drop, limit, None, 0, None)
+    assert call(0) == INV and call(2 * 10 ** 9 + 1) == INV and call(1000, T=0) == INV and call(1000, B=0) == INV
+    assert call(1000, drop=-1) == INV
+    assert call(1000) == WSP
 
 
 def test_page_refusals(lib):
