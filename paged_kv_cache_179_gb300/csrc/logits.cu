@@ -21,12 +21,11 @@
 // waits for other CTAs then.
 //
 // Bound by memory where there are many rows, by latency where there are few.  Measured on a
-// GB300, rows of 128000 bf16 logits to fp32 probabilities: 512 rows with histories of 300
-// tokens 146 us (2.7 TB/s of the logits read once and the probabilities written), of 4096
-// tokens 184 us: the histories' insertion, and two rounds of two CTAs an SM, are what
-// separates them from the 58 us of a copy of those bytes.  The cluster form takes 212 and
-// 248 us there.  At 152 rows: 60 against 81 us, 78 against 95 with the long histories.
-// One row of 32000 fp32 logits: 6 us.
+// GB300, rows of 128000 bf16 logits to fp32 probabilities, biases and a grammar's mask: 512
+// rows with histories of 4096 tokens 149 us, 2.7 TB/s of what is read and written once (a
+// copy of those bytes would take 59 us): 35 us are the histories' insertion, the rest two
+// rounds of two CTAs an SM.  The same by clusters takes 310 us.  To logits 79 us.  One
+// row of 32000 fp32 logits: 6 us.
 //
 // Counts are integers, and a token's biases are added in their order, so results
 // do not depend on the order of execution.
@@ -353,12 +352,20 @@ logits_kernel(const LogitsArgs a, int slice, int rows_per_unit) {
 constexpr int kStreamThreads = 512;
 constexpr int kStreamSlots = 8192;                 // of the hash table, at most
 constexpr int kStreamKnown = kStreamSlots * 3 / 4;   // tokens that it takes
-constexpr int kStreamSteps = 8;                    // loads in flight
+constexpr int kStreamSteps = 4;                    // loads in flight, of 16 bytes each
+template <typename T>
+constexpr int kStreamVec = 16 / static_cast<int>(sizeof(T));
+template <typename T>
+struct alignas(16) Wide {
+  T v[kStreamVec<T>];
+};
 
 template <typename T, bool PROBS>
 __global__ void __launch_bounds__(kStreamThreads, 2)
 stream_kernel(const LogitsArgs a, int log_slots) {
   using O = std::conditional_t<PROBS, float, T>;
+  constexpr int kVec = kStreamVec<T>, kSteps = kStreamSteps;
+  constexpr unsigned kAll = (1u << kVec) - 1u;
   constexpr int kWarps = kStreamThreads / 32, kChunk = kStreamThreads * kVec;
   extern __shared__ __align__(16) unsigned known[];   // a bit a token, then the table
   __shared__ int bias_t[kLogitsMaxBias];
@@ -378,10 +385,16 @@ stream_kernel(const LogitsArgs a, int log_slots) {
     reinterpret_cast<uint4*>(vals)[j] = make_uint4(0u, 0u, 0u, 0u);
   }
   __syncthreads();
-  auto slot_of = [&](int t) {                      // (more slots than tokens: one is found)
+  // A token's slot (more slots than tokens: one is found).  Most tokens of a text are there
+  // already, so a slot is read before it is asked for.
+  auto slot_of = [&](int t) {
     unsigned h = (static_cast<unsigned>(t) * 2654435761u) >> (32 - log_slots);
     for (;;) {
-      const int k = atomicCAS(keys + h, -1, t);
+      int k = *reinterpret_cast<volatile int*>(keys + h);
+      if (k == -1) {
+        k = atomicCAS(keys + h, -1, t);
+        if (k == -1) atomicOr(known + (t >> 5), 1u << (t & 31));
+      }
       if (k == -1 || k == t) return h;
       h = (h + 1) & (slots - 1);
     }
@@ -392,7 +405,6 @@ stream_kernel(const LogitsArgs a, int log_slots) {
   };
   auto add = [&](int t, bool prompt) {
     if (!valid(t)) return;
-    atomicOr(known + (t >> 5), 1u << (t & 31));
     unsigned* v = vals + slot_of(t);
     if (prompt) atomicOr(v, kInPrompt);
     else atomicAdd(v, 1u);
@@ -422,7 +434,6 @@ stream_kernel(const LogitsArgs a, int log_slots) {
     bias_t[j] = t;
     bias_v[j] = sp.bias_values[static_cast<int64_t>(b) * sp.num_bias + j];
     if (!valid(t)) continue;
-    atomicOr(known + (t >> 5), 1u << (t & 31));
     atomicOr(vals + slot_of(t), kHasBias);
   }
   const Penalties pen(sp, b);
@@ -450,34 +461,51 @@ stream_kernel(const LogitsArgs a, int log_slots) {
     }
   };
   // ---- the known tokens
-  for (int j = tid; j < slots; j += kStreamThreads) {
-    const int t = keys[j];
-    if (t < 0) continue;
-    float x = pen.adjust(to_f32(in[t]), vals[j], t, bias_t, bias_v, sp.num_bias);
-    if (allowed != nullptr && !((allowed[t >> 5] >> (t & 31)) & 1u)) x = -INFINITY;
-    vals[j] = __float_as_uint(x);
-    if (PROBS) take(x, t);
+  for (int j0 = tid; j0 < slots; j0 += 8 * kStreamThreads) {   // eight loads in flight
+    int key[8];
+    T v[8];
+    unsigned ok[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) key[u] = j0 + u * kStreamThreads < slots ? keys[j0 + u * kStreamThreads] : -1;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int t = max(key[u], 0);
+      v[u] = in[t];
+      ok[u] = allowed != nullptr ? allowed[t >> 5] >> (t & 31) : 1u;
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      if (key[u] < 0) continue;
+      unsigned* w = vals + j0 + u * kStreamThreads;
+      const float x = ok[u] & 1u ? pen.adjust(to_f32(v[u]), *w, key[u], bias_t, bias_v, sp.num_bias) : -INFINITY;
+      *w = __float_as_uint(x);
+      if (PROBS) take(x, key[u]);
+    }
   }
   __syncthreads();                                 // (in place, the rest is written over them)
-  // ---- the rest: kStreamSteps loads in flight, none of them behind a branch
+  // ---- the rest: kSteps loads in flight, none of them behind a branch
   const int last = (a.V - kVec) & ~(kVec - 1);
-  auto load = [&](int t0, Pack<T> (&raw)[kStreamSteps], unsigned (&bits)[kStreamSteps]) {
+  auto load = [&](int t0, bool again, Wide<T> (&raw)[kSteps], unsigned (&bits)[kSteps]) {
 #pragma unroll
-    for (int k = 0; k < kStreamSteps; ++k)
-      raw[k] = *reinterpret_cast<const Pack<T>*>(in + min(t0 + k * kChunk, last));
+    for (int k = 0; k < kSteps; ++k) {
+      const uint4* at = reinterpret_cast<const uint4*>(in + min(t0 + k * kChunk, last));
+      // (a row that is read a second time is not needed any more)
+      const uint4 x = again ? __ldcs(at) : *at;
+      raw[k] = reinterpret_cast<const Wide<T>&>(x);
+    }
 #pragma unroll
-    for (int k = 0; k < kStreamSteps; ++k) {       // bit j: token t + j is there and allowed
+    for (int k = 0; k < kSteps; ++k) {             // bit j: token t + j is there and allowed
       const int t = t0 + k * kChunk, at = min(t, last);
-      bits[k] = (allowed != nullptr ? allowed[at >> 5] >> (at & 31) : 0xfu) & (t <= last ? 0xfu : 0u);
+      bits[k] = (allowed != nullptr ? allowed[at >> 5] >> (at & 31) : kAll) & (t <= last ? kAll : 0u);
     }
   };
   if (PROBS) {
-    for (int t0 = tid * kVec; t0 < a.V; t0 += kStreamSteps * kChunk) {
-      Pack<T> raw[kStreamSteps];
-      unsigned bits[kStreamSteps];
-      load(t0, raw, bits);
+    for (int t0 = tid * kVec; t0 < a.V; t0 += kSteps * kChunk) {
+      Wide<T> raw[kSteps];
+      unsigned bits[kSteps];
+      load(t0, false, raw, bits);
 #pragma unroll
-      for (int k = 0; k < kStreamSteps; ++k) {
+      for (int k = 0; k < kSteps; ++k) {
         const int t = t0 + k * kChunk;
         const unsigned ok = bits[k] & ~(known[min(t, last) >> 5] >> (t & 31));
         float x[kVec], top = -INFINITY;
@@ -496,8 +524,10 @@ stream_kernel(const LogitsArgs a, int log_slots) {
           m = top;
         }
         if (m > -INFINITY) {
+          float part[2] = {0.f, 0.f};
 #pragma unroll
-          for (int j = 0; j < kVec; ++j) sum += fast_exp2((x[j] - m) * c);
+          for (int j = 0; j < kVec; ++j) part[j & 1] += fast_exp2((x[j] - m) * c);
+          sum += part[0] + part[1];
         }
       }
     }
@@ -541,19 +571,33 @@ stream_kernel(const LogitsArgs a, int log_slots) {
     if (!(x > -INFINITY)) return 0.f;              // (a NaN counts as -inf)
     return x == m ? scale : fast_exp2((x - m) * c) * scale;
   };
-  for (int t0 = tid * kVec; t0 < a.V; t0 += kStreamSteps * kChunk) {
-    Pack<T> raw[kStreamSteps];
-    unsigned bits[kStreamSteps];
-    load(t0, raw, bits);
+  const bool plain = !greedy && fabsf(m) < INFINITY;   // exp(0) at the maximum, 0 at -inf
+  for (int t0 = tid * kVec; t0 < a.V; t0 += kSteps * kChunk) {
+    Wide<T> raw[kSteps];
+    unsigned bits[kSteps];
+    load(t0, PROBS, raw, bits);
 #pragma unroll
-    for (int k = 0; k < kStreamSteps; ++k) {
+    for (int k = 0; k < kSteps; ++k) {
       const int t = t0 + k * kChunk;
       if (t > last) continue;
-      Pack<O> p;
+      struct alignas(16) {
+        O v[kVec];
+      } r;
+      if (PROBS && plain) {
 #pragma unroll
-      for (int j = 0; j < kVec; ++j)
-        from_f32(result((bits[k] >> j) & 1u ? to_f32(raw[k].v[j]) : -INFINITY, t + j), &p.v[j]);
-      *reinterpret_cast<Pack<O>*>(out + t) = p;
+        for (int j = 0; j < kVec; ++j) {           // (fmaxf: a NaN counts as -inf)
+          const float x = (bits[k] >> j) & 1u ? fmaxf(to_f32(raw[k].v[j]), -INFINITY) : -INFINITY;
+          from_f32(fast_exp2((x - m) * c) * scale, &r.v[j]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j)
+          from_f32(result((bits[k] >> j) & 1u ? to_f32(raw[k].v[j]) : -INFINITY, t + j), &r.v[j]);
+      }
+      // (past what the other rows read again)
+#pragma unroll
+      for (int j = 0; j < static_cast<int>(sizeof(r) / 16); ++j)
+        __stcs(reinterpret_cast<uint4*>(out + t) + j, reinterpret_cast<const uint4*>(&r)[j]);
     }
   }
   for (int t = last + kVec + tid; t < a.V; t += kStreamThreads) {
@@ -606,10 +650,14 @@ cudaError_t launch_type(const LogitsArgs& a, bool probs, cudaStream_t s) {
   // rows that begin at a multiple of kVec elements are read kVec at a time
   const bool wide = a.V >= kVec && (a.in_stride % kVec) == 0 && (a.out_stride % kVec) == 0 &&
                     reinterpret_cast<uintptr_t>(a.out) % (out_size * kVec) == 0;
-  // tokens that something may be known of in a row; from a row an SM on a CTA makes a row
-  // by itself (152 rows to logits: 31 us, by clusters 51)
+  // tokens that something may be known of in a row
   const int64_t known = (a.spec.history != nullptr ? a.spec.history_stride : 0) + a.spec.num_bias + a.rows;
-  if (wide && static_cast<int64_t>(a.B) * a.rows >= 152 && known <= kStreamKnown)
+  // From a row for every second SM on (third, for logits) a CTA makes a row by itself.  Rows of
+  // 128000 bf16 logits with histories of 4096 tokens, by clusters and by a CTA a row: to
+  // probabilities 64 rows 50 and 57 us, 96 rows 72 and 58; to logits 32 rows 19 and 30 us,
+  // 64 rows 35 and 30.
+  const bool aligned = a.V >= kStreamVec<T> && a.in_stride * sizeof(T) % 16 == 0 && a.out_stride * out_size % 16 == 0;
+  if (aligned && static_cast<int64_t>(a.B) * a.rows >= (probs ? 76 : 48) && known <= kStreamKnown)
     return probs ? launch_stream<T, true>(a, known, s) : launch_stream<T, false>(a, known, s);
   // as few CTAs a row as hold it, more where there are not enough rows for the SMs
   const int blocks = (a.V + 127) / 128;
