@@ -29,26 +29,6 @@
 namespace pa {
 namespace {
 
-// These calls are short and follow one another: each kernel is launched while the one before
-// it on the stream still runs, and waits for its end before it touches memory.
-cudaLaunchAttribute after_previous() {
-  cudaLaunchAttribute a{};
-  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  a.val.programmaticStreamSerializationAllowed = 1;
-  return a;
-}
-template <typename... P, typename... A>
-cudaError_t launch_after(void (*kern)(P...), unsigned grid, unsigned threads, cudaStream_t s, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1] = {after_previous()};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
 constexpr int kScanThreads = 1024;
 constexpr int kScanWarps = kScanThreads / 32;
 constexpr int kScanCtas = 8;                       // a portable cluster, for larger pools
@@ -588,14 +568,14 @@ cudaError_t launch_alloc_pages(const TakeArgs& a, cudaStream_t s) { return launc
 cudaError_t launch_free_pages(int32_t* tables, int mbs, int32_t* num_pages, int num_rows,
                               const int32_t* rows, int items, int32_t* ref_counts, int num_blocks,
                               unsigned* status, cudaStream_t s) {
-  return launch_after(free_kernel, static_cast<unsigned>(items), kFreeThreads, s, tables, mbs, num_pages,
+  return launch_after(free_kernel, dim3(static_cast<unsigned>(items)), kFreeThreads, 0, s, tables, mbs, num_pages,
                       num_rows, rows, ref_counts, num_blocks, status);
 }
 
 cudaError_t launch_fork_pages(const TakeArgs& a, int32_t* context_lens, const PagePools& p,
                               cudaStream_t s) {
   if (const cudaError_t e = launch_take<true>(a, s)) return e;
-  return launch_after(fork_kernel, static_cast<unsigned>(a.items), kForkThreads, s, a, context_lens, p);
+  return launch_after(fork_kernel, dim3(static_cast<unsigned>(a.items)), kForkThreads, 0, s, a, context_lens, p);
 }
 
 size_t compact_workspace_bytes(int num_blocks) {
@@ -617,7 +597,7 @@ cudaError_t launch_compact_pages(const CompactArgs& a, const PagePools& p, cudaS
   cfg.numAttrs = one ? 1 : 2;
   auto* plan = one ? compact_plan_kernel<1> : compact_plan_kernel<kScanCtas>;
   if (const cudaError_t e = cudaLaunchKernelEx(&cfg, plan, a)) return e;
-  return launch_after(compact_move_kernel, static_cast<unsigned>(device_sm_count()) * 8, kMoveThreads, s, a, p);
+  return launch_after(compact_move_kernel, dim3(static_cast<unsigned>(device_sm_count()) * 8), kMoveThreads, 0, s, a, p);
 }
 
 }  // namespace pa

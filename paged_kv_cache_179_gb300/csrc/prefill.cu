@@ -335,6 +335,7 @@ prefill_kernel(const __grid_constant__ Args ka) {
   };
   auto wait_warp = [&](int b, int n) { return __all_sync(0xffffffffu, wait(b, n)); };
 
+  griddep_wait();
   // ---- 1. the items' lengths, and this CTA's share of them
   {
     Setup& su = *reinterpret_cast<Setup*>(smem);
@@ -1265,6 +1266,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Args
   const PrefillArgs& a = ka.a;
   const int w = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int* head = ka.ws_head + w * kHeader;
+  griddep_wait();
   if (!head[kHasTail]) return;
   const int t0 = head[kTailT0], h = head[kTailH], tokens = head[kTailTokens];
   const int row = blockIdx.y * kMergeRows + lane, s = row / kTile, r = row % kTile;
@@ -1401,11 +1403,11 @@ cudaError_t launch(const PrefillArgs& args, cudaStream_t s) {
     k.a.block_tables = args.block_tables + static_cast<int64_t>(b0) * args.mbs;
     k.a.context_lens = args.context_lens + b0;
     k.a.starts = args.starts + b0;
-    kern<<<grid, C::kThreads, smem, s>>>(k);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = launch_after(kern, dim3(static_cast<unsigned>(grid)), C::kThreads, smem, s, k);
+    if (e != cudaSuccess) return e;
     if (!cuts) continue;
-    merge_kernel<D, BF16><<<dim3(static_cast<unsigned>(grid), 256 / kMergeRows), 256, 0, s>>>(k, grid);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = launch_after(merge_kernel<D, BF16>, dim3(static_cast<unsigned>(grid), 256 / kMergeRows), 256, 0, s, k, grid);
+    if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
 }

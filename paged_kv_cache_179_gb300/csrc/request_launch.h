@@ -32,6 +32,28 @@ struct PrefillArgs {
   int drop_tile;               // a test's: this tile of each CTA's is not copied (-1: none)
 };
 size_t prefill_workspace_bytes(int B, int T, int Hq, int Hkv, int D);
+// Calls of these kernels follow one another: each is launched while the one before it on the
+// stream still ends, and waits for that end before it touches memory (griddep_wait).
+inline cudaLaunchAttribute after_previous() {
+  cudaLaunchAttribute a{};
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  return a;
+}
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kern)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s,
+                         const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1] = {after_previous()};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 cudaError_t launch_prefill(const PrefillArgs& a, bool fp8, bool bf16, cudaStream_t s);
 
 // --------------------------------------------------------------------- pages
