@@ -139,6 +139,7 @@ logits_kernel(const LogitsArgs a, int slice, int rows_per_unit) {
   for (int j = tid; j < slice / 4; j += THREADS)
     reinterpret_cast<uint4*>(seen)[j] = make_uint4(0u, 0u, 0u, 0u);
   if (tid == 0) n_bias = 0;
+  griddep_wait();                                  // (nothing of memory was touched before)
   __syncthreads();
   auto add = [&](int t, bool prompt) {
     if (t >= a.V) {
@@ -384,6 +385,7 @@ stream_kernel(const LogitsArgs a, int log_slots) {
     reinterpret_cast<int4*>(keys)[j] = make_int4(-1, -1, -1, -1);
     reinterpret_cast<uint4*>(vals)[j] = make_uint4(0u, 0u, 0u, 0u);
   }
+  griddep_wait();                                  // (nothing of memory was touched before)
   __syncthreads();
   // A token's slot (more slots than tokens: one is found).  Most tokens of a text are there
   // already, so a slot is read before it is asked for.
@@ -618,8 +620,7 @@ cudaError_t launch_stream(const LogitsArgs& a, int64_t known, cudaStream_t s) {
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (kLogitsMaxVocab + 127) / 128 * 16 + kStreamSlots * 8);
   if (e != cudaSuccess) return e;
-  kern<<<static_cast<unsigned>(a.B * a.rows), kStreamThreads, smem, s>>>(a, log_slots);
-  return cudaGetLastError();
+  return launch_after(kern, dim3(static_cast<unsigned>(a.B * a.rows)), kStreamThreads, smem, s, a, log_slots);
 }
 
 template <typename T, bool PROBS, bool WIDE, int THREADS>
@@ -635,12 +636,13 @@ cudaError_t launch(const LogitsArgs& a, int C, int slice, int rows_per_unit, cud
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = static_cast<size_t>(slice) * 4;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(C);
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0] = after_previous();
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(C);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, a, slice, rows_per_unit);
 }
 
