@@ -13,11 +13,11 @@
 //
 // Latency bounds them, the pages' copies excepted: the counts of a pool of 577k pages are
 // 2.3 MB, read once from memory and, where pages are taken, again from L2.  Measured on
-// a GB300: 64 rows given back and 256 served from that pool 26 us (two launches; 85 with
+// a GB300: 64 rows given back and 256 served from that pool 20 us (two launches; 85 with
 // contiguous parts of the pool for the warps and one load in flight); the same in a pool
-// of 64 pages 8 us; 96 forks with their copies, after 96 rows are given back, 16 us;
+// of 64 pages 8 us; 96 forks with their copies, after 96 rows are given back, 14 us;
 // compaction of 16384 pages, half of them live (132 MB of copies and tables), 28 us,
-// 4.7 TB/s; of 49001 E4M3 pages (341 MB) 65 us, 5.3 TB/s, 78 % of a plain copy's rate.
+// 4.7 TB/s; of 49001 E4M3 pages (341 MB) 62 us, 5.5 TB/s, 81 % of a plain copy's rate.
 #include <algorithm>
 #include <climits>
 
@@ -31,11 +31,12 @@ namespace {
 
 constexpr int kScanThreads = 1024;
 constexpr int kScanWarps = kScanThreads / 32;
-constexpr int kScanCtas = 8;                       // a portable cluster, for larger pools
-// Up to this many pages one CTA ranks by itself: 4 pages a lane, and no cluster's barriers
-// (a fork of four beams in a small pool: 10 us for the call and the free before it, 14 with
-// the cluster; beyond, the cluster reads the counts in an eighth of the rounds).
-constexpr int kOneCtaPages = 4096;
+constexpr int kScanCtas = 16;                      // a cluster, for larger pools
+// Up to so many pages one CTA ranks by itself, without a cluster's barriers.  64 rows served
+// and given back, by one CTA and by a cluster: 11.7 and 13.0 us in 4096 pages, 12.0 and 13.1
+// in 16384, 15.4 and 13.4 in 32768.  A compaction that moves nothing: 6.0 and 6.5 us of 4096
+// pages, 8.2 and 6.5 of 8192.  (Clusters of 8 take 14.5 us instead of 10.7 for 131072.)
+constexpr int kOneCtaTake = 16384, kOneCtaCompact = 4096;
 // Where items' pages go is kept in shared memory for up to this many items.
 constexpr int kKeptItems = 8192;
 constexpr unsigned kMany = (1u << 30) + 1u;        // sums of needs saturate above any pool
@@ -342,12 +343,16 @@ cudaError_t launch_take(const TakeArgs& a, cudaStream_t s) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = CTAS > 1 ? 2 : 1;
+  if (CTAS > 1) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
   return cudaLaunchKernelEx(&cfg, kern, a);
 }
 template <bool FORK>
 cudaError_t launch_take(const TakeArgs& a, cudaStream_t s) {
   static_assert(kKeptItems * 12 + 16 <= (kPagesMaxItems + 4) * 4, "one limit serves both layouts");
-  return a.num_blocks <= kOneCtaPages ? launch_take<FORK, 1>(a, s) : launch_take<FORK, kScanCtas>(a, s);
+  return a.num_blocks <= kOneCtaTake ? launch_take<FORK, 1>(a, s) : launch_take<FORK, kScanCtas>(a, s);
 }
 
 // -------------------------------------------------------------------- giving back
@@ -583,7 +588,7 @@ size_t compact_workspace_bytes(int num_blocks) {
 }
 
 cudaError_t launch_compact_pages(const CompactArgs& a, const PagePools& p, cudaStream_t s) {
-  const bool one = a.num_blocks <= kOneCtaPages;
+  const bool one = a.num_blocks <= kOneCtaCompact;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(one ? 1 : kScanCtas);
   cfg.blockDim = dim3(kScanThreads);
@@ -596,6 +601,10 @@ cudaError_t launch_compact_pages(const CompactArgs& a, const PagePools& p, cudaS
   cfg.attrs = attr;
   cfg.numAttrs = one ? 1 : 2;
   auto* plan = one ? compact_plan_kernel<1> : compact_plan_kernel<kScanCtas>;
+  if (!one) {
+    const cudaError_t e = cudaFuncSetAttribute(plan, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
   if (const cudaError_t e = cudaLaunchKernelEx(&cfg, plan, a)) return e;
   return launch_after(compact_move_kernel, dim3(static_cast<unsigned>(device_sm_count()) * 8), kMoveThreads, 0, s, a, p);
 }
