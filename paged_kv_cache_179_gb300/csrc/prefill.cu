@@ -21,11 +21,12 @@
 //   warp 11          copies V; or, warps 11-15, of E4M3 pools: codes to f16 (exact)
 //                    between two shared-memory rings.
 //
-// The softmax offset of a row is the maximum of an early tile's scores and moves only
-// when weights grow out of the products' range (kMaxSum): any standing offset gives the
-// same softmax.  So most tiles need no maximum: their weights are made at once, their
-// sum shows whether they may stand, and O is scaled in tensor memory hardly ever.  The
-// weights of a tile's first half are announced alone, and its product begins.
+// The softmax offset of a row is the maximum of an early tile's scores (the first of which
+// it sees a number) and moves only when weights grow out of the products' range (kMaxSum):
+// any standing offset gives the same softmax.  So once a warp's rows have theirs, most
+// tiles need no maximum: their weights are made at once, their sum shows whether they may
+// stand, and O is scaled in tensor memory hardly ever.  The weights of a tile's first half
+// are announced alone, and its product begins.
 //
 // What bounds it: a product of 128 x 128 x 16 takes 64 cycles (measured, alone; 65 to 80
 // with the softmax beside it), so a tile of both subtiles takes 2048 of the tensor
@@ -1000,8 +1001,10 @@ prefill_kernel(const __grid_constant__ Args ka) {
         // ---- a run of whole tiles: a loop of its own, as short as it can be.  The weights at
         // the standing offset do unless they have grown out of the products' range, which
         // their sum shows (a NaN too); then the exact form below takes over, from that half on.
+        // (A tile of which a row sees a number gives it its offset.  Its first one need not be the
+        // subtile's: a window may begin behind that, its pages may be invalid.)
         int from = 0;
-        bool more = t > tiles.x;           // (a row's first tile gives it its offset)
+        bool more = t > tiles.x && !__any_sync(0xffffffffu, row_live && off == -INFINITY);
         while (more) {
           if (!wait_warp(kSFull + w, s_n)) {
             ok = false;
