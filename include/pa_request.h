@@ -41,10 +41,12 @@ extern "C" {
  * over positions j up to its own, within the last window_size of them when that is
  * not 0.  Rounded once, to dtype.  A query before position 0 gets zeros, as
  * does one that sees no page with a valid id, and so do the queries of a
- * sequence whose context_len is out of bounds (PA_STATUS_BAD_LEN).  Tokens that
- * belong to no sequence (before query_starts[0], from query_starts[num_seqs]
- * on) are left as they were.  Starts that decrease or leave [0, num_tokens] set
- * PA_STATUS_BAD_LEN and their sequence's queries are left as they were.
+ * sequence whose context_len is out of bounds (PA_STATUS_BAD_LEN).  Pages of a
+ * sequence before the windows of all its queries are not looked at: their table
+ * entries may be anything.  Tokens that belong to no sequence (before
+ * query_starts[0], from query_starts[num_seqs] on) are left as they were.  Starts
+ * that decrease or leave [0, num_tokens] set PA_STATUS_BAD_LEN and their sequence's
+ * queries are left as they were.
  *   q: num_q_heads x head_dim dense elements a token, q_stride elements from one
  *   token to the next (a multiple of 8: a view of one projection's output);
  *   out: [num_tokens][num_q_heads][head_dim]; query_starts: int32

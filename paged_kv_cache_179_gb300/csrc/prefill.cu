@@ -123,7 +123,7 @@ struct Desc {                              // a piece, or the end (h < 0)
 };
 
 struct Meta {
-  unsigned valid;                          // bit j: page j of the tile has a valid id
+  unsigned valid;                          // bit j: page j of the tile is seen and has a valid id
   float ks[kPages], vs[kPages], v_big;     // E4M3 pools: the scales, V's largest
 };
 
@@ -263,6 +263,11 @@ __device__ __forceinline__ int item_units(int n, int L, int j, int sub, int wind
   if (last < 0) return 1;
   if (window > 0) *lo = max(0, first - window + 1) / kTile;
   return last / kTile + 1 - *lo;
+}
+// The first page that a query of a piece's item sees: those before it are behind every
+// window, and neither their ids nor their contents are looked at.
+__device__ __forceinline__ int first_page(const Desc& d, int window) {
+  return window > 0 ? max(0, d.L - d.n + d.i0 - window + 1) / 16 : 0;
 }
 // The tiles that subtile w of a piece sees, within the piece's.
 __device__ __forceinline__ int2 sub_tiles(const Desc& d, int w, int sub, int window) {
@@ -574,10 +579,10 @@ prefill_kernel(const __grid_constant__ Args ka) {
         // ---- its tiles: four tiles' page ids at a time, the next four on their way, and of
         // E4M3 pools the next tile's scales
         const int32_t* table = a.block_tables + static_cast<int64_t>(b) * a.mbs;
-        const int last_page = (L + 15) / 16 - 1;
+        const int p_lo = first_page(x, a.window), last_page = (L + 15) / 16 - 1;
         auto ids_at = [&](int t) {
           const int p = t * kPages + lane;
-          return p <= last_page && t + (lane >> 3) < x.k_hi ? table[p] : -1;
+          return p >= p_lo && p <= last_page && t + (lane >> 3) < x.k_hi ? table[p] : -1;
         };
         int ids = ids_at(x.k_lo), ids_next = ids_at(x.k_lo + 4), id = -1;
         float sk = 0.f, sv = 0.f;
@@ -589,7 +594,8 @@ prefill_kernel(const __grid_constant__ Args ka) {
             ids_next = ids_at(t + 4);
           }
           id = __shfl_sync(0xffffffffu, ids, in4 * 8 + (lane & 7));
-          const bool mine = t < x.k_hi && lane < kPages && t * kPages + lane <= last_page;
+          const int p = t * kPages + lane;
+          const bool mine = t < x.k_hi && lane < kPages && p >= p_lo && p <= last_page;
           valid = mine && id >= 0 && id < a.num_blocks;
           if (mine && !valid) atomicOr(a.status, kStatusBadBlock);
           if constexpr (FP8) {
@@ -815,12 +821,12 @@ prefill_kernel(const __grid_constant__ Args ka) {
         if (h < 0) break;
         const int k_lo = uniform(x.k_lo), k_hi = uniform(x.k_hi);
         const int32_t* table = a.block_tables + static_cast<int64_t>(x.b) * a.mbs;
-        const int last_page = (x.L + 15) / 16 - 1;
+        const int p_lo = first_page(x, a.window), last_page = (x.L + 15) / 16 - 1;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kDEmpty + d % kDescs));
         auto ids_at = [&](int t) {
           const int p = t * kPages + lane;
-          return p <= last_page && t + (lane >> 3) < k_hi ? table[p] : -1;
+          return p >= p_lo && p <= last_page && t + (lane >> 3) < k_hi ? table[p] : -1;
         };
         int ids = ids_at(k_lo), ids_next = ids_at(k_lo + 4);
         for (int t = k_lo; ok && t < k_hi; ++t, ++g) {

@@ -1,0 +1,36 @@
+"""pa_prefill and what none of a call's queries sees: pages before every window."""
+import pytest
+import torch
+
+from test_request_gpu import BF16, F16, Prompts, ok
+
+pytestmark = pytest.mark.gpu
+
+# context, new tokens, window: the first query's window begins inside a tile, its pages before
+# (L - n - window + 1) // 16 are behind every window
+BEHIND = [(1300, 20, 532), (1300, 20, 600), (700, 1, 100), (2600, 300, 1000), (300, 3, 40)]
+
+
+@pytest.mark.parametrize("G,D,dtype", [(1, 64, F16), (4, 128, BF16), (7, 128, F16), (8, 64, BF16)])
+@pytest.mark.parametrize("L,n,window", BEHIND)
+@pytest.mark.parametrize("fp8", [False, True])
+def test_pages_behind_every_window_are_not_looked_at(L, n, window, G, D, dtype, fp8):
+    """Their ids may be anything (a page that was given back), and what stands in one."""
+    gone = (L - n - window + 1) // 16
+    for bad in (-1, 10 ** 6):
+        p = Prompts([L], [n], 2 * G, 2, D, dtype, fp8, window)
+        p.tables[0, :gone] = bad
+        out = p.run()
+        ok()
+        p.check(out)
+    p = Prompts([L], [n], 2 * G, 2, D, dtype, fp8, window)
+    clean = Prompts([L], [n], 2 * G, 2, D, dtype, fp8, window)
+    ids = p.tables[0, :gone].long()
+    if fp8:
+        p.ks[ids], p.vs[ids] = float("nan"), 1e30
+        p.kc[ids] = p.vc[ids] = 0x7f
+    else:
+        p.kc[ids], p.vc[ids] = float("nan"), float("inf")
+    out = p.run()
+    ok()
+    clean.check(out)
