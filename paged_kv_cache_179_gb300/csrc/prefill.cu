@@ -39,7 +39,8 @@
 // 450 tokens of two prompts over 115k cached ones take 1.07 ms, 1.38 PFLOP/s, 73 %.
 //
 // Page scales: K's multiply the scores of their 16 columns, V's the weights (relative
-// to a power of two that follows the largest seen, so that P stays in f16's range).
+// to a power of two that follows the largest that the row has seen, so that P stays in
+// f16's range and a page that the row does not see has no say).
 //
 // The batch's items, each as long as its tiles, are laid end to end and cut into one
 // share a CTA; a cut within kSnap tiles of an item's border moves there.  An item that
@@ -932,6 +933,7 @@ prefill_kernel(const __grid_constant__ Args ka) {
       // rows behind the subtile's hold whatever was there: they ask for nothing
       const bool row_live = r < cnt * G;
       float off = -INFINITY, l = 0.f, ref = FP8 ? 0.f : 1.f;
+      [[maybe_unused]] float low_ref = 0.f;   // the lowest reference of the warp's rows
       float sl2 = ka.sl2;
       if (FP8 && BF16 && tiles.x < tiles.y) {
         // bf16 rows to f16, scaled by a power of two so that the row's largest element lies
@@ -989,7 +991,8 @@ prefill_kernel(const __grid_constant__ Args ka) {
           }
           sum[(j / 2) & 1] = add2(sum[(j / 2) & 1], e);
           if constexpr (FP8) {
-            const float u = mt.vs[page + j / 16] * inv_ref;
+            float u = mt.vs[page + j / 16] * inv_ref;
+            if (N == 32 && ((bits >> (j & 16)) & 0xffffu) == 0u) u = 0.f;   // (0 weights, whatever the scale)
             e = mul2(e, make_float2(u, u));
           }
           out[j / 2] = __uint_as_float(pack2<kMmaBf16>(e.x, e.y));
@@ -1017,7 +1020,7 @@ prefill_kernel(const __grid_constant__ Args ka) {
             break;
           }
           const Meta& mt = sm.meta[(x.g0 + t - x.k_lo) % kMetas];
-          if (t < full_lo || t >= full_hi || mt.valid != 0xffu || (FP8 && mt.v_big > 2.f * ref)) break;
+          if (t < full_lo || t >= full_hi || mt.valid != 0xffu || (FP8 && mt.v_big > 2.f * low_ref)) break;
           tc_fence_after();
           float v[kTile], p[32];
           tmem_ld<32>(ts, *reinterpret_cast<float (*)[32]>(v));
@@ -1059,7 +1062,6 @@ prefill_kernel(const __grid_constant__ Args ka) {
         const Meta& mt = sm.meta[g % kMetas];
         const unsigned valid = mt.valid;
         const bool start = t == tiles.x, edge = t < full_lo || t >= full_hi || valid != 0xffu;
-        const float v_big = FP8 ? mt.v_big : 0.f;
         // columns [jl, jh) of the tile are this row's, those of valid pages
         const int jh = pos + 1 - p0, jl = a.window > 0 ? max(max(pos, 0) - a.window + 1 - p0, 0) : 0;
         auto below = [](int j) { return j <= 0 ? 0u : j >= 32 ? ~0u : (1u << j) - 1u; };
@@ -1068,6 +1070,16 @@ prefill_kernel(const __grid_constant__ Args ka) {
                                  ((valid >> (2 * c + 1)) & 1u ? 0xffff0000u : 0u);
           return edge ? below(jh - 32 * c) & ~below(jl - 32 * c) & pages : ~0u;
         };
+        float v_big = 0.f;                 // the largest scale of V's pages that this row sees
+        if constexpr (FP8) {
+          if (edge) {
+#pragma unroll 1
+            for (int c = 0; c < kPages; ++c)
+              if ((word(c / 2) >> (c % 2 * 16)) & 0xffffu) v_big = fmaxf(v_big, mt.vs[c]);
+          } else {
+            v_big = mt.v_big;
+          }
+        }
         if (from == 1 && !wait_warp(kPVHalf + w, s_n - 1)) {   // (O changes below)
           ok = false;
           break;
@@ -1091,7 +1103,7 @@ prefill_kernel(const __grid_constant__ Args ka) {
           // this tile's; O (when it holds something) and the sum are scaled down to them.
           const bool move = start || (row_live && m > off + kSlack);
           const bool refer = FP8 && (v_big > 2.f * ref || !(ref > 0.f));
-          if (refer || __any_sync(0xffffffffu, move)) {
+          if (__any_sync(0xffffffffu, move || refer)) {
             float f = 1.f;
             if (move) {
               const float to_off = fmaxf(off, m);
@@ -1104,6 +1116,8 @@ prefill_kernel(const __grid_constant__ Args ka) {
               f *= ref > 0.f ? ref / top : 1.f;
               ref = top;
             }
+            if constexpr (FP8)
+              low_ref = __uint_as_float(__reduce_min_sync(0xffffffffu, row_live ? __float_as_uint(ref) : 0x7f800000u));
             if (!start) {
 #pragma unroll 1
               for (int c = 0; c < D / 16; ++c) {

@@ -1,4 +1,5 @@
-"""pa_prefill and what none of a call's queries sees: pages before every window."""
+"""pa_prefill and what none of a call's queries sees, or not the one at hand: pages before every
+window, and the scales of pages that other queries see."""
 import pytest
 import torch
 
@@ -34,3 +35,24 @@ def test_pages_behind_every_window_are_not_looked_at(L, n, window, G, D, dtype, 
     out = p.run()
     ok()
     clean.check(out)
+
+
+@pytest.mark.parametrize("factor", [2. ** 40, float("nan")])
+@pytest.mark.parametrize("G,D,dtype", [(1, 64, F16), (4, 128, BF16), (7, 128, F16), (8, 64, BF16)])
+@pytest.mark.parametrize("window", [0, 100])
+def test_scales_of_pages_that_a_query_does_not_see(window, G, D, dtype, factor):
+    """A page's scales reach the queries that see it.  Those before it (and, with a window,
+    those past it) get what they would get from any other page in its place."""
+    for at in (5, 11, 20):
+        case = ([500, 64], [500, 64], 2 * G, 2, D, dtype, True, window)
+        p, clean = Prompts(*case), Prompts(*case)
+        for s in (p.ks, p.vs):
+            s[int(p.tables[0, at])] *= factor
+        got, want = p.run(), clean.run()
+        ok()
+        pos = torch.arange(500, device="cuda")
+        sees = pos >= 16 * at
+        if window:
+            sees &= pos - window + 1 < 16 * (at + 1)
+        sees = torch.cat([sees, torch.zeros(64, dtype=torch.bool, device="cuda")])
+        clean.check(torch.where(sees[:, None, None], want, got))
