@@ -27,8 +27,9 @@
 // rounds of two CTAs an SM.  The same by clusters takes 310 us.  To logits 79 us.  One
 // row of 32000 fp32 logits: 6 us.
 //
-// Counts are integers, and a token's biases are added in their order, so results
-// do not depend on the order of execution.
+// Counts are integers, a token's biases are added in their order, and what is summed by
+// slots of the hash table, whose tokens' places depend on who came first, is summed in whole
+// numbers, so results do not depend on the order of execution.
 #include <type_traits>
 
 #include <cuda_bf16.h>
@@ -373,6 +374,7 @@ stream_kernel(const LogitsArgs a, int log_slots) {
   __shared__ float bias_v[kLogitsMaxBias];
   __shared__ float red_m[kWarps], red_s[kWarps];
   __shared__ unsigned red_i[kWarps];
+  __shared__ unsigned long long red_u[kWarps];
   const pa_logits_spec& sp = a.spec;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = blockIdx.x / a.rows, i = blockIdx.x - b * a.rows;
@@ -481,7 +483,38 @@ stream_kernel(const LogitsArgs a, int log_slots) {
       unsigned* w = vals + j0 + u * kStreamThreads;
       const float x = ok[u] & 1u ? pen.adjust(to_f32(v[u]), *w, key[u], bias_t, bias_v, sp.num_bias) : -INFINITY;
       *w = __float_as_uint(x);
-      if (PROBS) take(x, key[u]);
+      if (PROBS && greedy) take(x, key[u]);
+      else if (PROBS) m = fmaxf(m, x);             // (passes NaN over)
+    }
+  }
+  if (PROBS && !greedy) {
+    // Their sum.  Which slot a token has, and so which thread, depends on who came first; whole
+    // numbers add up to the same in any order.  Relative to the largest of them, in units of
+    // 2^-40: each is off by half a unit, 6144 of them by 2^-28 of a sum that is 1 at least.
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) red_m[warp] = m;
+    __syncthreads();
+    m = red_m[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) m = fmaxf(m, red_m[w]);
+    unsigned long long units = 0u;
+    if (m > -INFINITY) {
+      for (int j = tid; j < slots; j += kStreamThreads) {   // (this thread's own, as above)
+        const float x = __uint_as_float(vals[j]);
+        if (keys[j] < 0 || !(x > -INFINITY)) continue;
+        units += __float2ull_rn((x == m ? 1.f : fast_exp2((x - m) * c)) * 0x1p40f);
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) units += __shfl_xor_sync(0xffffffffu, units, o);
+    if (lane == 0) red_u[warp] = units;
+    __syncthreads();
+    if (tid == 0) {
+      for (int w = 1; w < kWarps; ++w) units += red_u[w];
+      sum = __ull2float_rn(units) * 0x1p-40f;
+    } else {
+      m = -INFINITY;
     }
   }
   __syncthreads();                                 // (in place, the rest is written over them)
