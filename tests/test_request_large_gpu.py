@@ -1,11 +1,11 @@
-"""Page calls over pools that a cluster of CTAs ranks, and prompts of more sequences than one
-launch sorts whose items are cut."""
+"""Page calls over pools that a cluster of CTAs ranks and with more pairs than shared memory keeps
+the places of, and prompts of more sequences than one launch sorts whose items are cut."""
 import numpy as np
 import pytest
 import torch
 
 from paged_kv_cache_179_gb300 import _abi
-from test_request_gpu import BF16, F16, Prompts, State, gen, i32, ok, pools, scales
+from test_request_gpu import BF16, F16, Prompts, State, gen, i32, ok, pools, scales, status
 
 pytestmark = pytest.mark.gpu
 
@@ -43,6 +43,30 @@ def test_fork_in_large_pools(NB, Hkv, fp8):
     ok()
     assert granted.tolist() == s.host.fork(src, dst, lens, data)
     assert 17 < sum(granted.tolist()) < len(src)
+    assert L.tolist() == lens
+    s.same()
+    for a, b in zip(dev, data):
+        assert torch.equal(a.cpu(), b)
+
+
+def test_fork_of_many_pairs():
+    """More than shared memory keeps the places of; bad pairs among them."""
+    g = gen(31)
+    n, NB = 9000, 20011
+    s = State([2, 1, 3] + [0] * n, NB, 3)
+    lens = [20, 16, 48] + [0] * n
+    data = pools(g, NB, 1, 64, False)
+    dev = [x.cuda() for x in data]
+    src = [(0, 1, 0, 2)[i % 4] for i in range(n)]
+    dst = list(range(n + 2, 2, -1))
+    src[5], src[4001], dst[8500] = -1, n + 3, -7
+    take_all_but(s, free_of(s, 4300, g))
+    t, pages, ref = s.dev
+    L, granted = i32(lens), i32([9] * n)
+    _abi.pa_fork_pages(dev[0], dev[1], t, pages, L, i32(src), i32(dst), ref, granted)
+    status(_abi.PA_STATUS_BAD_ROW)
+    assert granted.tolist() == s.host.fork(src, dst, lens, data)
+    assert 8000 < sum(granted.tolist()) < n - 3
     assert L.tolist() == lens
     s.same()
     for a, b in zip(dev, data):
