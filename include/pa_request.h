@@ -39,8 +39,13 @@ extern "C" {
  * sequence (0: none; 1: a decode step):
  *   out[t][hq][:] = sum_j softmax_j(scale * q[t][hq] . K_j) * V_j
  * over positions j up to its own, within the last window_size of them when that is
- * not 0.  Rounded once, to dtype.  A query before position 0 gets zeros, as
- * does one that sees no page with a valid id, and so do the queries of a
+ * not 0.  Scores, sums and statistics are fp32; the weights enter the products with V
+ * in 16 bits, bf16 for bf16 pools (each off by 2^-8 of itself at most), else fp16
+ * (2^-11; weights, over E4M3 pools times V's scales, below 2^-20 of the largest lose
+ * bits, and below 2^-31 they count as 0);
+ * the result is rounded to dtype.  Weights are divided by their sum last: values of
+ * bf16 pools above 2^88 in magnitude may overflow.  A query before position 0 gets
+ * zeros, as does one that sees no page with a valid id, and so do the queries of a
  * sequence whose context_len is out of bounds (PA_STATUS_BAD_LEN).  Pages of a
  * sequence before the windows of all its queries are not looked at: their table
  * entries may be anything.  Tokens that belong to no sequence (before
@@ -73,7 +78,8 @@ int pa_prefill(void *out, const void *q, int64_t q_stride, const void *k_cache,
 /*
  * The same over E4M3 pools: K_j = e4m3(code) * k_scale[block][kv head], V_j
  * likewise (scales finite and not negative, as the appends and quantisers
- * make them).
+ * make them).  bf16 queries enter the products in fp16, each row scaled by a power of
+ * two: exactly, down to 2^-28 of the row's largest element.
  */
 int pa_prefill_fp8(void *out, const void *q, int64_t q_stride, const uint8_t *k_cache,
                    const uint8_t *v_cache, const float *k_scale, const float *v_scale,
@@ -131,7 +137,9 @@ int pa_free_pages(int32_t *block_tables, int max_blocks_per_seq, int32_t *num_pa
  * granted stays as it was.  context_lens int32 [num_rows]; one that is negative
  * or above what src holds passes the pair over (PA_STATUS_BAD_LEN), as does a
  * src that is its own dst (PA_STATUS_BAD_ROW).  An entry of src outside the pool
- * sets PA_STATUS_BAD_BLOCK, counts and copies nothing, and is taken over as it is.
+ * sets PA_STATUS_BAD_BLOCK, counts and copies nothing: that of a full page is taken
+ * over as it is; where it is the part-full last one, dst gets a page of its own whose
+ * contents stay as they were.
  * Destinations must be distinct and not the source of another pair; a source may
  * be forked many times.
  *   pool_type: PA_F16 / PA_BF16 (scales NULL) or PA_E4M3.

@@ -22,9 +22,9 @@
 //
 // Bound by memory where there are many rows, by latency where there are few.  Measured on a
 // GB300, rows of 128000 bf16 logits to fp32 probabilities, biases and a grammar's mask: 512
-// rows with histories of 4096 tokens 149 us, 2.7 TB/s of what is read and written once (a
+// rows with histories of 4096 tokens 147 us, 2.7 TB/s of what is read and written once (a
 // copy of those bytes would take 59 us): 35 us are the histories' insertion, the rest two
-// rounds of two CTAs an SM.  The same by clusters takes 310 us.  To logits 79 us.  One
+// rounds of two CTAs an SM.  The same by clusters takes 310 us.  To logits 77 us.  One
 // row of 32000 fp32 logits: 6 us.
 //
 // Counts are integers, a token's biases are added in their order, and what is summed by

@@ -36,7 +36,9 @@
 // subtiles' products in one queue unordered 1.95 (either in step, or one ahead until the
 // ring had no place for its keys), with one thread issuing both subtiles' 3.8.
 // Over E4M3 pools the codes' way through the converting warps is close behind: the next
-// 450 tokens of two prompts over 115k cached ones take 1.07 ms, 1.38 PFLOP/s, 73 %.
+// 450 tokens of two prompts over 115k cached ones take 1.13 ms when calls follow one another,
+// 1.31 PFLOP/s, 69 %.  With a window of 4096 that prompt takes 0.57 ms, 1.48 PFLOP/s (its
+// items are shorter), over an E4M3 pool 0.76.
 //
 // Page scales: K's multiply the scores of their 16 columns, V's the weights (relative
 // to a power of two that follows the largest that the row has seen, so that P stays in
@@ -880,8 +882,8 @@ prefill_kernel(const __grid_constant__ Args ka) {
         constexpr int kAll = kTile * kChunks, kEach = (kAll + C::kConvWarps * 32 - 1) / (C::kConvWarps * 32);
         // Into registers, all loads in flight at once; then their place is free for the next
         // copy.  (Released once they were written out, two places kept 32 KB in flight at
-        // most half of the time: 1.39 ms instead of 1.07 for two prompts' next 512 tokens over
-        // 100k cached ones.)
+        // most half of the time: 1.39 ms instead of 1.07, single calls, for two prompts' next
+        // 512 tokens over 100k cached ones.)
         uint4 all[kEach];
 #pragma unroll
         for (int n = 0; n < kEach; ++n) all[n] = lds128(src + 16 * min(ct + n * C::kConvWarps * 32, kAll - 1));
